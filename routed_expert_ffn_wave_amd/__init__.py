@@ -441,3 +441,8 @@ class MoELayer:
                                   _ptr(self.inv), _ptr(self.slot_of), T, E, k, self.bank.d, _ptr(self.out),
                                   _ptr(self.mask), self.out_flags, s))
         return self.out[:T], self.mask[:T]
+
+
+from .rows import (EXPORTED_ROWS, FT_ROWS_F32, Fp8MoELayer, ft_moe_combine_grad, ft_moe_dispatch, ft_moe_dispatch_fp8,  # noqa: E402,F401
+                   ft_moe_dispatch_grad, ft_moe_fp8_grouped_matmul, ft_moe_fp8_matmul, ft_moe_fp8_scale_cols,
+                   ft_moe_quant_fp8, ft_moe_swiglu_fp8)

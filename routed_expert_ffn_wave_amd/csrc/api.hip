@@ -4,8 +4,6 @@
 // host threads it starts and returns when done.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <climits>
 #include <cstring>
 #include <exception>
@@ -13,52 +11,12 @@
 #include <new>
 #include <thread>
 
-#include "../../include/ft_moe.h"
+#include "ft_api.h"
 #include "ft_kernels.h"
 
 namespace {
 
-thread_local char g_err[512] = {0};
-
-int fail(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-int ok() {
-  g_err[0] = 0;
-  return FT_OK;
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(FT_E_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-#define REQUIRE(cond, code, ...) \
-  do {                           \
-    if (!(cond)) return fail(code, __VA_ARGS__); \
-  } while (0)
-
-#define CHECK_PTR(p, name) \
-  do {                                                               \
-    if ((p) == nullptr) return fail(FT_E_INVAL, "%s is null", name); \
-    if (!aligned16(p)) return fail(FT_E_INVAL, "%s is not 16-byte aligned", name); \
-  } while (0)
-
-int check_tek(int T, int E, int k) {
-  REQUIRE(T >= 0, FT_E_INVAL, "T must be >= 0 (got %d)", T);
-  REQUIRE(E >= 1 && E <= 1024, FT_E_INVAL, "E must be in [1, 1024] (got %d)", E);
-  REQUIRE(k >= 1 && k <= E && k <= 32, FT_E_INVAL, "k must be in [1, min(E, 32)] (got k=%d, E=%d)", k, E);
-  REQUIRE((long long)T * k <= (1LL << 30), FT_E_INVAL, "T*k too large (%lld)", (long long)T * k);
-  return FT_OK;
-}
-
+using namespace ftk;  // the status helpers of ft_api.h
 
 int check_bank_shape(int fmt, int n_slots, int d, int I) {
   REQUIRE(fmt >= FT_W_BF16 && fmt <= FT_W_NVFP4, FT_E_UNSUPPORTED, "unknown weight format %d", fmt);

@@ -32,27 +32,18 @@ struct GroupList {
 __host__ __device__ inline size_t group_lds_bytes(int E) { return (((size_t)4 * (E + 2) + 4) * 4 + 15) & ~(size_t)15; }
 
 // Build the group list in LDS with wave 0 (ascending expert order, shared group last).
+// entry(e, slot, row0, cnt) gives expert e's slot (negative: none) and rows for e in [0, last);
 // items_of(cnt) gives the number of work items of a group with `cnt` rows.  Every thread of the
 // block must call this; it ends with a block barrier.
-template <class ItemsOf>
-__device__ __forceinline__ void build_groups(const GroupSrc& s, GroupList& g, int* tmp, ItemsOf items_of) {
+template <class EntryOf, class ItemsOf>
+__device__ __forceinline__ void build_group_list(int last, GroupList& g, int* tmp, EntryOf entry, ItemsOf items_of) {
   const int lane = threadIdx.x & 63;
   if (threadIdx.x < 64) {
     int n = 0;
-    const int last = s.E + (s.shared_slot >= 0 ? 1 : 0);
     for (int e0 = 0; e0 < last; e0 += 64) {
       const int e = e0 + lane;
       int slot = -1, row0 = 0, cnt = 0;
-      if (e < s.E) {
-        slot = s.slot_of[e];
-        row0 = s.offsets[e];
-        cnt = s.offsets[e + 1] - row0;
-      } else if (e == s.E && s.shared_slot >= 0) {
-        slot = s.shared_slot;
-        row0 = s.T * s.k;
-        cnt = s.T;
-      }
-      const bool keep = slot >= 0 && slot < s.n_slots && cnt > 0 && cnt >= s.min_cnt && cnt <= s.max_cnt;
+      const bool keep = entry(e, slot, row0, cnt);
       const uint64_t bal = __ballot(keep);
       if (keep) {
         const int at = n + __popcll(bal & ((lane == 0) ? 0ull : (~0ull >> (64 - lane))));
@@ -84,6 +75,42 @@ __device__ __forceinline__ void build_groups(const GroupSrc& s, GroupList& g, in
   }
   __syncthreads();
   g.n = tmp[0];
+}
+
+template <class ItemsOf>
+__device__ __forceinline__ void build_groups(const GroupSrc& s, GroupList& g, int* tmp, ItemsOf items_of) {
+  build_group_list(
+      s.E + (s.shared_slot >= 0 ? 1 : 0), g, tmp,
+      [&](int e, int& slot, int& row0, int& cnt) {
+        if (e < s.E) {
+          slot = s.slot_of[e];
+          row0 = s.offsets[e];
+          cnt = s.offsets[e + 1] - row0;
+        } else if (e == s.E && s.shared_slot >= 0) {
+          slot = s.shared_slot;
+          row0 = s.T * s.k;
+          cnt = s.T;
+        }
+        return slot >= 0 && slot < s.n_slots && cnt > 0 && cnt >= s.min_cnt && cnt <= s.max_cnt;
+      },
+      items_of);
+}
+
+// The same from offsets clipped to [0, P]: a group's rows lie inside the P rows whatever the table holds.
+template <class ItemsOf>
+__device__ __forceinline__ void build_clipped_groups(const int32_t* slot_of, const int32_t* offsets, int E, int P,
+                                                     int n_slots, GroupList& g, int* tmp, ItemsOf items_of) {
+  build_group_list(
+      E, g, tmp,
+      [&](int e, int& slot, int& row0, int& cnt) {
+        if (e < E) {
+          slot = slot_of[e];
+          row0 = min(max(offsets[e], 0), P);
+          cnt = min(max(offsets[e + 1], 0), P) - row0;
+        }
+        return slot >= 0 && slot < n_slots && cnt > 0;
+      },
+      items_of);
 }
 
 // Group holding work item `it` (item0 ascending): largest g with item0[g] <= it.
