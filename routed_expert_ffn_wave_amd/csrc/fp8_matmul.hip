@@ -6,6 +6,10 @@
 // K; its 8 waves take the 128-blocks in turn and their sums meet in LDS in a fixed order, so a single row
 // already keeps 8 waves a block busy with weight loads.  Codes are widened to bf16 (exact) and
 // multiplied on v_mfma_f32_16x16x32_bf16: products exact, fp32 sums.  Bound by the weights' bytes.
+#include <algorithm>
+#include <cmath>
+
+#include "fp8_tile.h"
 #include "ft_device.h"
 #include "ft_groups.h"
 #include "ft_kernels.h"
@@ -28,23 +32,24 @@ struct Tile {
   int slot, row0, rows, n0;
 };
 
-template <int MT, int NF, bool BF16>
+template <int MT, int NF, int PF, bool BF16>
 __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl, float* s_part) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int nb = (a.K + 127) / 128, nblk_n = (a.N + 127) / 128;
   // lane (r, g) holds row r and the 16-byte chunks g and g + 4 of a 128-block: any order of k that both
   // operands share is the same sum.  Rows past the end repeat the last one; their results are not stored.
-  const uint8_t* wp[NF];
-  const uint8_t* ap[MT];
-  const float* sp[MT];
+  const uint8_t* wb = a.w + ((size_t)tl.slot * a.N + tl.n0) * a.K;
+  const uint8_t* ab = a.a + (size_t)tl.row0 * a.K;
+  const float* sb = a.sa + (size_t)tl.row0 * a.S;
+  uint32_t wo[NF], ao[MT], so[MT];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) wp[f] = a.w + ((size_t)tl.slot * a.N + min(tl.n0 + 16 * f + r, a.N - 1)) * a.K;
+  for (int f = 0; f < NF; ++f) wo[f] = (uint32_t)min(16 * f + r, a.N - 1 - tl.n0) * (uint32_t)a.K + g * 16;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const size_t row = (size_t)tl.row0 + min(16 * m + r, tl.rows - 1);
-    ap[m] = a.a + row * a.K;
-    sp[m] = a.sa + row * a.S;
+    const uint32_t row = (uint32_t)min(16 * m + r, tl.rows - 1);
+    ao[m] = row * (uint32_t)a.K + g * 16;
+    so[m] = row * (uint32_t)a.S;
   }
   const float* swp = a.sw + ((size_t)tl.slot * nblk_n + tl.n0 / 128) * nb;  // 16 NF rows lie in one 128-block
   f32x4 acc[MT][NF];
@@ -52,21 +57,39 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
-  for (int b = wv; b < nb; b += RW) {
-    const float sw = swp[b];
-    u32x4 wc[NF][2], ac[MT][2];
-    float sa[MT];
+  // A block's operands in registers; PF blocks are in flight while the PF before them are multiplied.
+  struct Regs {
+    u32x4 w[NF][2], a[MT][2];
+    float sa[MT], sw;
+  };
+  const int zero = lane >> 6;  // a lane's index, so that the weight scale is a vector load among the others
+  auto load = [&](Regs& x, int b) {
+    const int bs = min(b, nb - 1);
+    if (b * 128 + 128 <= a.K) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = b * 128 + (g + 4 * h) * 16;
-      const bool in = c < a.K;  // chunks past K count as zero codes
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int f = 0; f < NF; ++f) wc[f][h] = in ? *(const u32x4*)(wp[f] + c) : u32x4{0, 0, 0, 0};
+        for (int f = 0; f < NF; ++f) x.w[f][h] = *(const u32x4*)(wb + (size_t)b * 128 + 64 * h + wo[f]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) ac[m][h] = in ? *(const u32x4*)(ap[m] + c) : u32x4{0, 0, 0, 0};
+        for (int m = 0; m < MT; ++m) x.a[m][h] = *(const u32x4*)(ab + (size_t)b * 128 + 64 * h + ao[m]);
+      }
+    } else {  // the short block, or none: chunks past K count as zero codes
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = b * 128 + (g + 4 * h) * 16 < a.K;
+        const size_t at = in ? (size_t)b * 128 + 64 * h : 0;
+        const u32x4 none = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int f = 0; f < NF; ++f) x.w[f][h] = in ? *(const u32x4*)(wb + at + wo[f]) : none;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) x.a[m][h] = in ? *(const u32x4*)(ab + at + ao[m]) : none;
+      }
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m) sa[m] = sp[m][b];
+    for (int m = 0; m < MT; ++m) x.sa[m] = sb[so[m] + bs];
+    x.sw = swp[bs + zero];
+  };
+  auto multiply = [&](const Regs& x) {
     f32x4 part[MT][NF];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -74,17 +97,17 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
       for (int f = 0; f < NF; ++f) part[m][f] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      bf16x8 wb[NF][2], ab[2];
+      bf16x8 wf[NF][2], af[2];
 #pragma unroll
-      for (int f = 0; f < NF; ++f) widen(wc[f][h], wb[f]);
+      for (int f = 0; f < NF; ++f) widen(x.w[f][h], wf[f]);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        widen(ac[m][h], ab);
+        widen(x.a[m][h], af);
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
           for (int q = 0; q < 2; ++q)
-            part[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[f][q], ab[q], part[m][f], 0, 0, 0);
+            part[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[f][q], af[q], part[m][f], 0, 0, 0);
       }
     }
 #pragma unroll
@@ -92,7 +115,21 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
 #pragma unroll
       for (int f = 0; f < NF; ++f)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][f][i] = fmaf(part[m][f][i], sa[m] * sw, acc[m][f][i]);
+        for (int i = 0; i < 4; ++i) acc[m][f][i] = fmaf(part[m][f][i], x.sa[m] * x.sw, acc[m][f][i]);
+  };
+  Regs cur[PF], nxt[PF];
+#pragma unroll
+  for (int i = 0; i < PF; ++i) load(cur[i], wv + i * RW);
+  for (int b = wv; b < nb; b += 2 * PF * RW) {
+#pragma unroll
+    for (int i = 0; i < PF; ++i) load(nxt[i], b + (PF + i) * RW);
+#pragma unroll
+    for (int i = 0; i < PF; ++i) multiply(cur[i]);
+    if (b + PF * RW >= nb) break;
+#pragma unroll
+    for (int i = 0; i < PF; ++i) load(cur[i], b + (2 * PF + i) * RW);
+#pragma unroll
+    for (int i = 0; i < PF; ++i) multiply(nxt[i]);
   }
   // lane (r, g) of a fragment holds row (activation) r and columns 4 g .. 4 g + 3 of the 16 weight rows
   constexpr int NV = MT * NF * 256;
@@ -118,13 +155,13 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
   __syncthreads();
 }
 
-template <int MT, int NF, bool BF16, bool GROUPED>
+template <int MT, int NF, int PF, bool BF16, bool GROUPED>
 __global__ __launch_bounds__(64 * RW) void fp8_rows_kernel(Fp8MatmulArgs a) {
   __shared__ __attribute__((aligned(16))) float s_part[RW * MT * NF * 256];
   const int ntn = (a.N + 16 * NF - 1) / (16 * NF);
   if constexpr (!GROUPED) {
     const int mt = blockIdx.x / ntn, nt = blockIdx.x % ntn;
-    rows_tile<MT, NF, BF16>(a, Tile{0, mt * 16 * MT, min(16 * MT, a.M - mt * 16 * MT), nt * 16 * NF}, s_part);
+    rows_tile<MT, NF, PF, BF16>(a, Tile{0, mt * 16 * MT, min(16 * MT, a.M - mt * 16 * MT), nt * 16 * NF}, s_part);
   } else {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int E2 = a.E + 2;
@@ -136,35 +173,157 @@ __global__ __launch_bounds__(64 * RW) void fp8_rows_kernel(Fp8MatmulArgs a) {
       const int gi = find_group(gl.item0, gl.n, it);
       const int local = it - gl.item0[gi], mt = local / ntn, nt = local % ntn;
       const int m0 = mt * 16 * MT;
-      rows_tile<MT, NF, BF16>(a, Tile{gl.slot[gi], gl.row0[gi] + m0, min(16 * MT, gl.cnt[gi] - m0), nt * 16 * NF},
+      rows_tile<MT, NF, PF, BF16>(a, Tile{gl.slot[gi], gl.row0[gi] + m0, min(16 * MT, gl.cnt[gi] - m0), nt * 16 * NF},
                               s_part);
     }
   }
 }
 
-template <int MT, int NF, bool BF16>
+template <int MT, int NF, int PF, bool BF16>
 hipError_t launch_rows(const Fp8MatmulArgs& a, hipStream_t s) {
   const long long ntn = (a.N + 16 * NF - 1) / (16 * NF), ntm = (a.M + 16 * MT - 1) / (16 * MT);
   if (a.E == 0) {
-    hipLaunchKernelGGL((fp8_rows_kernel<MT, NF, BF16, false>), dim3((uint32_t)(ntn * ntm)), dim3(64 * RW), 0, s, a);
+    hipLaunchKernelGGL((fp8_rows_kernel<MT, NF, PF, BF16, false>), dim3((uint32_t)(ntn * ntm)), dim3(64 * RW), 0, s, a);
     return hipGetLastError();
   }
   static LaunchCache cache;
   LaunchFacts f;
   const size_t lds = group_lds_bytes(a.E);
-  hipError_t e = cache.get((const void*)fp8_rows_kernel<MT, NF, BF16, true>, 64 * RW, lds, &f);
+  hipError_t e = cache.get((const void*)fp8_rows_kernel<MT, NF, PF, BF16, true>, 64 * RW, lds, &f);
   if (e != hipSuccess) return e;
   const long long upper = (ntm + (a.E < a.M ? a.E : a.M)) * ntn, most = (long long)f.per_cu * f.cus;
-  hipLaunchKernelGGL((fp8_rows_kernel<MT, NF, BF16, true>), dim3((uint32_t)(upper < most ? upper : most)), dim3(64 * RW),
+  hipLaunchKernelGGL((fp8_rows_kernel<MT, NF, PF, BF16, true>), dim3((uint32_t)(upper < most ? upper : most)), dim3(64 * RW),
                      lds, s, a);
   return hipGetLastError();
+}
+
+// Many rows: tiles of fp8_tile.h.  Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run
+// of the tile list, so that tiles that run together share rows and weights through its L2.
+template <class C, bool BF16, bool GROUPED>
+__global__ __launch_bounds__(C::NT, 2) void fp8_tile_kernel(Fp8MatmulArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int ntn = (a.N + C::BN - 1) / C::BN;
+  const int per = gridDim.x / 8, lb = (blockIdx.x % 8) * per + blockIdx.x / 8;  // gridDim.x % 8 == 0
+  if constexpr (!GROUPED) {
+    const int ntm = (a.M + C::BM - 1) / C::BM;
+    if (lb >= ntm * ntn) return;
+    // bands of 4 row tiles, weight tiles within a band in turn
+    constexpr int BAND = 4;
+    const int band = lb / (BAND * ntn), h = min(BAND, ntm - band * BAND), in = lb - band * BAND * ntn;
+    const int mt = band * BAND + in % h, nt = in / h;
+    fp8_tile<C, BF16>(a, TileJob{0, mt * C::BM, min(C::BM, a.M - mt * C::BM), nt * C::BN}, lds);
+  } else {
+    const int E2 = a.E + 2;
+    int* li = (int*)(lds + C::LDS);
+    GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
+    build_clipped_groups(a.slot_of, a.offsets, a.E, a.M, a.n_slots, gl, li + 4 * E2,
+                         [&](int cnt) { return (cnt + C::BM - 1) / C::BM * ntn; });
+    const int nitems = gl.item0[gl.n];
+    for (int it = lb; it < nitems; it += gridDim.x) {
+      const int gi = find_group(gl.item0, gl.n, it);
+      const int local = __builtin_amdgcn_readfirstlane(it - gl.item0[gi]);
+      const int slot = __builtin_amdgcn_readfirstlane(gl.slot[gi]);
+      const int row0 = __builtin_amdgcn_readfirstlane(gl.row0[gi]), cnt = __builtin_amdgcn_readfirstlane(gl.cnt[gi]);
+      const int m0 = local / ntn * C::BM, nt = local % ntn;
+      fp8_tile<C, BF16>(a, TileJob{slot, row0 + m0, min(C::BM, cnt - m0), nt * C::BN}, lds);
+    }
+  }
+}
+
+template <class C, bool BF16>
+hipError_t launch_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
+  static LaunchCache cache;
+  LaunchFacts f;
+  const long long ntn = (a.N + C::BN - 1) / C::BN, ntm = (a.M + C::BM - 1) / C::BM;
+  if (a.E == 0) {
+    hipError_t e = cache.get((const void*)fp8_tile_kernel<C, BF16, false>, C::NT, C::LDS, &f);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((fp8_tile_kernel<C, BF16, false>), dim3((uint32_t)((ntn * ntm + 7) / 8 * 8)), dim3(C::NT), C::LDS, s, a);
+    return hipGetLastError();
+  }
+  static LaunchCache gcache;
+  const size_t lds = C::LDS + group_lds_bytes(a.E);
+  hipError_t e = gcache.get((const void*)fp8_tile_kernel<C, BF16, true>, C::NT, lds, &f);
+  if (e != hipSuccess) return e;
+  const long long upper = ((ntm + (a.E < a.M ? a.E : a.M)) * ntn + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
+  hipLaunchKernelGGL((fp8_tile_kernel<C, BF16, true>), dim3((uint32_t)(upper < most ? upper : most)), dim3(C::NT), lds, s, a);
+  return hipGetLastError();
+}
+
+// Which kernel: the one whose blocks, taken in rounds of the 256 compute units (or as many times that as fit),
+// are through first.  `step` is the measured time of one 128-block of K in a round, in us on an MI355X; `full`
+// where a compute unit holds `per` of the blocks.  M rows x 4096 columns, K = 7168, us a call:
+//   M        16     32     64     128    512    8192
+//   16x16    10.1   -      -      -      -      -
+//   16x32    14.0   14.9   27.8   54.3   -      -
+//   32x32    -      18.0   18.3   34.3   -      -
+//   64x32    -      20.5   27.1   27.6   -      -
+//   64x128   -      48.9   48.9   40.0   40.7   384
+//   128x128  -      50.9   51.0   42.8   43.6   368
+//   128x256  -      47.0   47.7   49.2   50.4   263 - 311
+//   256x256  -      -      -      71.3   74.1   240 - 249
+struct Choice {
+  int rows, cols, per;
+  float step, full;
+  int lds;  // of the tiles kernels, 0 for the others
+};
+using T64 = TileCfg<64, 128, 1, 2, 3, false>;
+using T128 = TileCfg<128, 128, 2, 2, 4, false>;
+using T128x256 = TileCfg<128, 256, 2, 4, 3, false>;
+using T256 = TileCfg<256, 256, 2, 4, 2, false>;
+using TWide = TileCfg<128, 128, 2, 2, 2, true>;
+constexpr int kLds = 160 * 1024;  // of a compute unit
+constexpr Choice kChoices[] = {
+    {16, 16, 1, 0.18f, 0.18f, 0},  {16, 32, 1, 0.26f, 0.26f, 0},  {32, 32, 1, 0.32f, 0.32f, 0},
+     {64, 32, 1, 0.48f, 0.48f, 0},  {64, 128, 2, 0.71f, 0.86f, T64::LDS},
+    {128, 128, 1, 0.78f, 0.82f, T128::LDS}, {128, 256, 1, 0.88f, 1.25f, T128x256::LDS}, {256, 256, 1, 1.3f, 2.2f, T256::LDS}};
+constexpr Choice kWide = {128, 128, 2, 1.4f, 2.2f, TWide::LDS};  // fp32 results on the bf16 instructions
+
+// Rows with a slot and groups that have any, where only the device knows: as if experts were drawn evenly.
+struct Spread {
+  double rows, groups;
+};
+Spread spread(const Fp8MatmulArgs& a) {
+  const double held = std::min(1.0, (double)a.n_slots / a.E);
+  return {std::max(1.0, held * a.M), std::max(1.0, held * a.E * (1.0 - std::exp(-(double)a.M / a.E)))};
+}
+
+double cost(const Choice& c, const Fp8MatmulArgs& a) {
+  if (c.lds + (a.E > 0 ? group_lds_bytes(a.E) : 0) > kLds) return 1e30;
+  double chunks = (a.M + c.rows - 1) / c.rows;
+  if (a.E > 0) {  // each group has half a chunk to spare
+    const Spread p = spread(a);
+    chunks = std::max(p.groups, p.rows / c.rows + 0.5 * p.groups);
+  }
+  const double blocks = chunks * ((a.N + c.cols - 1) / c.cols);
+  return blocks <= 256 ? c.step : std::ceil(blocks / (256.0 * c.per)) * c.full;
 }
 
 }  // namespace
 
 hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
-  if (a.out_bf16) return launch_rows<4, 1, true>(a, s);
-  return launch_rows<4, 1, false>(a, s);
+  int best = 0;
+  constexpr int n = sizeof(kChoices) / sizeof(kChoices[0]);
+  for (int i = 1; i < n; ++i)
+    if ((a.out_bf16 || !kChoices[i].lds) && cost(kChoices[i], a) < cost(kChoices[best], a)) best = i;
+  // A few rows a group: bound by the weights' bytes, and with long rows 16 x 32 blocks stream them fastest (top 8 of
+  // 256 experts, 96 resident, K = 7168, 16 / 32 tokens: 183 - 198 / 281 us, 5.9 TB/s; 64 x 128 tiles 207 / 293;
+  // with K = 2048 and 4 / 16 tokens 21 / 52 us against 20 / 44)
+  if (a.E > 0 && a.K >= 4096 && spread(a).rows <= 3 * spread(a).groups)
+    best = 1;
+  else if (!a.out_bf16 && cost(kWide, a) < cost(kChoices[best], a)) return launch_tiles<TWide, false>(a, s);
+#define ROWS(MT, NF) return a.out_bf16 ? launch_rows<MT, NF, 1, true>(a, s) : launch_rows<MT, NF, 1, false>(a, s)
+  switch (best) {
+    case 0: ROWS(1, 1);
+    case 1: ROWS(1, 2);
+    case 2: ROWS(2, 2);
+    case 3: ROWS(4, 2);
+    case 4: return launch_tiles<T64, true>(a, s);
+    case 5: return launch_tiles<T128, true>(a, s);
+    case 6: return launch_tiles<T128x256, true>(a, s);
+    default: return launch_tiles<T256, true>(a, s);
+  }
+#undef ROWS
 }
 
 }  // namespace ftk

@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import FT_E_INVAL, FT_OUT_BF16, FtError, _check, _ptr, lib
+from . import FT_E_INVAL, FT_OUT_BF16, FtError, _check, lib
 
 FT_ROWS_F32 = 0x20
 
@@ -33,71 +33,84 @@ for _name, _args in _SIG.items():
 
 EXPORTED_ROWS = tuple(_SIG)
 
-_CODES = (torch.float8_e4m3fn, torch.uint8)
-_FLOATS = (torch.bfloat16, torch.float32)
+_E4, _U8, _BF, _F32, _I32 = torch.float8_e4m3fn, torch.uint8, torch.bfloat16, torch.float32, torch.int32
+_CODES = (_E4, _U8)
+_FLOATS = (_BF, _F32)
+
+# Calls of a few microseconds: the stream handle and the current device are asked for without building objects.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _refuse(text: str):
     raise FtError(FT_E_INVAL, text)
 
 
-class _Call:
-    """The tensors of one call: each checked for type, shape and layout, all on one GPU."""
-
-    def __init__(self, first: torch.Tensor, name: str):
-        if not isinstance(first, torch.Tensor):
-            _refuse(f"{name} must be a tensor")
-        self.device = first.device
-        if self.device.type != "cuda":
-            _refuse(f"{name} must be on a GPU (it is on {self.device})")
-
-    def take(self, t, name, dtypes, shape, optional=False):
-        """Checks one tensor; `shape` holds sizes, None where any will do."""
-        if t is None and optional:
-            return None
-        if not isinstance(t, torch.Tensor):
-            _refuse(f"{name} must be a tensor")
-        dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
-        if t.dtype not in dtypes:
-            _refuse(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
-        if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-            want = ", ".join("any" if s is None else str(s) for s in shape)
-            _refuse(f"{name} must have shape [{want}] (got {list(t.shape)})")
-        if t.device != self.device:
-            _refuse(f"{name} is on {t.device}, not on {self.device}")
-        if not t.is_contiguous():
-            _refuse(f"{name} must be contiguous")
-        return t
-
-    def out(self, t, name, dtypes, shape):
-        """An output: the caller's tensor, or a new one of the first type."""
-        first = dtypes[0] if isinstance(dtypes, tuple) else dtypes
-        return torch.empty(shape, dtype=first, device=self.device) if t is None else self.take(t, name, dtypes, shape)
-
-    def run(self, fn, *args, stream=None):
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        with torch.cuda.device(self.device):
-            _check(fn(*args, ctypes.c_void_p(s.cuda_stream)))
-
-    def pairs(self, ids, inv, slot_of_expert, E, T=None):
-        """The pair tables; returns (T, E, k)."""
-        self.take(ids, "ids", torch.int32, (T, None))
-        T, k = ids.shape
-        if not isinstance(inv, torch.Tensor) or inv.numel() != T * k:
-            _refuse(f"inv must hold T*k = {T * k} entries")
-        self.take(inv, "inv", torch.int32, (T, k) if inv.dim() == 2 else (T * k,))
-        if slot_of_expert is not None:
-            self.take(slot_of_expert, "slot_of_expert", torch.int32, (None,))
-            if E is not None and E != slot_of_expert.shape[0]:
-                _refuse(f"E = {E} does not match slot_of_expert ({slot_of_expert.shape[0]} experts)")
-            E = slot_of_expert.shape[0]
-        if E is None:
-            _refuse("E is needed when slot_of_expert is not given")
-        return T, E, k
+def _first(t, name: str, dims: int, dtypes) -> int:
+    """Checks a call's first tensor, whose sizes the others follow; returns its GPU."""
+    if not isinstance(t, torch.Tensor):
+        _refuse(f"{name} must be a tensor")
+    if not t.is_cuda:
+        _refuse(f"{name} must be on a GPU (it is on {t.device})")
+    if t.dim() != dims or t.dtype not in dtypes or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous tensor of {dims} dimensions and type "
+                f"{' or '.join(str(d) for d in dtypes)} (got {t.dtype}, {list(t.shape)}, strides {t.stride()})")
+    return t.get_device()
 
 
-def _f32(t: torch.Tensor) -> int:
-    return FT_ROWS_F32 if t.dtype == torch.float32 else 0
+def _take(t, name: str, dtypes, shape, dev: int):
+    """Checks one more tensor; returns its address."""
+    if not isinstance(t, torch.Tensor):
+        _refuse(f"{name} must be a tensor")
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype not in dtypes:
+        _refuse(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
+    if t.shape != shape:
+        _refuse(f"{name} must have shape {list(shape)} (got {list(t.shape)})")
+    if t.get_device() != dev:
+        _refuse(f"{name} is on {t.device}, not on cuda:{dev}")
+    _refuse(f"{name} must be contiguous")
+
+
+def _run(fn, dev: int, stream, *args):
+    """Enqueues on `stream`, or on the current stream of GPU `dev`, with that GPU as the current one."""
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if _current_device() == dev:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc:
+        _check(rc)
+
+
+def _new(shape, dtype, dev: int):
+    return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+
+
+def _pairs(ids, inv, slot_of_expert, E, T, dev: int):
+    """The pair tables: (their addresses, E, k); T None: as many tokens as ids has rows."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or (T is not None and ids.shape[0] != T):
+        _refuse(f"ids must be a tensor of shape [{'T' if T is None else T}, k]")
+    T, k = ids.shape
+    pi = _take(ids, "ids", (_I32,), (T, k), dev)
+    flat = isinstance(inv, torch.Tensor) and inv.dim() == 1
+    pv = _take(inv, "inv", (_I32,), (T * k,) if flat else (T, k), dev)
+    ps = None
+    if slot_of_expert is not None:
+        n = slot_of_expert.shape[0] if isinstance(slot_of_expert, torch.Tensor) and slot_of_expert.dim() == 1 else -1
+        ps = _take(slot_of_expert, "slot_of_expert", (_I32,), (n,), dev)
+        if E is not None and E != n:
+            _refuse(f"E = {E} does not match slot_of_expert ({n} experts)")
+        E = n
+    elif E is None:
+        _refuse("E is needed when slot_of_expert is not given")
+    return pi, pv, ps, T, E, k
+
+
+def _cols(K: int) -> int:
+    return (K + 511) // 512 * 4
 
 
 def ft_moe_fp8_scale_cols(K: int) -> int:
@@ -105,64 +118,68 @@ def ft_moe_fp8_scale_cols(K: int) -> int:
     return lib.ft_moe_fp8_scale_cols(K)
 
 
+def _rows_out(codes, scales, rows: int, K: int, dev: int):
+    if codes is None:
+        codes = _new((rows, K), _E4, dev)
+    if scales is None:
+        scales = _new((rows, _cols(K)), _F32, dev)
+    return codes, scales, _take(codes, "codes", _CODES, (rows, K), dev), _take(scales, "scales", (_F32,), (rows, _cols(K)), dev)
+
+
 def ft_moe_quant_fp8(x, codes=None, scales=None, stream=None):
     """bf16 or fp32 rows [rows][K] -> (codes [rows][K], scales fp32 [rows][S]): per block of 128 the scale is the
     largest magnitude / 448 and the codes are the nearest e4m3 values of x / scale."""
-    c = _Call(x, "x")
-    c.take(x, "x", _FLOATS, (None, None))
+    dev = _first(x, "x", 2, _FLOATS)
     rows, K = x.shape
-    codes = c.out(codes, "codes", _CODES, (rows, K))
-    scales = c.out(scales, "scales", torch.float32, (rows, ft_moe_fp8_scale_cols(K)))
-    c.run(lib.ft_moe_quant_fp8, _ptr(x), rows, K, _ptr(codes), _ptr(scales), _f32(x), stream=stream)
+    codes, scales, pc, ps = _rows_out(codes, scales, rows, K, dev)
+    _run(lib.ft_moe_quant_fp8, dev, stream, x.data_ptr(), rows, K, pc, ps, FT_ROWS_F32 if x.dtype is _F32 else 0)
     return codes, scales
 
 
 def ft_moe_swiglu_fp8(gu, codes=None, scales=None, stream=None):
     """bf16 rows [rows][2 I] = [gate | up] -> the 8-bit rows (codes [rows][I], scales) of SiLU(gate) * up."""
-    c = _Call(gu, "gu")
-    c.take(gu, "gu", torch.bfloat16, (None, None))
+    dev = _first(gu, "gu", 2, (_BF,))
     rows, I2 = gu.shape
     if I2 % 2:
         _refuse(f"gu must have gate and up columns (got {I2})")
-    codes = c.out(codes, "codes", _CODES, (rows, I2 // 2))
-    scales = c.out(scales, "scales", torch.float32, (rows, ft_moe_fp8_scale_cols(I2 // 2)))
-    c.run(lib.ft_moe_swiglu_fp8, _ptr(gu), rows, I2 // 2, _ptr(codes), _ptr(scales), stream=stream)
+    codes, scales, pc, ps = _rows_out(codes, scales, rows, I2 // 2, dev)
+    _run(lib.ft_moe_swiglu_fp8, dev, stream, gu.data_ptr(), rows, I2 // 2, pc, ps)
     return codes, scales
 
 
 def ft_moe_dispatch(x, ids, inv, E=None, slot_of_expert=None, x_sorted=None, stream=None):
     """Token rows [T][d] (bf16 or fp32) to their places in expert order [T*k][d]."""
-    c = _Call(x, "x")
-    c.take(x, "x", _FLOATS, (None, None))
-    T, E, k = c.pairs(ids, inv, slot_of_expert, E, x.shape[0])
-    x_sorted = c.out(x_sorted, "x_sorted", x.dtype, (T * k, x.shape[1]))
-    c.run(lib.ft_moe_dispatch, _ptr(x), _ptr(ids), _ptr(inv), _ptr(slot_of_expert), T, E, k, x.shape[1], _ptr(x_sorted),
-          _f32(x), stream=stream)
+    dev = _first(x, "x", 2, _FLOATS)
+    T, d = x.shape
+    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
+    if x_sorted is None:
+        x_sorted = _new((T * k, d), x.dtype, dev)
+    out = _take(x_sorted, "x_sorted", (x.dtype,), (T * k, d), dev)
+    _run(lib.ft_moe_dispatch, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if x.dtype is _F32 else 0)
     return x_sorted
 
 
 def ft_moe_dispatch_fp8(x, ids, inv, E=None, slot_of_expert=None, codes=None, scales=None, stream=None):
     """Token rows [T][d] (bf16 or fp32) to 8-bit rows in expert order: (codes [T*k][d], scales [T*k][S])."""
-    c = _Call(x, "x")
-    c.take(x, "x", _FLOATS, (None, None))
-    T, E, k = c.pairs(ids, inv, slot_of_expert, E, x.shape[0])
-    d = x.shape[1]
-    codes = c.out(codes, "codes", _CODES, (T * k, d))
-    scales = c.out(scales, "scales", torch.float32, (T * k, ft_moe_fp8_scale_cols(d)))
-    c.run(lib.ft_moe_dispatch_fp8, _ptr(x), _ptr(ids), _ptr(inv), _ptr(slot_of_expert), T, E, k, d, _ptr(codes),
-          _ptr(scales), _f32(x), stream=stream)
+    dev = _first(x, "x", 2, _FLOATS)
+    T, d = x.shape
+    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
+    codes, scales, pc, ps = _rows_out(codes, scales, T * k, d, dev)
+    _run(lib.ft_moe_dispatch_fp8, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, pc, ps,
+         FT_ROWS_F32 if x.dtype is _F32 else 0)
     return codes, scales
 
 
 def ft_moe_dispatch_grad(dx_sorted, ids, inv, E=None, slot_of_expert=None, dx=None, stream=None):
     """Gradient of ft_moe_dispatch: the sum [T][d] of every token's rows of dx_sorted [T*k][d]."""
-    c = _Call(dx_sorted, "dx_sorted")
-    T, E, k = c.pairs(ids, inv, slot_of_expert, E)
-    c.take(dx_sorted, "dx_sorted", _FLOATS, (T * k, None))
+    dev = _first(dx_sorted, "dx_sorted", 2, _FLOATS)
+    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, None, dev)
     d = dx_sorted.shape[1]
-    dx = c.out(dx, "dx", dx_sorted.dtype, (T, d))
-    c.run(lib.ft_moe_dispatch_grad, _ptr(dx_sorted), _ptr(ids), _ptr(inv), _ptr(slot_of_expert), T, E, k, d, _ptr(dx),
-          _f32(dx_sorted), stream=stream)
+    src = _take(dx_sorted, "dx_sorted", _FLOATS, (T * k, d), dev)
+    if dx is None:
+        dx = _new((T, d), dx_sorted.dtype, dev)
+    out = _take(dx, "dx", (dx_sorted.dtype,), (T, d), dev)
+    _run(lib.ft_moe_dispatch_grad, dev, stream, src, pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if dx_sorted.dtype is _F32 else 0)
     return dx
 
 
@@ -170,42 +187,45 @@ def ft_moe_combine_grad(dout, y_sorted, ids, w, inv, E=None, slot_of_expert=None
                         want_dlogits: bool = True, stream=None):
     """Gradient of ft_moe_combine for dout [T][d] (fp32 or bf16): (dy_sorted bf16 [T*k][d], dw fp32 [T][k],
     dlogits fp32 [T][E] through the renormalised softmax of the chosen logits, or None)."""
-    c = _Call(dout, "dout")
-    c.take(dout, "dout", _FLOATS, (None, None))
-    T, E, k = c.pairs(ids, inv, slot_of_expert, E, dout.shape[0])
-    d = dout.shape[1]
-    c.take(y_sorted, "y_sorted", torch.bfloat16, (T * k, d))
-    c.take(w, "w", torch.float32, (T, k))
-    dy_sorted = c.out(dy_sorted, "dy_sorted", torch.bfloat16, (T * k, d))
-    dw = c.out(dw, "dw", torch.float32, (T, k))
-    dlogits = c.out(dlogits, "dlogits", torch.float32, (T, E)) if want_dlogits or dlogits is not None else None
-    c.run(lib.ft_moe_combine_grad, _ptr(dout), _ptr(y_sorted), _ptr(ids), _ptr(w), _ptr(inv), _ptr(slot_of_expert), T, E,
-          k, d, _ptr(dy_sorted), _ptr(dw), _ptr(dlogits), FT_OUT_BF16 if dout.dtype == torch.bfloat16 else 0,
-          stream=stream)
+    dev = _first(dout, "dout", 2, _FLOATS)
+    T, d = dout.shape
+    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
+    py = _take(y_sorted, "y_sorted", (_BF,), (T * k, d), dev)
+    pw = _take(w, "w", (_F32,), (T, k), dev)
+    if dy_sorted is None:
+        dy_sorted = _new((T * k, d), _BF, dev)
+    if dw is None:
+        dw = _new((T, k), _F32, dev)
+    if dlogits is None and want_dlogits:
+        dlogits = _new((T, E), _F32, dev)
+    pl = None if dlogits is None else _take(dlogits, "dlogits", (_F32,), (T, E), dev)
+    _run(lib.ft_moe_combine_grad, dev, stream, dout.data_ptr(), py, pi, pw, pv, pt, T, E, k, d,
+         _take(dy_sorted, "dy_sorted", (_BF,), (T * k, d), dev), _take(dw, "dw", (_F32,), (T, k), dev), pl,
+         FT_OUT_BF16 if dout.dtype is _BF else 0)
     return dy_sorted, dw, dlogits
 
 
-def _matmul_out(c, out, out_dtype, shape):
+def _product_out(out, out_dtype, shape, dev: int):
     if out is None:
         if out_dtype not in _FLOATS:
             _refuse(f"out_dtype must be torch.bfloat16 or torch.float32 (got {out_dtype})")
-        return torch.empty(shape, dtype=out_dtype, device=c.device)
-    return c.take(out, "out", _FLOATS, shape)
+        out = _new(shape, out_dtype, dev)
+    return out, _take(out, "out", _FLOATS, shape, dev), FT_OUT_BF16 if out.dtype is _BF else 0
 
 
 def ft_moe_fp8_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """8-bit rows a [M][K] (scales [M][S]) times w [N][K] transposed (fp32 scales [ceil(N/128)][ceil(K/128)]):
     [M][N] in bf16, or in fp32 with out_dtype=torch.float32 (or an fp32 `out`)."""
-    c = _Call(a, "a")
-    c.take(a, "a", _CODES, (None, None))
+    dev = _first(a, "a", 2, _CODES)
     M, K = a.shape
-    c.take(a_scales, "a_scales", torch.float32, (M, ft_moe_fp8_scale_cols(K)))
-    c.take(w, "w", _CODES, (None, K))
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        _refuse("w must be a tensor of shape [N, K]")
     N = w.shape[0]
-    c.take(w_scales, "w_scales", torch.float32, ((N + 127) // 128, (K + 127) // 128))
-    out = _matmul_out(c, out, out_dtype, (M, N))
-    c.run(lib.ft_moe_fp8_matmul, _ptr(a), _ptr(a_scales), M, _ptr(w), _ptr(w_scales), N, K, _ptr(out),
-          FT_OUT_BF16 if out.dtype == torch.bfloat16 else 0, stream=stream)
+    psa = _take(a_scales, "a_scales", (_F32,), (M, _cols(K)), dev)
+    pw = _take(w, "w", _CODES, (N, K), dev)
+    psw = _take(w_scales, "w_scales", (_F32,), ((N + 127) // 128, (K + 127) // 128), dev)
+    out, po, flags = _product_out(out, out_dtype, (M, N), dev)
+    _run(lib.ft_moe_fp8_matmul, dev, stream, a.data_ptr(), psa, M, pw, psw, N, K, po, flags)
     return out
 
 
@@ -214,20 +234,19 @@ def ft_moe_fp8_grouped_matmul(a, a_scales, w, w_scales, offsets, slot_of_expert,
     """8-bit rows a [P][K] in expert order, each expert's rows times its matrix of w [n_slots][N][K] transposed
     (fp32 scales [n_slots][ceil(N/128)][ceil(K/128)]): [P][N] in bf16 or fp32.  Rows of experts without a slot
     are left as they were (with out=None: unset)."""
-    c = _Call(a, "a")
-    c.take(a, "a", _CODES, (None, None))
+    dev = _first(a, "a", 2, _CODES)
     P, K = a.shape
-    c.take(a_scales, "a_scales", torch.float32, (P, ft_moe_fp8_scale_cols(K)))
-    c.take(w, "w", _CODES, (None, None, K))
-    n_slots, N = w.shape[:2]
-    c.take(w_scales, "w_scales", torch.float32, (n_slots, (N + 127) // 128, (K + 127) // 128))
-    c.take(slot_of_expert, "slot_of_expert", torch.int32, (None,))
-    E = slot_of_expert.shape[0]
-    c.take(offsets, "offsets", torch.int32, (E + 1,))
-    out = _matmul_out(c, out, out_dtype, (P, N))
-    c.run(lib.ft_moe_fp8_grouped_matmul, _ptr(a), _ptr(a_scales), P, _ptr(w), _ptr(w_scales), n_slots, N, K,
-          _ptr(offsets), _ptr(slot_of_expert), E, _ptr(out), FT_OUT_BF16 if out.dtype == torch.bfloat16 else 0,
-          stream=stream)
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        _refuse("w must be a tensor of shape [n_slots, N, K]")
+    n_slots, N, _ = w.shape
+    psa = _take(a_scales, "a_scales", (_F32,), (P, _cols(K)), dev)
+    pw = _take(w, "w", _CODES, (n_slots, N, K), dev)
+    psw = _take(w_scales, "w_scales", (_F32,), (n_slots, (N + 127) // 128, (K + 127) // 128), dev)
+    E = slot_of_expert.shape[0] if isinstance(slot_of_expert, torch.Tensor) and slot_of_expert.dim() == 1 else 0
+    pt = _take(slot_of_expert, "slot_of_expert", (_I32,), (E,), dev)
+    pf = _take(offsets, "offsets", (_I32,), (E + 1,), dev)
+    out, po, flags = _product_out(out, out_dtype, (P, N), dev)
+    _run(lib.ft_moe_fp8_grouped_matmul, dev, stream, a.data_ptr(), psa, P, pw, psw, n_slots, N, K, pf, pt, E, po, flags)
     return out
 
 
@@ -243,25 +262,26 @@ class Fp8MoELayer:
     where MoELayer carries two."""
 
     def __init__(self, w13, s13, w2, s2, slot_of_expert, k: int, T: int, out_bf16: bool = False):
-        c = _Call(w13, "w13")
-        c.take(w13, "w13", _CODES, (None, None, None))
+        dev = _first(w13, "w13", 3, _CODES)
         self.n_slots, I2, self.d = w13.shape
         self.I = I2 // 2
         nb = lambda v: (v + 127) // 128  # noqa: E731
-        c.take(w2, "w2", _CODES, (self.n_slots, self.d, self.I))
-        c.take(s13, "s13", torch.float32, (self.n_slots, nb(I2), nb(self.d)))
-        c.take(s2, "s2", torch.float32, (self.n_slots, nb(self.d), nb(self.I)))
-        c.take(slot_of_expert, "slot_of_expert", torch.int32, (None,))
-        if T < 0 or I2 % 2:
-            _refuse(f"invalid layer shape T={T}, w13 rows={I2}")
+        _take(w2, "w2", _CODES, (self.n_slots, self.d, self.I), dev)
+        _take(s13, "s13", (_F32,), (self.n_slots, nb(I2), nb(self.d)), dev)
+        _take(s2, "s2", (_F32,), (self.n_slots, nb(self.d), nb(self.I)), dev)
+        _first(slot_of_expert, "slot_of_expert", 1, (_I32,))
+        _take(slot_of_expert, "slot_of_expert", (_I32,), slot_of_expert.shape, dev)
+        if T < 0 or I2 % 2 or not 1 <= k <= min(slot_of_expert.shape[0], 32):
+            _refuse(f"invalid layer shape T={T}, k={k}, E={slot_of_expert.shape[0]}, w13 rows={I2}")
+        self.dev = dev
         self.w13, self.s13, self.w2, self.s2, self.slot_of = w13, s13, w2, s2, slot_of_expert
         self.E, self.k, self.T, self.flags = slot_of_expert.shape[0], k, T, FT_OUT_BF16 if out_bf16 else 0
-        new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=c.device)  # noqa: E731
-        P, e4, f32, bf, i32 = T * k, torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32
+        new = lambda *shape, dtype: _new(shape, dtype, dev)  # noqa: E731
+        P, e4, f32, bf, i32 = T * k, _E4, _F32, _BF, _I32
         self.ids, self.w, self.inv = new(T, k, dtype=i32), new(T, k, dtype=f32), new(max(P, 1), dtype=i32)
         self.counts, self.offsets, self.gather = new(self.E, dtype=i32), new(self.E + 1, dtype=i32), new(max(P, 1), dtype=i32)
         self.perm_ws = new(max(lib.ft_moe_permute_workspace(T, self.E, k), 16), dtype=torch.uint8)
-        S = ft_moe_fp8_scale_cols
+        S = _cols
         self.x8, self.xs = new(P, self.d, dtype=e4), new(P, S(self.d), dtype=f32)
         self.gu = new(P, I2, dtype=bf)
         self.h8, self.hs = new(P, self.I, dtype=e4), new(P, S(self.I), dtype=f32)
@@ -270,20 +290,20 @@ class Fp8MoELayer:
 
     def forward(self, logits, x, stream=None):
         """logits fp32 [T][E], x bf16 [T][d] -> (out [T][d], residual mask [T])."""
-        c = _Call(x, "x")
-        c.take(x, "x", torch.bfloat16, (self.T, self.d))
-        c.take(logits, "logits", torch.float32, (self.T, self.E))
-        if self.T == 0:
+        dev, T, E, k = self.dev, self.T, self.E, self.k
+        px = _take(x, "x", (_BF,), (T, self.d), dev)
+        pl = _take(logits, "logits", (_F32,), (T, E), dev)
+        if T == 0:
             return self.out, self.mask[:0]
-        inv = self.inv.view(self.T, self.k)
-        c.run(lib.ft_moe_route, _ptr(logits), self.T, self.E, self.k, _ptr(self.ids), _ptr(self.w), stream=stream)
-        c.run(lib.ft_moe_permute, _ptr(self.ids), self.T, self.E, self.k, _ptr(self.counts), _ptr(self.offsets),
-              _ptr(self.gather), _ptr(inv), _ptr(self.perm_ws), self.perm_ws.numel(), stream=stream)
-        ft_moe_dispatch_fp8(x, self.ids, inv, slot_of_expert=self.slot_of, codes=self.x8, scales=self.xs, stream=stream)
-        ft_moe_fp8_grouped_matmul(self.x8, self.xs, self.w13, self.s13, self.offsets, self.slot_of, out=self.gu, stream=stream)
+        inv, slot = self.inv.view(T, k), self.slot_of
+        pi, pw, pv, pt = self.ids.data_ptr(), self.w.data_ptr(), inv.data_ptr(), slot.data_ptr()
+        _run(lib.ft_moe_route, dev, stream, pl, T, E, k, pi, pw)
+        _run(lib.ft_moe_permute, dev, stream, pi, T, E, k, self.counts.data_ptr(), self.offsets.data_ptr(),
+             self.gather.data_ptr(), pv, self.perm_ws.data_ptr(), self.perm_ws.numel())
+        _run(lib.ft_moe_dispatch_fp8, dev, stream, px, pi, pv, pt, T, E, k, self.d, self.x8.data_ptr(), self.xs.data_ptr(), 0)
+        ft_moe_fp8_grouped_matmul(self.x8, self.xs, self.w13, self.s13, self.offsets, slot, out=self.gu, stream=stream)
         ft_moe_swiglu_fp8(self.gu, codes=self.h8, scales=self.hs, stream=stream)
-        ft_moe_fp8_grouped_matmul(self.h8, self.hs, self.w2, self.s2, self.offsets, self.slot_of, out=self.y_sorted,
-                                  stream=stream)
-        c.run(lib.ft_moe_combine, _ptr(self.y_sorted), None, _ptr(self.ids), _ptr(self.w), _ptr(inv), _ptr(self.slot_of),
-              self.T, self.E, self.k, self.d, _ptr(self.out), _ptr(self.mask), self.flags, stream=stream)
-        return self.out, self.mask[: self.T]
+        ft_moe_fp8_grouped_matmul(self.h8, self.hs, self.w2, self.s2, self.offsets, slot, out=self.y_sorted, stream=stream)
+        _run(lib.ft_moe_combine, dev, stream, self.y_sorted.data_ptr(), None, pi, pw, pv, pt, T, E, k, self.d,
+             self.out.data_ptr(), self.mask.data_ptr(), self.flags)
+        return self.out, self.mask[:T]

@@ -269,7 +269,9 @@ def test_gradients_against_differences_of_the_library():
 # ---------------------------------------------------------------------------------------------- products
 
 SHAPES = [(1, 1, 16), (1, 16, 128), (1, 130, 2048), (2, 100, 48), (15, 33, 112), (16, 128, 144), (17, 64, 256), (33, 250, 528),
-          (64, 256, 768), (65, 129, 2000), (128, 384, 512), (200, 520, 1040), (257, 300, 640), (300, 1536, 2048), (515, 1023, 272)]
+          (64, 256, 768), (65, 129, 2000), (128, 384, 512), (200, 520, 1040), (257, 300, 640), (300, 1536, 2048), (515, 1023, 272),
+          (17, 4100, 144), (40, 4096, 1040), (33, 7168, 144), (90, 4096, 400), (700, 4100, 400), (1100, 4096, 144),
+          (2050, 4097, 272), (1800, 4104, 528)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -307,7 +309,8 @@ def test_product_of_any_codes(M, dtype):
 
 
 GROUPS = [(1, 1, 1, None, 16, 16), (1, 8, 8, 3, 130, 144), (16, 256, 8, 96, 256, 512), (40, 12, 4, 7, 100, 272),
-          (300, 16, 4, 11, 264, 256), (700, 6, 2, 5, 384, 768), (37, 5, 3, 0, 64, 64)]
+          (300, 16, 4, 11, 264, 256), (700, 6, 2, 5, 384, 768), (37, 5, 3, 0, 64, 64), (6, 24, 2, 20, 520, 4112),
+          (64, 32, 8, 32, 1536, 768), (400, 16, 4, 16, 1032, 144), (1500, 16, 4, 12, 1040, 144), (900, 6, 3, 6, 2056, 272), (3000, 4, 4, 4, 2056, 144)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
