@@ -2,10 +2,13 @@
 // linear of the FreeToken walk-through "深入FreeToken架构…全链路剖析", section 六, over the expert groups of
 // section 五):  out[m][n] = sum_b sa[m][b] sw[n/128][b] sum_{k in b} a[m][k] w[n][k],  b = blocks of 128.
 //
-// fp8_rows_kernel: few rows.  A block takes 16 NF weight rows and up to 16 MT activation rows over the whole of
+// fp8_rows_kernel: few rows.  A block takes 16 NF weight rows and up to 16 activation rows over the whole of
 // K; its 8 waves take the 128-blocks in turn and their sums meet in LDS in a fixed order, so a single row
 // already keeps 8 waves a block busy with weight loads.  Codes are widened to bf16 (exact) and
-// multiplied on v_mfma_f32_16x16x32_bf16: products exact, fp32 sums.  Bound by the weights' bytes.
+// multiplied on v_mfma_f32_16x16x32_bf16: products exact, fp32 sums.  Bound by the weights' bytes: 38 experts
+// of 4096 x 7168 with one to three rows each in 183 us, 5.9 TB/s.  (More rows a block do not pay: a lane's
+// 16-byte chunks of 16 different rows cost the address unit 64 cycles a load, where 8 lanes a row cost 16;
+// 64 x 32 blocks of 128 rows took 28 us against 18 for the 64 x 64 tiles loaded through LDS.)
 #include <algorithm>
 #include <cmath>
 
@@ -32,7 +35,7 @@ struct Tile {
   int slot, row0, rows, n0;
 };
 
-template <int MT, int NF, int PF, bool BF16>
+template <int NF, bool BF16>
 __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl, float* s_part) {
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -41,37 +44,27 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
   // operands share is the same sum.  Rows past the end repeat the last one; their results are not stored.
   const uint8_t* wb = a.w + ((size_t)tl.slot * a.N + tl.n0) * a.K;
   const uint8_t* ab = a.a + (size_t)tl.row0 * a.K;
-  const float* sb = a.sa + (size_t)tl.row0 * a.S;
-  uint32_t wo[NF], ao[MT], so[MT];
+  uint32_t wo[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) wo[f] = (uint32_t)min(16 * f + r, a.N - 1 - tl.n0) * (uint32_t)a.K + g * 16;
+  const uint32_t row = (uint32_t)min(r, tl.rows - 1), ao = row * (uint32_t)a.K + g * 16;
+  const float* sap = a.sa + (size_t)tl.row0 * a.S + row * (uint32_t)a.S;
+  const float* swp = a.sw + ((size_t)tl.slot * nblk_n + tl.n0 / 128) * nb + (lane >> 6);  // 16 NF rows lie in one 128-block
+  f32x4 acc[NF];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const uint32_t row = (uint32_t)min(16 * m + r, tl.rows - 1);
-    ao[m] = row * (uint32_t)a.K + g * 16;
-    so[m] = row * (uint32_t)a.S;
-  }
-  const float* swp = a.sw + ((size_t)tl.slot * nblk_n + tl.n0 / 128) * nb;  // 16 NF rows lie in one 128-block
-  f32x4 acc[MT][NF];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
-  // A block's operands in registers; PF blocks are in flight while the PF before them are multiplied.
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4{0, 0, 0, 0};
+  // A block's operands in registers: the next block is in flight while one is multiplied.
   struct Regs {
-    u32x4 w[NF][2], a[MT][2];
-    float sa[MT], sw;
+    u32x4 w[NF][2], a[2];
+    float sa, sw;
   };
-  const int zero = lane >> 6;  // a lane's index, so that the weight scale is a vector load among the others
   auto load = [&](Regs& x, int b) {
-    const int bs = min(b, nb - 1);
     if (b * 128 + 128 <= a.K) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int f = 0; f < NF; ++f) x.w[f][h] = *(const u32x4*)(wb + (size_t)b * 128 + 64 * h + wo[f]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) x.a[m][h] = *(const u32x4*)(ab + (size_t)b * 128 + 64 * h + ao[m]);
+        x.a[h] = *(const u32x4*)(ab + (size_t)b * 128 + 64 * h + ao);
       }
     } else {  // the short block, or none: chunks past K count as zero codes
 #pragma unroll
@@ -81,69 +74,51 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
         const u32x4 none = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int f = 0; f < NF; ++f) x.w[f][h] = in ? *(const u32x4*)(wb + at + wo[f]) : none;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) x.a[m][h] = in ? *(const u32x4*)(ab + at + ao[m]) : none;
+        x.a[h] = in ? *(const u32x4*)(ab + at + ao) : none;
       }
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x.sa[m] = sb[so[m] + bs];
-    x.sw = swp[bs + zero];
+    x.sa = sap[min(b, nb - 1)];
+    x.sw = swp[min(b, nb - 1)];
   };
   auto multiply = [&](const Regs& x) {
-    f32x4 part[MT][NF];
+    f32x4 part[NF];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int f = 0; f < NF; ++f) part[m][f] = f32x4{0, 0, 0, 0};
+    for (int f = 0; f < NF; ++f) part[f] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      bf16x8 wf[NF][2], af[2];
+      bf16x8 wf[2], af[2];
+      widen(x.a[h], af);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) widen(x.w[f][h], wf[f]);
+      for (int f = 0; f < NF; ++f) {
+        widen(x.w[f][h], wf);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        widen(x.a[m][h], af);
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            part[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[f][q], af[q], part[m][f], 0, 0, 0);
+        for (int q = 0; q < 2; ++q) part[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[q], af[q], part[f], 0, 0, 0);
       }
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][f][i] = fmaf(part[m][f][i], x.sa[m] * x.sw, acc[m][f][i]);
+      for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(part[f][i], x.sa * x.sw, acc[f][i]);
   };
-  Regs cur[PF], nxt[PF];
-#pragma unroll
-  for (int i = 0; i < PF; ++i) load(cur[i], wv + i * RW);
-  for (int b = wv; b < nb; b += 2 * PF * RW) {
-#pragma unroll
-    for (int i = 0; i < PF; ++i) load(nxt[i], b + (PF + i) * RW);
-#pragma unroll
-    for (int i = 0; i < PF; ++i) multiply(cur[i]);
-    if (b + PF * RW >= nb) break;
-#pragma unroll
-    for (int i = 0; i < PF; ++i) load(cur[i], b + (2 * PF + i) * RW);
-#pragma unroll
-    for (int i = 0; i < PF; ++i) multiply(nxt[i]);
+  Regs even, odd;
+  load(even, wv);
+  for (int b = wv; b < nb; b += 2 * RW) {
+    load(odd, b + RW);
+    multiply(even);
+    if (b + RW >= nb) break;
+    load(even, b + 2 * RW);
+    multiply(odd);
   }
-  // lane (r, g) of a fragment holds row (activation) r and columns 4 g .. 4 g + 3 of the 16 weight rows
-  constexpr int NV = MT * NF * 256;
+  // lane (r, g) of a fragment holds activation row r and columns 4 g .. 4 g + 3 of the 16 weight rows
+  constexpr int NV = NF * 256;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) *(f32x4*)(s_part + wv * NV + ((m * NF + f) * 16 + r) * 16 + 4 * g) = acc[m][f];
+  for (int f = 0; f < NF; ++f) *(f32x4*)(s_part + wv * NV + (f * 16 + r) * 16 + 4 * g) = acc[f];
   __syncthreads();
   for (int i = threadIdx.x; i < NV; i += 64 * RW) {
     float v = s_part[i];
 #pragma unroll
     for (int q = 1; q < RW; ++q) v += s_part[q * NV + i];
-    const int fr = i >> 8, rr = (i >> 4) & 15, cc = i & 15;
-    const int m = 16 * (fr / NF) + rr, n = tl.n0 + 16 * (fr % NF) + cc;
+    const int m = (i >> 4) & 15, n = tl.n0 + 16 * (i >> 8) + (i & 15);
     if (m < tl.rows && n < a.N) {
       const size_t at = (size_t)(tl.row0 + m) * a.N + n;
       if (BF16)
@@ -155,45 +130,42 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
   __syncthreads();
 }
 
-template <int MT, int NF, int PF, bool BF16, bool GROUPED>
+template <int NF, bool BF16, bool GROUPED>
 __global__ __launch_bounds__(64 * RW) void fp8_rows_kernel(Fp8MatmulArgs a) {
-  __shared__ __attribute__((aligned(16))) float s_part[RW * MT * NF * 256];
+  __shared__ __attribute__((aligned(16))) float s_part[RW * NF * 256];
   const int ntn = (a.N + 16 * NF - 1) / (16 * NF);
   if constexpr (!GROUPED) {
     const int mt = blockIdx.x / ntn, nt = blockIdx.x % ntn;
-    rows_tile<MT, NF, PF, BF16>(a, Tile{0, mt * 16 * MT, min(16 * MT, a.M - mt * 16 * MT), nt * 16 * NF}, s_part);
+    rows_tile<NF, BF16>(a, Tile{0, mt * 16, min(16, a.M - mt * 16), nt * 16 * NF}, s_part);
   } else {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int E2 = a.E + 2;
     GroupList gl{(int*)lds, (int*)lds + E2, (int*)lds + 2 * E2, (int*)lds + 3 * E2, 0};
     build_clipped_groups(a.slot_of, a.offsets, a.E, a.M, a.n_slots, gl, (int*)lds + 4 * E2,
-                         [&](int cnt) { return (cnt + 16 * MT - 1) / (16 * MT) * ntn; });
+                         [&](int cnt) { return (cnt + 15) / 16 * ntn; });
     const int nitems = gl.item0[gl.n];
     for (int it = blockIdx.x; it < nitems; it += gridDim.x) {
       const int gi = find_group(gl.item0, gl.n, it);
-      const int local = it - gl.item0[gi], mt = local / ntn, nt = local % ntn;
-      const int m0 = mt * 16 * MT;
-      rows_tile<MT, NF, PF, BF16>(a, Tile{gl.slot[gi], gl.row0[gi] + m0, min(16 * MT, gl.cnt[gi] - m0), nt * 16 * NF},
-                              s_part);
+      const int local = it - gl.item0[gi], m0 = local / ntn * 16, nt = local % ntn;
+      rows_tile<NF, BF16>(a, Tile{gl.slot[gi], gl.row0[gi] + m0, min(16, gl.cnt[gi] - m0), nt * 16 * NF}, s_part);
     }
   }
 }
 
-template <int MT, int NF, int PF, bool BF16>
+template <int NF, bool BF16>
 hipError_t launch_rows(const Fp8MatmulArgs& a, hipStream_t s) {
-  const long long ntn = (a.N + 16 * NF - 1) / (16 * NF), ntm = (a.M + 16 * MT - 1) / (16 * MT);
+  const long long ntn = (a.N + 16 * NF - 1) / (16 * NF), ntm = (a.M + 15) / 16;
   if (a.E == 0) {
-    hipLaunchKernelGGL((fp8_rows_kernel<MT, NF, PF, BF16, false>), dim3((uint32_t)(ntn * ntm)), dim3(64 * RW), 0, s, a);
+    hipLaunchKernelGGL((fp8_rows_kernel<NF, BF16, false>), dim3((uint32_t)(ntn * ntm)), dim3(64 * RW), 0, s, a);
     return hipGetLastError();
   }
   static LaunchCache cache;
   LaunchFacts f;
   const size_t lds = group_lds_bytes(a.E);
-  hipError_t e = cache.get((const void*)fp8_rows_kernel<MT, NF, PF, BF16, true>, 64 * RW, lds, &f);
+  hipError_t e = cache.get((const void*)fp8_rows_kernel<NF, BF16, true>, 64 * RW, lds, &f);
   if (e != hipSuccess) return e;
   const long long upper = (ntm + (a.E < a.M ? a.E : a.M)) * ntn, most = (long long)f.per_cu * f.cus;
-  hipLaunchKernelGGL((fp8_rows_kernel<MT, NF, PF, BF16, true>), dim3((uint32_t)(upper < most ? upper : most)), dim3(64 * RW),
-                     lds, s, a);
+  hipLaunchKernelGGL((fp8_rows_kernel<NF, BF16, true>), dim3((uint32_t)(upper < most ? upper : most)), dim3(64 * RW), lds, s, a);
   return hipGetLastError();
 }
 
@@ -252,32 +224,40 @@ hipError_t launch_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
 
 // Which kernel: the one whose blocks, taken in rounds of the 256 compute units (or as many times that as fit),
 // are through first.  `step` is the measured time of one 128-block of K in a round, in us on an MI355X; `full`
-// where a compute unit holds `per` of the blocks.  M rows x 4096 columns, K = 7168, us a call:
-//   M        16     32     64     128    512    8192
-//   16x16    10.1   -      -      -      -      -
-//   16x32    14.0   14.9   27.8   54.3   -      -
-//   32x32    -      18.0   18.3   34.3   -      -
-//   64x32    -      20.5   27.1   27.6   -      -
-//   64x128   -      48.9   48.9   40.0   40.7   384
-//   128x128  -      50.9   51.0   42.8   43.6   368
-//   128x256  -      47.0   47.7   49.2   50.4   263 - 311
-//   256x256  -      -      -      71.3   74.1   240 - 249
+// where rounds follow each other.  M rows x 4096 columns, K = 7168, us a call (bf16 results):
+//   M           16     32     64     128    256    512    1024   8192
+//   16x16       10.2   18.3   34     65     -      -      -      -
+//   16x32       14.0   13.4   24     46     88     -      -      -
+//   64x64       15.3   15.1   15.9   18.2   19.1   35.7   68.8   533
+//   64x128      -      39     39     39     40     41     -      384
+//   128x128     -      43     43     43     43     43     49     368
+//   128x256     -      47     48     49     49     50     -      263 - 311
+//   256x256     -      -      -      71     74     74     -      206 - 249
+// and fp32 results:  16x32 88 at 256 rows, 64x64 19.3 / 21.7 / 73 at 64 / 256 / 1024, 128x128 64 / 66 / 71 and 450 at 8192.
 struct Choice {
   int rows, cols, per;
   float step, full;
   int lds;  // of the tiles kernels, 0 for the others
 };
+using Solo = TileCfg<64, 64, 1, 1, 2, false, 4>;
+using SoloWide = TileCfg<64, 64, 1, 1, 2, true, 4>;
 using T64 = TileCfg<64, 128, 1, 2, 3, false>;
 using T128 = TileCfg<128, 128, 2, 2, 4, false>;
 using T128x256 = TileCfg<128, 256, 2, 4, 3, false>;
 using T256 = TileCfg<256, 256, 2, 4, 2, false>;
 using TWide = TileCfg<128, 128, 2, 2, 2, true>;
 constexpr int kLds = 160 * 1024;  // of a compute unit
-constexpr Choice kChoices[] = {
-    {16, 16, 1, 0.18f, 0.18f, 0},  {16, 32, 1, 0.26f, 0.26f, 0},  {32, 32, 1, 0.32f, 0.32f, 0},
-     {64, 32, 1, 0.48f, 0.48f, 0},  {64, 128, 2, 0.71f, 0.86f, T64::LDS},
-    {128, 128, 1, 0.78f, 0.82f, T128::LDS}, {128, 256, 1, 0.88f, 1.25f, T128x256::LDS}, {256, 256, 1, 1.3f, 2.2f, T256::LDS}};
-constexpr Choice kWide = {128, 128, 2, 1.4f, 2.2f, TWide::LDS};  // fp32 results on the bf16 instructions
+constexpr Choice kBf16[] = {{16, 16, 1, 0.18f, 0.18f, 0},
+                            {16, 32, 1, 0.26f, 0.26f, 0},
+                            {64, 64, 1, 0.29f, 0.32f, Solo::LDS},
+                            {64, 128, 2, 0.71f, 0.86f, T64::LDS},
+                            {128, 128, 1, 0.78f, 0.82f, T128::LDS},
+                            {128, 256, 1, 0.88f, 1.25f, T128x256::LDS},
+                            {256, 256, 1, 1.3f, 2.2f, T256::LDS}};
+constexpr Choice kF32[] = {{16, 16, 1, 0.18f, 0.18f, 0},
+                           {16, 32, 1, 0.26f, 0.26f, 0},
+                           {64, 64, 1, 0.35f, 0.33f, SoloWide::LDS},
+                           {128, 128, 2, 1.2f, 2.0f, TWide::LDS}};
 
 // Rows with a slot and groups that have any, where only the device knows: as if experts were drawn evenly.
 struct Spread {
@@ -299,31 +279,43 @@ double cost(const Choice& c, const Fp8MatmulArgs& a) {
   return blocks <= 256 ? c.step : std::ceil(blocks / (256.0 * c.per)) * c.full;
 }
 
+template <bool BF16>
+int choose(const Fp8MatmulArgs& a) {
+  // A few rows a group: bound by the weights' bytes, and with long rows 16 x 32 blocks stream them fastest (top 8 of
+  // 256 experts, 96 resident, K = 7168, 16 / 32 tokens: 176 - 198 / 281 us, 5.9 TB/s; 64 x 128 tiles 207 / 293,
+  // 64 x 64 210; with K = 2048 and 4 / 16 tokens 21 / 52 us against 20 / 44 for 64 x 128)
+  if (a.E > 0 && a.K >= 4096) {
+    const Spread p = spread(a);
+    if (p.rows <= 3 * p.groups) return 1;
+  }
+  const Choice* c = BF16 ? kBf16 : kF32;
+  const int n = BF16 ? sizeof(kBf16) / sizeof(Choice) : sizeof(kF32) / sizeof(Choice);
+  int best = 0;
+  for (int i = 1; i < n; ++i)
+    if (cost(c[i], a) < cost(c[best], a)) best = i;
+  return best;
+}
+
 }  // namespace
 
 hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
-  int best = 0;
-  constexpr int n = sizeof(kChoices) / sizeof(kChoices[0]);
-  for (int i = 1; i < n; ++i)
-    if ((a.out_bf16 || !kChoices[i].lds) && cost(kChoices[i], a) < cost(kChoices[best], a)) best = i;
-  // A few rows a group: bound by the weights' bytes, and with long rows 16 x 32 blocks stream them fastest (top 8 of
-  // 256 experts, 96 resident, K = 7168, 16 / 32 tokens: 183 - 198 / 281 us, 5.9 TB/s; 64 x 128 tiles 207 / 293;
-  // with K = 2048 and 4 / 16 tokens 21 / 52 us against 20 / 44)
-  if (a.E > 0 && a.K >= 4096 && spread(a).rows <= 3 * spread(a).groups)
-    best = 1;
-  else if (!a.out_bf16 && cost(kWide, a) < cost(kChoices[best], a)) return launch_tiles<TWide, false>(a, s);
-#define ROWS(MT, NF) return a.out_bf16 ? launch_rows<MT, NF, 1, true>(a, s) : launch_rows<MT, NF, 1, false>(a, s)
-  switch (best) {
-    case 0: ROWS(1, 1);
-    case 1: ROWS(1, 2);
-    case 2: ROWS(2, 2);
-    case 3: ROWS(4, 2);
-    case 4: return launch_tiles<T64, true>(a, s);
-    case 5: return launch_tiles<T128, true>(a, s);
-    case 6: return launch_tiles<T128x256, true>(a, s);
+  if (!a.out_bf16) {
+    switch (choose<false>(a)) {
+      case 0: return launch_rows<1, false>(a, s);
+      case 1: return launch_rows<2, false>(a, s);
+      case 2: return launch_tiles<SoloWide, false>(a, s);
+      default: return launch_tiles<TWide, false>(a, s);
+    }
+  }
+  switch (choose<true>(a)) {
+    case 0: return launch_rows<1, true>(a, s);
+    case 1: return launch_rows<2, true>(a, s);
+    case 2: return launch_tiles<Solo, true>(a, s);
+    case 3: return launch_tiles<T64, true>(a, s);
+    case 4: return launch_tiles<T128, true>(a, s);
+    case 5: return launch_tiles<T128x256, true>(a, s);
     default: return launch_tiles<T256, true>(a, s);
   }
-#undef ROWS
 }
 
 }  // namespace ftk

@@ -45,19 +45,24 @@ __device__ __forceinline__ void unrolled(F&& f) {
   }
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, bool WIDE_>
+template <int BM_, int BN_, int WM_, int WN_, int NS_, bool WIDE_, int KG_ = 1>
 struct TileCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;  // NS: stages in LDS
   static constexpr bool WIDE = WIDE_;  // codes widened to bf16 (exact products), else 8-bit matrix instructions
-  static constexpr int NT = 64 * WM * WN;
+  // KG > 1: the block is KG single waves, each with the whole tile, a share of K and stages of its own; they run
+  // without barriers and their results are added at the end, in the order of K.
+  static constexpr int KG = KG_, GW = WM * WN;  // waves of a group
+  static constexpr int NT = 64 * GW * KG;
   static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;  // fragments of a wave
-  static constexpr int RQ = NT / 8;                           // rows of one load pass (8 lanes a row)
+  static constexpr int RQ = 8 * GW;                           // rows of one load pass (8 lanes a row)
   static constexpr int QA = BM / RQ, QB = BN / RQ;
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int SBUF = NS * STAGE;         // scales of 4 steps, twice: activations [BM][4] fp32,
   static constexpr int SW = SBUF + 2 * BM * 16;  // weights [BN / 128][4] in 256 bytes
-  static constexpr int LDS = SW + 2 * 256;
-  static_assert(BM % RQ == 0 && BN % RQ == 0 && BM % 64 == 0 && BM / 64 < WM * WN, "load passes");
+  static constexpr int GROUP = SW + 2 * 256, LDS = KG * GROUP;
+  static constexpr int PITCH = BN + 4;           // floats of a row of results in LDS (KG > 1), over the stages
+  static_assert(BM % RQ == 0 && BN % RQ == 0 && BM % 64 == 0 && (BM / 64 < GW || (BM == 64 && GW == 1)), "load passes");
+  static_assert(KG == 1 || (GW == 1 && BM == 64 && BN == 64 && BM * PITCH * 4 <= GROUP), "single waves share K");
   static_assert(NS >= 2 && NS <= 4, "the scales of 4 steps are held twice");
   static_assert(NF == 4 && 128 % (BN / WN) == 0, "a wave's 64 weight rows share one scale");
 };
@@ -74,32 +79,37 @@ struct TileJob {
 template <class C, bool BF16>
 __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& job, uint8_t* lds) {
   constexpr int MF = C::MF, NF = C::NF;
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63, gwv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = gwv / C::GW, wv = gwv % C::GW, tid = wv * 64 + lane;  // in the group
   const int r = lane & 15, g = lane >> 4;
   const int wm = wv / C::WN, wn = wv % C::WN;
   const int K = a.K, nb = (K + 127) / 128, nblk_n = (a.N + 127) / 128;
+  const int b0 = nb * kg / C::KG, b1 = nb * (kg + 1) / C::KG;  // this group's blocks
+  uint8_t* const block_lds = lds;
+  lds += kg * C::GROUP;
   const uint32_t lds0 = lds_addr(lds);
 
   // ---- loads: rows past the end repeat the last one (their results are not stored)
-  const int lrow = tid >> 3, ca = (tid & 7) ^ key_a(lrow);  // key_a's bits do not change from pass to pass
+  const int lrow = tid >> 3;
+  auto ca = [&](int q) { return (tid & 7) ^ key_a(q * C::RQ + lrow); };
   auto cb = [&](int q) { return (tid & 7) ^ key_b(q * C::RQ + lrow); };
   const int wrows = min(C::BN, a.N - job.n0);
   uint32_t va[C::QA], vb[C::QB];
 #pragma unroll
-  for (int q = 0; q < C::QA; ++q) va[q] = (uint32_t)min(q * C::RQ + lrow, job.rows - 1) * (uint32_t)K + ca * 16;
+  for (int q = 0; q < C::QA; ++q) va[q] = (uint32_t)min(q * C::RQ + lrow, job.rows - 1) * (uint32_t)K + ca(q) * 16;
 #pragma unroll
   for (int q = 0; q < C::QB; ++q) vb[q] = (uint32_t)min(q * C::RQ + lrow, wrows - 1) * (uint32_t)K + cb(q) * 16;
   const uint32_t vs = (uint32_t)min(tid, job.rows - 1) * (uint32_t)a.S * 4;
-  const uint8_t* pa = a.a + (size_t)job.row0 * K;
-  const uint8_t* pb = a.w + ((size_t)job.slot * a.N + job.n0) * K;
+  const uint8_t* pa = a.a + (size_t)job.row0 * K + (size_t)b0 * 128;
+  const uint8_t* pb = a.w + ((size_t)job.slot * a.N + job.n0) * K + (size_t)b0 * 128;
   const uint8_t* ps = (const uint8_t*)(a.sa + (size_t)job.row0 * a.S);
   const uint8_t* pw = (const uint8_t*)(a.sw + ((size_t)job.slot * nblk_n + job.n0 / 128) * nb);
-  const int wblk = min((lane >> 2) & (C::BN / 128 - 1), nblk_n - 1 - job.n0 / 128);  // lane / 4's block of 128 weight rows
+  const int wblk = min((lane >> 2) & (C::BN > 128 ? C::BN / 128 - 1 : 0), nblk_n - 1 - job.n0 / 128);  // lane / 4's block of 128 weight rows
   const int nfull = K >> 7;  // whole blocks; a shorter one may follow
   // The loads of a stage, one at a time, in stage order: U units of 16 bytes a lane, and every fourth stage a load
   // of the next 4 steps' scales (the last wave's are the weights').  fill: the stage being loaded and its buffer.
   constexpr int U = C::QA + C::QB, NS = C::NS;
-  int fill = 0;
+  int fill = b0;
   uint32_t fill_lds = lds0 + wv * 1024;
   auto issue_unit = [&](auto u_) {
     constexpr int u = decltype(u_)::value;
@@ -111,16 +121,15 @@ __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& 
   // Before a stage's units: its scales, and chunks of a short block past K load the block's first chunk (turn()
   // clears them).
   auto open = [&] {
-    if ((fill & 3) == 0) {
-      const uint32_t half = (fill >> 2) & 1;
-      if (wv < C::BM / 64)
-        dma16<C::SBUF>(ps + (size_t)fill * 4, vs, lds0 + half * C::BM * 16 + wv * 1024);
-      else if (wv == C::WM * C::WN - 1)
-        dma4(pw, (uint32_t)(wblk * nb + min(fill + (lane & 3), nb - 1)) * 4, lds0 + C::SW + half * 256);
+    if ((fill & 3) == 0 || fill == b0) {
+      const uint32_t half = (fill >> 2) & 1, first = fill & ~3;
+      if (wv < C::BM / 64) dma16<C::SBUF>(ps + (size_t)first * 4, vs, lds0 + half * C::BM * 16 + wv * 1024);
+      if (wv == C::GW - 1)
+        dma4(pw, (uint32_t)(wblk * nb + min((int)first + (lane & 3), nb - 1)) * 4, lds0 + C::SW + half * 256);
     }
     if (fill == nfull) {
 #pragma unroll
-      for (int q = 0; q < C::QA; ++q) va[q] -= fill * 128 + ca * 16 < K ? 0 : ca * 16;
+      for (int q = 0; q < C::QA; ++q) va[q] -= fill * 128 + ca(q) * 16 < K ? 0 : ca(q) * 16;
 #pragma unroll
       for (int q = 0; q < C::QB; ++q) vb[q] -= fill * 128 + cb(q) * 16 < K ? 0 : cb(q) * 16;
     }
@@ -166,26 +175,30 @@ __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& 
   // whose buffer can be loaded again.  The chunks of a short block that lie past K become zero codes.
   // (The stages after it that are in flight, U loads or one more each, may stay so.)
   auto turn = [&](int b, const uint8_t* stage) {
-    const int newer = min(NS - 2, nb - 1 - b);
+    const int newer = min(NS - 2, b1 - 1 - b);
     if (NS == 4 && newer == 2)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * U) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * U) : "memory");
     else if (NS > 2 && newer == 1)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(U) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(U) : "memory");
     else
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    if constexpr (C::GW > 1) asm volatile("s_barrier" ::: "memory");
     if (b == nfull) {
       uint8_t* st = const_cast<uint8_t*>(stage) + tid * 16;
 #pragma unroll
       for (int q = 0; q < C::QA; ++q)
-        if (b * 128 + ca * 16 >= K) *(u32x4*)(st + q * C::RQ * 128) = u32x4{0, 0, 0, 0};
+        if (b * 128 + ca(q) * 16 >= K) *(u32x4*)(st + q * C::RQ * 128) = u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < C::QB; ++q)
         if (b * 128 + cb(q) * 16 >= K) *(u32x4*)(st + C::BM * 128 + q * C::RQ * 128) = u32x4{0, 0, 0, 0};
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if constexpr (C::GW > 1) asm volatile("s_barrier" ::: "memory");
     }
   };
 
-  if constexpr (!C::WIDE) {
+  if (C::KG > 1 && b0 == b1) {
+    // fewer blocks than groups
+  } else if constexpr (!C::WIDE) {
     // The instruction stream is one pipeline over all steps, in groups of two fragment rows by four fragments:
     // each matrix instruction is followed by the multiply-adds of the fragment two instructions back and by
     // LDS reads of what comes a group later.  The turn from stage b to b + 1 comes before the last group of
@@ -204,31 +217,31 @@ __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& 
       for (int i = 0; i < 4; ++i) c[i] = fmaf(q[i], s, c[i]);
       asm volatile("" : "+v"(c));  // here, not sunk to where it is next read
     };
-    while (fill < min(NS - 1, nb)) issue();
-    turn(0, lds);
-    if (fill < nb) issue();
+    while (fill < min(b0 + NS - 1, b1)) issue();
+    turn(b0, lds);
+    if (fill < b1) issue();
 #pragma unroll
     for (int f = 0; f < NF; ++f) wf[f] = frag(lds, rb + f * 512);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       af[0][i] = frag(lds, ra + i * 2048);
-      sa[i] = sa_of(0, i);
+      sa[i] = sa_of(b0, i);
     }
-    sw = sw_of(0);
+    sw = sw_of(b0);
     const uint8_t* st = lds;
-    for (int b = 0; b < nb; ++b) {
+    for (int b = b0; b < b1; ++b) {
       const uint8_t* nx = after(st);  // past the last step: read but unused
       // the stage that takes the buffer freed by the last turn is loaded after it: first units in the last group of
       // a step, the others in the next step's
-      bool filling = b > 0 && fill < nb;
+      bool filling = b > b0 && fill < b1;
 #pragma unroll
       for (int p = 0; p < G; ++p) {
         if (p == G - 1) {
           if (filling) advance();
           filling = false;
-          if (b + 1 < nb) {
+          if (b + 1 < b1) {
             turn(b + 1, nx);
-            filling = fill < nb;
+            filling = fill < b1;
             if (filling) open();
           }
         }
@@ -296,57 +309,80 @@ __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& 
         }
       }
     };
-    while (fill < min(NS - 1, nb)) issue();
+    while (fill < min(b0 + NS - 1, b1)) issue();
     const uint8_t* st = lds;
-    for (int b = 0; b < nb; ++b, st = after(st)) {
+    for (int b = b0; b < b1; ++b, st = after(st)) {
       turn(b, st);
-      if (fill < nb) issue();
+      if (fill < b1) issue();
       step(b, st);
     }
   }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the stages are free for the next tile
-
-  // ---- lane (r, g), fragment m: row wm 16 MF + 16 m + r, columns wn 64 + 16 g .. + 15
-  const int n = job.n0 + wn * 16 * NF + 16 * g;
-  const bool whole = n + 16 <= a.N && (a.N & (BF16 ? 7 : 3)) == 0;
-#pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    const int row = arow + 16 * m;
-    if (row >= job.rows || n >= a.N) continue;
+  // 16 consecutive results of a row
+  auto store = [&](int row, int n, const f32x4 (&v)[4]) {
+    if (row >= job.rows || n >= a.N) return;
     const size_t at = (size_t)(job.row0 + row) * a.N + n;
-    if (BF16) {
+    const bool whole = n + 16 <= a.N && (a.N & (BF16 ? 7 : 3)) == 0;
+    if constexpr (BF16) {
       uint16_t* o = (uint16_t*)a.out + at;
       if (whole) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          u32x4 v;
+          u32x4 w;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const f32x4& p = acc[m][2 * h + i / 2];
-            v[i] = (uint32_t)f32_to_bf16_bits(p[2 * (i & 1)]) | ((uint32_t)f32_to_bf16_bits(p[2 * (i & 1) + 1]) << 16);
+            const f32x4& p = v[2 * h + i / 2];
+            w[i] = (uint32_t)f32_to_bf16_bits(p[2 * (i & 1)]) | ((uint32_t)f32_to_bf16_bits(p[2 * (i & 1) + 1]) << 16);
           }
-          *(u32x4*)(o + 8 * h) = v;
+          *(u32x4*)(o + 8 * h) = w;
         }
       } else {
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+        for (int f = 0; f < 4; ++f)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (n + 4 * f + i < a.N) o[4 * f + i] = f32_to_bf16_bits(acc[m][f][i]);
+            if (n + 4 * f + i < a.N) o[4 * f + i] = f32_to_bf16_bits(v[f][i]);
       }
     } else {
       float* o = (float*)a.out + at;
       if (whole) {
 #pragma unroll
-        for (int f = 0; f < NF; ++f) *(f32x4*)(o + 4 * f) = acc[m][f];
+        for (int f = 0; f < 4; ++f) *(f32x4*)(o + 4 * f) = v[f];
       } else {
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
+        for (int f = 0; f < 4; ++f)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (n + 4 * f + i < a.N) o[4 * f + i] = acc[m][f][i];
+            if (n + 4 * f + i < a.N) o[4 * f + i] = v[f][i];
       }
     }
+  };
+
+  if constexpr (C::KG == 1) {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the stages are free for the next tile
+    // lane (r, g), fragment row m: row wm 16 MF + 16 m + r, columns wn 64 + 16 g .. + 15
+#pragma unroll
+    for (int m = 0; m < MF; ++m) store(arow + 16 * m, job.n0 + wn * 16 * NF + 16 * g, acc[m]);
+  } else {
+    // every wave's results over its own stages, then the sums in the order of K
+    float* mine = (float*)lds;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) *(f32x4*)(mine + (16 * m + r) * C::PITCH + 16 * g + 4 * f) = acc[m][f];
+    __syncthreads();
+    for (int i = threadIdx.x; i < C::BM * C::BN / 16; i += C::NT) {
+      const int row = i / (C::BN / 16), n = i % (C::BN / 16) * 16;
+      f32x4 v[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) v[f] = *(const f32x4*)((const float*)block_lds + row * C::PITCH + n + 4 * f);
+#pragma unroll
+      for (int q = 1; q < C::KG; ++q)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) v[f] += *(const f32x4*)((const float*)(block_lds + q * C::GROUP) + row * C::PITCH + n + 4 * f);
+      store(row, job.n0 + n, v);
+    }
+    __syncthreads();  // the stages are free for the next tile
   }
 }
 
