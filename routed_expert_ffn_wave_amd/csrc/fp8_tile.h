@@ -198,6 +198,14 @@ __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& 
 
   if (C::KG > 1 && b0 == b1) {
     // fewer blocks than groups
+  } else if (C::GW > 1 && wm * 16 * MF >= job.rows) {
+    // a wave without rows: its share of the loads and the turns
+    while (fill < min(b0 + NS - 1, b1)) issue();
+    const uint8_t* st = lds;
+    for (int b = b0; b < b1; ++b, st = after(st)) {
+      turn(b, st);
+      if (fill < b1) issue();
+    }
   } else if constexpr (!C::WIDE) {
     // The instruction stream is one pipeline over all steps, in groups of two fragment rows by four fragments:
     // each matrix instruction is followed by the multiply-adds of the fragment two instructions back and by
