@@ -27,6 +27,12 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return o;
 }
 
+// Lane j: the row of pair f0 + j, -1 without one (also from k on): one chain of loads for all k pairs.
+__device__ __forceinline__ int rows_of(const PairTab& tab, int f0) {
+  const int lane = threadIdx.x & 63;
+  return lane < tab.k ? tab.row(f0 + lane) : -1;
+}
+
 // One wave per (token, 4 KiB of its row).  pieces: 16-byte pieces per row.
 __global__ __launch_bounds__(256) void dispatch_kernel(const u32x4* __restrict__ x, PairTab tab, uint32_t nwork,
                                                        uint32_t nseg, int pieces, u32x4* __restrict__ xs) {
@@ -38,8 +44,9 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const u32x4* __restrict__
 #pragma unroll
   for (int q = 0; q < SEG_U; ++q)
     if (p0 + 64 * q < pieces) v[q] = x[(size_t)t * pieces + p0 + 64 * q];
+  const int rows = rows_of(tab, (int)t * tab.k);
   for (int j = 0; j < tab.k; ++j) {
-    const int r = tab.row((int)t * tab.k + j);
+    const int r = __builtin_amdgcn_readlane(rows, j);
     if (r < 0) continue;
 #pragma unroll
     for (int q = 0; q < SEG_U; ++q)
@@ -57,6 +64,7 @@ __global__ __launch_bounds__(256) void dispatch_grad_kernel(const u32x4* __restr
   if (wk >= nwork) return;
   const uint32_t t = wk / nseg;
   const int p0 = (int)(wk - t * nseg) * (64 * SEG_U) + (threadIdx.x & 63);
+  const int rows = rows_of(tab, (int)t * tab.k);
   float acc[SEG_U][NV];
 #pragma unroll
   for (int q = 0; q < SEG_U; ++q)
@@ -66,7 +74,7 @@ __global__ __launch_bounds__(256) void dispatch_grad_kernel(const u32x4* __restr
     u32x4 v[JB][SEG_U];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
-      const int r = j0 + j < tab.k ? tab.row((int)t * tab.k + j0 + j) : -1;
+      const int r = __builtin_amdgcn_readlane(rows, j0 + j);  // -1 from k on (k <= 32)
 #pragma unroll
       for (int q = 0; q < SEG_U; ++q) {
         v[j][q] = u32x4{0, 0, 0, 0};
@@ -108,7 +116,30 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// One block per token: dy rows, the k dot products dout . y, and the row of dlogits.
+// Sums of 8 values over the wave: lane l gets the sum of value l % 8.  Three exchanges halve the values a lane holds,
+// three more add the 8 partial sums of a value: 10 exchanges instead of 48.
+__device__ __forceinline__ float wave_sums8(const float (&v)[8]) {
+  const int lane = threadIdx.x & 63;
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // keep the values whose bit 0 is the lane's
+    const float keep = lane & 1 ? v[2 * i + 1] : v[2 * i], give = lane & 1 ? v[2 * i] : v[2 * i + 1];
+    a[i] = keep + __shfl_xor(give, 1, 64);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = lane & 2 ? a[2 * i + 1] : a[2 * i], give = lane & 2 ? a[2 * i] : a[2 * i + 1];
+    b[i] = keep + __shfl_xor(give, 2, 64);
+  }
+  const float keep = lane & 4 ? b[1] : b[0], give = lane & 4 ? b[0] : b[1];
+  float s = keep + __shfl_xor(give, 4, 64);
+#pragma unroll
+  for (int o = 8; o <= 32; o <<= 1) s += __shfl_xor(s, o, 64);
+  return s;
+}
+
+// One block per token: dy rows, the k dot products dout . y, and the row of dlogits.  The pair tables are read once,
+// a lane per pair, beside the first piece of dout.
 template <bool BF16>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const void* __restrict__ dout,
                                                            const uint16_t* __restrict__ y,
@@ -121,13 +152,16 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const void* __restric
   __shared__ int s_id[32];
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int f0 = t * tab.k;
+  const bool on = lane < tab.k;
+  const int rows = rows_of(tab, f0), id = on ? tab.ids[f0 + lane] : -1;
+  const float wl = on ? w[f0 + lane] : 0.0f;
   for (int j0 = 0; j0 < tab.k; j0 += JB) {
     int r[JB];
     float wj[JB], acc[JB];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
-      r[j] = j0 + j < tab.k ? tab.row(f0 + j0 + j) : -1;
-      wj[j] = j0 + j < tab.k ? w[f0 + j0 + j] : 0.0f;
+      r[j] = __builtin_amdgcn_readlane(rows, j0 + j);
+      wj[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wl), j0 + j));
       acc[j] = 0.0f;
     }
     for (int c = tid * 8; c < d; c += 256 * 8) {
@@ -157,23 +191,18 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const void* __restric
           *(u32x4*)(dy + (size_t)r[j] * d + c) = pack8(o);
         }
     }
-#pragma unroll
-    for (int j = 0; j < JB; ++j) {
-      const float a = wave_sum(acc[j]);
-      if (lane == 0 && j0 + j < tab.k) s_part[wv][j0 + j] = a;
-    }
+    const float s = wave_sums8(acc);
+    if (lane < JB) s_part[wv][j0 + lane] = s;  // k <= 32: j0 + 7 < 32
   }
   __syncthreads();
   if (tid < 64) {
-    const bool on = lane < tab.k;
     const float a = on ? (s_part[0][lane] + s_part[1][lane]) + (s_part[2][lane] + s_part[3][lane]) : 0.0f;
     if (on) dw[f0 + lane] = a;
     if (dlogits) {
-      const float wl = on ? w[f0 + lane] : 0.0f;
       const float mean = wave_sum(on ? wl * a : 0.0f);
       if (on) {
         s_dl[lane] = wl * (a - mean);
-        s_id[lane] = tab.ids[f0 + lane];
+        s_id[lane] = id;
       }
     }
   }
