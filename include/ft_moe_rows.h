@@ -12,7 +12,9 @@
  * caller-owned buffers, enqueue-only on `stream`, FT_OK or a status with ft_moe_last_error(), calls
  * reentrant and capturable into a graph.  No call here needs a workspace or keeps any state, and no
  * result depends on the order in which blocks or atomics run: the same inputs give the same bits.
- * Outputs must not overlap inputs or each other.  Sizes of 0 rows or tokens are no-ops.
+ * Outputs must not overlap inputs or each other.  Sizes of 0 rows or tokens are no-ops.  Sizes that one launch
+ * cannot count are refused with FT_E_UNSUPPORTED: 2^29 scales, 2^26 pieces of 1024 values of token rows, 2^24
+ * tokens (ft_moe_combine_grad), 2^23 tiles of a product.
  *
  * 8-bit rows.  A row of K values (K % 16 == 0) is K e4m3fn codes and S = ft_moe_fp8_scale_cols(K) fp32
  * scales: scale b covers values 128 b .. 128 b + 127 (the last block may be shorter) and the columns
@@ -48,6 +50,7 @@ int ft_moe_quant_fp8(const void* x, int rows, int K, uint8_t* codes, float* scal
  * The 8-bit rows of h = SiLU(g) * u, SiLU(g) = g / (1 + e^-g), computed and quantised in fp32 (h is not
  * rounded to bf16 in between).  gu bf16 [rows][2 I]: gate columns 0 .. I-1, up columns I .. 2I-1
  * (what ft_moe_fp8_grouped_matmul gives for W13 rows [gate ; up]) -> codes [rows][I], scales [rows][S].
+ * 1 / (1 + e^-g) under 2^-126 (g < -87.3) may count as 0.
  */
 int ft_moe_swiglu_fp8(const uint16_t* gu, int rows, int I, uint8_t* codes, float* scales, hipStream_t stream);
 
@@ -109,7 +112,8 @@ int ft_moe_fp8_matmul(const uint8_t* a, const float* a_scales, int M, const uint
  * The same with one matrix per expert: rows offsets[e] .. offsets[e+1]-1 of the P rows (offsets int32 [E+1]
  * from ft_moe_permute; entries are taken as if clipped to [0, P]) are multiplied with the matrix in slot
  * slot_of_expert[e] of w [n_slots][N][K], w_scales [n_slots][ceil(N/128)][ceil(K/128)].  Rows of experts
- * without a slot in [0, n_slots), and rows that belong to no expert, are left as they were.
+ * without a slot in [0, n_slots), and rows that belong to no expert, are left as they were; a row that a table
+ * which does not ascend gives to several experts gets the result of one of them.
  * 1 <= E <= 1024.
  */
 int ft_moe_fp8_grouped_matmul(const uint8_t* a, const float* a_scales, int P, const uint8_t* w, const float* w_scales,

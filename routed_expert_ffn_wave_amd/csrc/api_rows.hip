@@ -20,7 +20,8 @@ int check_rows_fp8(int rows, int K, const char* rows_name, const char* K_name) {
   REQUIRE(rows >= 0, FT_E_INVAL, "%s must be >= 0 (got %d)", rows_name, rows);
   REQUIRE(K > 0 && K % 16 == 0 && K <= (1 << 20), FT_E_INVAL, "%s must be a positive multiple of 16, at most 2^20 (got %d)",
           K_name, K);
-  REQUIRE((long long)rows * fp8_scale_cols(K) <= (1LL << 31), FT_E_UNSUPPORTED, "%s too large (%d rows of %d values)",
+  // 8 lanes per scale, under the 2^32 threads of a launch
+  REQUIRE((long long)rows * fp8_scale_cols(K) < (1LL << 29), FT_E_UNSUPPORTED, "%s too large (%d rows of %d values)",
           rows_name, rows, K);
   return FT_OK;
 }
@@ -30,8 +31,8 @@ int check_pairs(int T, int E, int k, int d, int multiple) {
   if (rc) return rc;
   REQUIRE(d > 0 && d % multiple == 0 && d <= (1 << 20), FT_E_INVAL,
           "d must be a positive multiple of %d, at most 2^20 (got %d)", multiple, d);
-  // work units of a launch: one per token and 4 KiB of a row
-  REQUIRE((long long)T * ((d + 1023) / 1024) <= (1LL << 31), FT_E_UNSUPPORTED, "T too large (%d tokens of %d values)", T, d);
+  // a wave per token and 4 KiB of a row, under the 2^32 threads of a launch
+  REQUIRE((long long)T * ((d + 1023) / 1024) < (1LL << 26), FT_E_UNSUPPORTED, "T too large (%d tokens of %d values)", T, d);
   return FT_OK;
 }
 
@@ -51,6 +52,12 @@ int check_matmul(int rows, const char* rows_name, int N, int K, int E, int flags
   REQUIRE(((long long)rows / 16 + 1 + E) * ((N + 15) / 16) < (1LL << 31), FT_E_UNSUPPORTED,
           "product too large (%d rows, N=%d)", rows, N);
   return FT_OK;
+}
+
+int run_matmul(const Fp8MatmulArgs& m, const char* what, hipStream_t stream) {
+  const hipError_t e = launch_fp8_matmul(m, stream);
+  REQUIRE(e != hipErrorNotSupported, FT_E_UNSUPPORTED, "product too large (%d rows, N=%d, E=%d)", m.M, m.N, m.E);
+  return hip_status(e, what);
 }
 
 }  // namespace
@@ -151,6 +158,7 @@ int ft_moe_combine_grad(const void* dout, const uint16_t* y_sorted, const int32_
     int rc = check_pairs(T, E, k, d, 8);
     if (rc) return rc;
     if ((rc = check_flags(flags, FT_OUT_BF16))) return rc;
+    REQUIRE(T < (1 << 24), FT_E_UNSUPPORTED, "T too large (%d tokens, a block of 256 threads each)", T);
     if (T == 0) return ok();
     CHECK_PTR(dout, "dout");
     CHECK_PTR(y_sorted, "y_sorted");
@@ -181,7 +189,7 @@ int ft_moe_fp8_matmul(const uint8_t* a, const float* a_scales, int M, const uint
     CHECK_PTR(out, "out");
     Fp8MatmulArgs m{a, a_scales, w, w_scales, M, N, K, fp8_scale_cols(K), 1, nullptr, nullptr, 0, out,
                     (flags & FT_OUT_BF16) != 0};
-    return hip_status(launch_fp8_matmul(m, stream), "ft_moe_fp8_matmul launch");
+    return run_matmul(m, "ft_moe_fp8_matmul launch", stream);
   } catch (...) {
     return fail(FT_E_INTERNAL, "ft_moe_fp8_matmul: unexpected exception");
   }
@@ -205,7 +213,7 @@ int ft_moe_fp8_grouped_matmul(const uint8_t* a, const float* a_scales, int P, co
     CHECK_PTR(out, "out");
     Fp8MatmulArgs m{a, a_scales, w, w_scales, P, N, K, fp8_scale_cols(K), n_slots, offsets, slot_of_expert, E, out,
                     (flags & FT_OUT_BF16) != 0};
-    return hip_status(launch_fp8_matmul(m, stream), "ft_moe_fp8_grouped_matmul launch");
+    return run_matmul(m, "ft_moe_fp8_grouped_matmul launch", stream);
   } catch (...) {
     return fail(FT_E_INTERNAL, "ft_moe_fp8_grouped_matmul: unexpected exception");
   }

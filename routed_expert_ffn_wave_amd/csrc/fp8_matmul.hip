@@ -49,7 +49,9 @@ __device__ __forceinline__ void rows_tile(const Fp8MatmulArgs& a, const Tile& tl
   for (int f = 0; f < NF; ++f) wo[f] = (uint32_t)min(16 * f + r, a.N - 1 - tl.n0) * (uint32_t)a.K + g * 16;
   const uint32_t row = (uint32_t)min(r, tl.rows - 1), ao = row * (uint32_t)a.K + g * 16;
   const float* sap = a.sa + (size_t)tl.row0 * a.S + row * (uint32_t)a.S;
-  const float* swp = a.sw + ((size_t)tl.slot * nblk_n + tl.n0 / 128) * nb + (lane >> 6);  // 16 NF rows lie in one 128-block
+  // 16 NF rows lie in one 128-block.  (lane >> 6 is 0, but by lane: vector loads, which complete in order, where a scalar
+  // load is waited for together with every LDS operation.)
+  const float* swp = a.sw + ((size_t)tl.slot * nblk_n + tl.n0 / 128) * nb + (lane >> 6);
   f32x4 acc[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) acc[f] = f32x4{0, 0, 0, 0};
@@ -268,32 +270,41 @@ Spread spread(const Fp8MatmulArgs& a) {
   return {std::max(1.0, held * a.M), std::max(1.0, held * a.E * (1.0 - std::exp(-(double)a.M / a.E)))};
 }
 
+constexpr double kNever = 1e30;
+
 double cost(const Choice& c, const Fp8MatmulArgs& a) {
-  if (c.lds + (a.E > 0 ? group_lds_bytes(a.E) : 0) > kLds) return 1e30;
+  if (c.lds + (a.E > 0 ? group_lds_bytes(a.E) : 0) > kLds) return kNever;
+  // Counts that have to fit: the threads of a dense launch (at most 512 a block) in 32 bits, the tiles of all groups
+  // in an int whatever the table holds (one that does not ascend can give all rows to every second expert).
+  const double ntn = (a.N + c.cols - 1) / c.cols;
+  if (a.E == 0 ? ((a.M + c.rows - 1) / c.rows) * ntn >= 1 << 23
+               : (a.M / c.rows + 2.0) * (a.E / 2 + 1) * ntn >= 2147483648.0)
+    return kNever;
   double chunks = (a.M + c.rows - 1) / c.rows;
   if (a.E > 0) {  // each group has half a chunk to spare
     const Spread p = spread(a);
     chunks = std::max(p.groups, p.rows / c.rows + 0.5 * p.groups);
   }
-  const double blocks = chunks * ((a.N + c.cols - 1) / c.cols);
+  const double blocks = chunks * ntn;
   return blocks <= 256 ? c.step : std::ceil(blocks / (256.0 * c.per)) * c.full;
 }
 
+// -1: none fits
 template <bool BF16>
 int choose(const Fp8MatmulArgs& a) {
+  const Choice* c = BF16 ? kBf16 : kF32;
   // A few rows a group: bound by the weights' bytes, and with long rows 16 x 32 blocks stream them fastest (top 8 of
   // 256 experts, 96 resident, K = 7168, 16 / 32 tokens: 176 - 198 / 281 us, 5.9 TB/s; 64 x 128 tiles 207 / 293,
   // 64 x 64 210; with K = 2048 and 4 / 16 tokens 21 / 52 us against 20 / 44 for 64 x 128)
   if (a.E > 0 && a.K >= 4096) {
     const Spread p = spread(a);
-    if (p.rows <= 3 * p.groups) return 1;
+    if (p.rows <= 3 * p.groups && cost(c[1], a) < kNever) return 1;
   }
-  const Choice* c = BF16 ? kBf16 : kF32;
   const int n = BF16 ? sizeof(kBf16) / sizeof(Choice) : sizeof(kF32) / sizeof(Choice);
   int best = 0;
   for (int i = 1; i < n; ++i)
     if (cost(c[i], a) < cost(c[best], a)) best = i;
-  return best;
+  return cost(c[best], a) < kNever ? best : -1;
 }
 
 }  // namespace
@@ -301,6 +312,7 @@ int choose(const Fp8MatmulArgs& a) {
 hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
   if (!a.out_bf16) {
     switch (choose<false>(a)) {
+      case -1: return hipErrorNotSupported;
       case 0: return launch_rows<1, false>(a, s);
       case 1: return launch_rows<2, false>(a, s);
       case 2: return launch_tiles<SoloWide, false>(a, s);
@@ -308,6 +320,7 @@ hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
     }
   }
   switch (choose<true>(a)) {
+    case -1: return hipErrorNotSupported;
     case 0: return launch_rows<1, true>(a, s);
     case 1: return launch_rows<2, true>(a, s);
     case 2: return launch_tiles<Solo, true>(a, s);

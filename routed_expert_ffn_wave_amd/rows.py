@@ -3,7 +3,9 @@ order, and the gradients of the dispatch and of the weighted combine.
 
 The functions carry the C ABI's names.  Unlike the C calls they see the tensors' types, so they also
 refuse (FtError, FT_E_INVAL) a tensor of another type, shape, device or layout than the call reads.
-Work is enqueued on the current stream of the tensors' device, or on `stream`.  8-bit codes are
+Work is enqueued on the current stream of the tensors' device, or on `stream` (a stream of that device);
+outputs that are not given come from that stream's memory, and a tensor that other streams use too is the
+caller's to order and to keep (Tensor.record_stream), as with any work of torch's.  8-bit codes are
 torch.float8_e4m3fn tensors (uint8 is taken too)."""
 from __future__ import annotations
 
@@ -46,8 +48,8 @@ def _refuse(text: str):
     raise FtError(FT_E_INVAL, text)
 
 
-def _first(t, name: str, dims: int, dtypes) -> int:
-    """Checks a call's first tensor, whose sizes the others follow; returns its GPU."""
+def _first(t, name: str, dims: int, dtypes, stream=None) -> int:
+    """Checks a call's first tensor, whose sizes the others follow, and its stream; returns the tensor's GPU."""
     if not isinstance(t, torch.Tensor):
         _refuse(f"{name} must be a tensor")
     if not t.is_cuda:
@@ -55,7 +57,10 @@ def _first(t, name: str, dims: int, dtypes) -> int:
     if t.dim() != dims or t.dtype not in dtypes or not t.is_contiguous():
         _refuse(f"{name} must be a contiguous tensor of {dims} dimensions and type "
                 f"{' or '.join(str(d) for d in dtypes)} (got {t.dtype}, {list(t.shape)}, strides {t.stride()})")
-    return t.get_device()
+    dev = t.get_device()
+    if stream is not None and stream.device_index != dev:
+        _refuse(f"the stream is of cuda:{stream.device_index}, {name} is on cuda:{dev}")
+    return dev
 
 
 def _take(t, name: str, dtypes, shape, dev: int):
@@ -85,8 +90,12 @@ def _run(fn, dev: int, stream, *args):
         _check(rc)
 
 
-def _new(shape, dtype, dev: int):
-    return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+def _new(shape, dtype, dev: int, stream=None):
+    """A tensor to write on `stream`: from that stream's memory, which no work of another stream still uses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
 
 
 def _pairs(ids, inv, slot_of_expert, E, T, dev: int):
@@ -118,42 +127,42 @@ def ft_moe_fp8_scale_cols(K: int) -> int:
     return lib.ft_moe_fp8_scale_cols(K)
 
 
-def _rows_out(codes, scales, rows: int, K: int, dev: int):
+def _rows_out(codes, scales, rows: int, K: int, dev: int, stream):
     if codes is None:
-        codes = _new((rows, K), _E4, dev)
+        codes = _new((rows, K), _E4, dev, stream)
     if scales is None:
-        scales = _new((rows, _cols(K)), _F32, dev)
+        scales = _new((rows, _cols(K)), _F32, dev, stream)
     return codes, scales, _take(codes, "codes", _CODES, (rows, K), dev), _take(scales, "scales", (_F32,), (rows, _cols(K)), dev)
 
 
 def ft_moe_quant_fp8(x, codes=None, scales=None, stream=None):
     """bf16 or fp32 rows [rows][K] -> (codes [rows][K], scales fp32 [rows][S]): per block of 128 the scale is the
     largest magnitude / 448 and the codes are the nearest e4m3 values of x / scale."""
-    dev = _first(x, "x", 2, _FLOATS)
+    dev = _first(x, "x", 2, _FLOATS, stream)
     rows, K = x.shape
-    codes, scales, pc, ps = _rows_out(codes, scales, rows, K, dev)
+    codes, scales, pc, ps = _rows_out(codes, scales, rows, K, dev, stream)
     _run(lib.ft_moe_quant_fp8, dev, stream, x.data_ptr(), rows, K, pc, ps, FT_ROWS_F32 if x.dtype is _F32 else 0)
     return codes, scales
 
 
 def ft_moe_swiglu_fp8(gu, codes=None, scales=None, stream=None):
     """bf16 rows [rows][2 I] = [gate | up] -> the 8-bit rows (codes [rows][I], scales) of SiLU(gate) * up."""
-    dev = _first(gu, "gu", 2, (_BF,))
+    dev = _first(gu, "gu", 2, (_BF,), stream)
     rows, I2 = gu.shape
     if I2 % 2:
         _refuse(f"gu must have gate and up columns (got {I2})")
-    codes, scales, pc, ps = _rows_out(codes, scales, rows, I2 // 2, dev)
+    codes, scales, pc, ps = _rows_out(codes, scales, rows, I2 // 2, dev, stream)
     _run(lib.ft_moe_swiglu_fp8, dev, stream, gu.data_ptr(), rows, I2 // 2, pc, ps)
     return codes, scales
 
 
 def ft_moe_dispatch(x, ids, inv, E=None, slot_of_expert=None, x_sorted=None, stream=None):
     """Token rows [T][d] (bf16 or fp32) to their places in expert order [T*k][d]."""
-    dev = _first(x, "x", 2, _FLOATS)
+    dev = _first(x, "x", 2, _FLOATS, stream)
     T, d = x.shape
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
     if x_sorted is None:
-        x_sorted = _new((T * k, d), x.dtype, dev)
+        x_sorted = _new((T * k, d), x.dtype, dev, stream)
     out = _take(x_sorted, "x_sorted", (x.dtype,), (T * k, d), dev)
     _run(lib.ft_moe_dispatch, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if x.dtype is _F32 else 0)
     return x_sorted
@@ -161,10 +170,10 @@ def ft_moe_dispatch(x, ids, inv, E=None, slot_of_expert=None, x_sorted=None, str
 
 def ft_moe_dispatch_fp8(x, ids, inv, E=None, slot_of_expert=None, codes=None, scales=None, stream=None):
     """Token rows [T][d] (bf16 or fp32) to 8-bit rows in expert order: (codes [T*k][d], scales [T*k][S])."""
-    dev = _first(x, "x", 2, _FLOATS)
+    dev = _first(x, "x", 2, _FLOATS, stream)
     T, d = x.shape
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
-    codes, scales, pc, ps = _rows_out(codes, scales, T * k, d, dev)
+    codes, scales, pc, ps = _rows_out(codes, scales, T * k, d, dev, stream)
     _run(lib.ft_moe_dispatch_fp8, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, pc, ps,
          FT_ROWS_F32 if x.dtype is _F32 else 0)
     return codes, scales
@@ -172,12 +181,12 @@ def ft_moe_dispatch_fp8(x, ids, inv, E=None, slot_of_expert=None, codes=None, sc
 
 def ft_moe_dispatch_grad(dx_sorted, ids, inv, E=None, slot_of_expert=None, dx=None, stream=None):
     """Gradient of ft_moe_dispatch: the sum [T][d] of every token's rows of dx_sorted [T*k][d]."""
-    dev = _first(dx_sorted, "dx_sorted", 2, _FLOATS)
+    dev = _first(dx_sorted, "dx_sorted", 2, _FLOATS, stream)
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, None, dev)
     d = dx_sorted.shape[1]
     src = _take(dx_sorted, "dx_sorted", _FLOATS, (T * k, d), dev)
     if dx is None:
-        dx = _new((T, d), dx_sorted.dtype, dev)
+        dx = _new((T, d), dx_sorted.dtype, dev, stream)
     out = _take(dx, "dx", (dx_sorted.dtype,), (T, d), dev)
     _run(lib.ft_moe_dispatch_grad, dev, stream, src, pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if dx_sorted.dtype is _F32 else 0)
     return dx
@@ -187,17 +196,17 @@ def ft_moe_combine_grad(dout, y_sorted, ids, w, inv, E=None, slot_of_expert=None
                         want_dlogits: bool = True, stream=None):
     """Gradient of ft_moe_combine for dout [T][d] (fp32 or bf16): (dy_sorted bf16 [T*k][d], dw fp32 [T][k],
     dlogits fp32 [T][E] through the renormalised softmax of the chosen logits, or None)."""
-    dev = _first(dout, "dout", 2, _FLOATS)
+    dev = _first(dout, "dout", 2, _FLOATS, stream)
     T, d = dout.shape
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
     py = _take(y_sorted, "y_sorted", (_BF,), (T * k, d), dev)
     pw = _take(w, "w", (_F32,), (T, k), dev)
     if dy_sorted is None:
-        dy_sorted = _new((T * k, d), _BF, dev)
+        dy_sorted = _new((T * k, d), _BF, dev, stream)
     if dw is None:
-        dw = _new((T, k), _F32, dev)
+        dw = _new((T, k), _F32, dev, stream)
     if dlogits is None and want_dlogits:
-        dlogits = _new((T, E), _F32, dev)
+        dlogits = _new((T, E), _F32, dev, stream)
     pl = None if dlogits is None else _take(dlogits, "dlogits", (_F32,), (T, E), dev)
     _run(lib.ft_moe_combine_grad, dev, stream, dout.data_ptr(), py, pi, pw, pv, pt, T, E, k, d,
          _take(dy_sorted, "dy_sorted", (_BF,), (T * k, d), dev), _take(dw, "dw", (_F32,), (T, k), dev), pl,
@@ -205,18 +214,18 @@ def ft_moe_combine_grad(dout, y_sorted, ids, w, inv, E=None, slot_of_expert=None
     return dy_sorted, dw, dlogits
 
 
-def _product_out(out, out_dtype, shape, dev: int):
+def _product_out(out, out_dtype, shape, dev: int, stream):
     if out is None:
         if out_dtype not in _FLOATS:
             _refuse(f"out_dtype must be torch.bfloat16 or torch.float32 (got {out_dtype})")
-        out = _new(shape, out_dtype, dev)
+        out = _new(shape, out_dtype, dev, stream)
     return out, _take(out, "out", _FLOATS, shape, dev), FT_OUT_BF16 if out.dtype is _BF else 0
 
 
 def ft_moe_fp8_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """8-bit rows a [M][K] (scales [M][S]) times w [N][K] transposed (fp32 scales [ceil(N/128)][ceil(K/128)]):
     [M][N] in bf16, or in fp32 with out_dtype=torch.float32 (or an fp32 `out`)."""
-    dev = _first(a, "a", 2, _CODES)
+    dev = _first(a, "a", 2, _CODES, stream)
     M, K = a.shape
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         _refuse("w must be a tensor of shape [N, K]")
@@ -224,7 +233,7 @@ def ft_moe_fp8_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat
     psa = _take(a_scales, "a_scales", (_F32,), (M, _cols(K)), dev)
     pw = _take(w, "w", _CODES, (N, K), dev)
     psw = _take(w_scales, "w_scales", (_F32,), ((N + 127) // 128, (K + 127) // 128), dev)
-    out, po, flags = _product_out(out, out_dtype, (M, N), dev)
+    out, po, flags = _product_out(out, out_dtype, (M, N), dev, stream)
     _run(lib.ft_moe_fp8_matmul, dev, stream, a.data_ptr(), psa, M, pw, psw, N, K, po, flags)
     return out
 
@@ -234,7 +243,7 @@ def ft_moe_fp8_grouped_matmul(a, a_scales, w, w_scales, offsets, slot_of_expert,
     """8-bit rows a [P][K] in expert order, each expert's rows times its matrix of w [n_slots][N][K] transposed
     (fp32 scales [n_slots][ceil(N/128)][ceil(K/128)]): [P][N] in bf16 or fp32.  Rows of experts without a slot
     are left as they were (with out=None: unset)."""
-    dev = _first(a, "a", 2, _CODES)
+    dev = _first(a, "a", 2, _CODES, stream)
     P, K = a.shape
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         _refuse("w must be a tensor of shape [n_slots, N, K]")
@@ -245,7 +254,7 @@ def ft_moe_fp8_grouped_matmul(a, a_scales, w, w_scales, offsets, slot_of_expert,
     E = slot_of_expert.shape[0] if isinstance(slot_of_expert, torch.Tensor) and slot_of_expert.dim() == 1 else 0
     pt = _take(slot_of_expert, "slot_of_expert", (_I32,), (E,), dev)
     pf = _take(offsets, "offsets", (_I32,), (E + 1,), dev)
-    out, po, flags = _product_out(out, out_dtype, (P, N), dev)
+    out, po, flags = _product_out(out, out_dtype, (P, N), dev, stream)
     _run(lib.ft_moe_fp8_grouped_matmul, dev, stream, a.data_ptr(), psa, P, pw, psw, n_slots, N, K, pf, pt, E, po, flags)
     return out
 
@@ -259,7 +268,7 @@ class Fp8MoELayer:
     fp32 scales per 128 x 128 block (s13, s2); slot_of_expert int32 [E], -1 for experts that are not resident
     (left to the residual mask).  Every buffer is allocated here for a fixed (T, k): forward() allocates
     nothing and can be captured into a graph.  The accuracy is that of one e4m3 term per activation,
-    where MoELayer carries two."""
+    where MoELayer carries two.  One forward() at a time: its results and buffers are the next one's."""
 
     def __init__(self, w13, s13, w2, s2, slot_of_expert, k: int, T: int, out_bf16: bool = False):
         dev = _first(w13, "w13", 3, _CODES)
@@ -291,6 +300,8 @@ class Fp8MoELayer:
     def forward(self, logits, x, stream=None):
         """logits fp32 [T][E], x bf16 [T][d] -> (out [T][d], residual mask [T])."""
         dev, T, E, k = self.dev, self.T, self.E, self.k
+        if stream is not None and stream.device_index != dev:
+            _refuse(f"the stream is of cuda:{stream.device_index}, the layer is on cuda:{dev}")
         px = _take(x, "x", (_BF,), (T, self.d), dev)
         pl = _take(logits, "logits", (_F32,), (T, E), dev)
         if T == 0:

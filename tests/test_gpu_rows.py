@@ -560,3 +560,86 @@ def test_empty_calls_and_refused_tensors():
                  lambda: ft.ft_moe_fp8_grouped_matmul(a, sa, w[None], sw[None], ids.view(-1), z(4, dtype=i32))):
         with pytest.raises(ft.FtError):
             call()
+
+
+# tables of 1024 experts take 16 KiB of the LDS that the largest tiles would need
+MANY = [(40, 1024, 8, 700, 96, 4112), (1500, 1024, 8, 1024, 264, 144), (16000, 1024, 4, 1024, 200, 144), (16000, 1024, 8, 1000, 200, 144)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T, E, k, held, N, K", MANY)
+def test_grouped_product_of_many_experts(T, E, k, held, N, K, dtype):
+    g = gen(T + E)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(256)]).repeat((T + 255) // 256, 1)[:T]
+    offsets = torch.zeros(E + 1, dtype=torch.int32)
+    offsets[1:] = torch.bincount(ids.reshape(-1), minlength=E).cumsum(0)
+    slot = torch.full((E,), -1, dtype=torch.int32)
+    slot[torch.randperm(E, generator=g)[:held]] = torch.randperm(held, generator=g).to(torch.int32)
+    P = T * k
+    a, sa = ref.random_rows(g, P, K)
+    w, sw = ref.random_weights(g, held, N, K)
+    out = ft.ft_moe_fp8_grouped_matmul(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), offsets.cuda(), slot.cuda(),
+                                       out=filled(P, N, dtype=dtype)).cpu().double()
+    for e in range(0, E, 1 if P < 20000 else 29):
+        r0, r1, s = int(offsets[e]), int(offsets[e + 1]), int(slot[e])
+        if s < 0:
+            assert (out[r0:r1] == FILL).all()
+        elif r1 > r0:
+            want, mag = ref.product(a[r0:r1], sa[r0:r1], w[s], sw[s])
+            assert ((out[r0:r1] - want).abs() <= ref.product_bound(want, mag, K, dtype == BF)).all()
+
+
+@pytest.mark.parametrize("P, N, K", [(50, 64, 4112), (600, 200, 144), (3000, 600, 144)])
+def test_grouped_product_of_a_table_that_does_not_ascend(P, N, K):
+    """Every second expert has all rows: a row holds the result of one of them."""
+    g = gen(P)
+    E, n = 6, 3
+    a, sa = ref.random_rows(g, P, K)
+    w, sw = ref.random_weights(g, n, N, K)
+    offsets = torch.tensor([0, P, 0, P, 0, P, 0], dtype=torch.int32)
+    slot = torch.tensor([0, 0, 1, 0, 2, 0], dtype=torch.int32)
+    out = ft.ft_moe_fp8_grouped_matmul(a.cuda(), sa.cuda(), w.cuda(), sw.cuda(), offsets.cuda(), slot.cuda(), out_dtype=F32).cpu().double()
+    near = torch.zeros(P, N, dtype=torch.bool)
+    for s in range(n):
+        want, mag = ref.product(a, sa, w[s], sw[s])
+        near |= (out - want).abs() <= ref.product_bound(want, mag, K, False)
+    assert near.all()
+
+
+def test_streams_of_another_gpu_are_refused():
+    import types
+    other = types.SimpleNamespace(device_index=1, cuda_stream=0)
+    z = lambda *s, dtype=BF: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    x, ids, i1 = z(4, 64), z(4, 2, dtype=torch.int32), z(1, dtype=torch.int32)
+    a, sa, w, sw = z(4, 64, dtype=E4), z(4, 4, dtype=F32), z(64, 64, dtype=E4), z(1, 1, dtype=F32)
+    layer = ft.Fp8MoELayer(z(1, 64, 64, dtype=E4), z(1, 1, 1, dtype=F32), z(1, 64, 32, dtype=E4), z(1, 1, 1, dtype=F32), i1, 1, 4)
+    for call in (lambda: ft.ft_moe_quant_fp8(x, stream=other), lambda: ft.ft_moe_swiglu_fp8(x, stream=other),
+                 lambda: ft.ft_moe_dispatch(x, ids, ids, E=4, stream=other), lambda: ft.ft_moe_dispatch_fp8(x, ids, ids, E=4, stream=other),
+                 lambda: ft.ft_moe_dispatch_grad(z(8, 64), ids, ids, E=4, stream=other),
+                 lambda: ft.ft_moe_combine_grad(x, z(8, 64), ids, z(4, 2, dtype=F32), ids, E=4, stream=other),
+                 lambda: ft.ft_moe_fp8_matmul(a, sa, w, sw, stream=other),
+                 lambda: ft.ft_moe_fp8_grouped_matmul(a, sa, w[None], sw[None], z(2, dtype=torch.int32), i1, stream=other),
+                 lambda: layer.forward(z(4, 1, dtype=F32), x, stream=other)):
+        with pytest.raises(ft.FtError, match="stream"):
+            call()
+
+
+def test_outputs_made_for_another_stream_wait_for_nobody():
+    """Outputs of a call on a side stream come from that stream's memory: work of the current stream that still
+    writes a freed tensor of the same size cannot reach them."""
+    g = gen(6)
+    M, K = 2048, 2048
+    x = torch.randn(M, K, generator=g).to(BF).cuda()
+    want = ft.ft_moe_quant_fp8(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        busy = torch.randn(4096, 4096, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(4):
+            busy = busy @ busy * 1e-3
+        late = [torch.full((M, K), 1, dtype=torch.uint8, device="cuda"), torch.full((M, ref.cols(K)), 2.0, device="cuda")]
+        del late
+        got = ft.ft_moe_quant_fp8(x, stream=side)
+        torch.cuda.synchronize()
+        assert same_bits(got[0], want[0]) and same_bits(got[1], want[1])

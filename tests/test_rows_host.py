@@ -137,3 +137,15 @@ def test_reference_gradient_against_differences():
             v[0][t, j] += h
             v[1][t, j] -= h
             assert abs((loss(None, v[0]) - loss(None, v[1])) / (2 * h) - dw[t, j].item()) < 1e-8
+
+
+def test_sizes_that_a_launch_cannot_count():
+    err(L.ft_moe_quant_fp8(A, 1 << 27, 512, B, B, 0, None), ft.FT_E_UNSUPPORTED, "rows too large")
+    err(L.ft_moe_swiglu_fp8(A, 1 << 27, 16, B, B, None), ft.FT_E_UNSUPPORTED, "rows too large")
+    for name in ("dispatch", "dispatch_fp8", "dispatch_grad", "combine_grad"):
+        err(_one(name, T=1 << 26, d=1024, k=1), ft.FT_E_UNSUPPORTED, "T too large")
+    err(_one("combine_grad", T=1 << 24, d=8, k=1), ft.FT_E_UNSUPPORTED, "T too large")
+    # a table that does not ascend may give all rows to 512 of 1024 experts: more tiles than are counted
+    for flags in (0, ft.FT_OUT_BF16):
+        err(L.ft_moe_fp8_grouped_matmul(A, A, 1 << 30, A, A, 1, 1, 16, A, A, 1024, B, flags, None), ft.FT_E_UNSUPPORTED, "product too large")
+    err(L.ft_moe_fp8_matmul(A, A, 1 << 30, A, A, 1, 16, B, 0, None), ft.FT_E_UNSUPPORTED, "product too large")
