@@ -3,7 +3,11 @@
 //
 // All three move rows and are bound by HBM.  They work per token, not per sorted row: a token's row is
 // read once for its k copies (forward) and its k rows are summed in registers (gradient), so no atomics are
-// needed and every sum has a fixed order.  Rows are taken in pieces of 16 bytes a lane.
+// needed and every sum has a fixed order.  Rows are taken in pieces of 16 bytes a lane.  A wave moves 4 KiB: with 4 loads
+// in flight a lane, and with a block or more per compute unit from about 500 rows of 2048 on.  Measured:
+//   dispatch, 4096 rows of 7168 to 8 rows each: 529 MB in 106 us (5.0 TB/s; a 4 GiB copy reaches 4.9)
+//   its gradient, 1023 x 8 rows of 2048 in fp32: 75 MB in 12 us (6.1 TB/s)
+//   combine's gradient, 4096 tokens x 8 rows of 2048: 288 MB in 48 - 60 us; 8 tokens: 6.5 us
 #include "ft_device.h"
 #include "ft_rows.h"
 
@@ -138,8 +142,10 @@ __device__ __forceinline__ float wave_sums8(const float (&v)[8]) {
   return s;
 }
 
-// One block per token: dy rows, the k dot products dout . y, and the row of dlogits.  The pair tables are read once,
-// a lane per pair, beside the first piece of dout.
+// One block per token: dy rows, the k dot products dout . y, and the row of dlogits.  Eight pairs are taken together,
+// so dout is read once for k <= 8, and eight rows of y are in flight.  The pair tables are read once, a lane per pair,
+// beside the first piece of dout.  (With the tables read pair by pair, three dependent loads each, and every dot
+// product reduced alone, the kernel took 51 us instead of 48 for 4096 tokens and 8.6 instead of 6.5 for 8.)
 template <bool BF16>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const void* __restrict__ dout,
                                                            const uint16_t* __restrict__ y,

@@ -12,6 +12,11 @@
 //
 // In expert order a token's row is quantised once and its codes are stored at each of its k rows:
 // x is read once instead of k times.
+//
+// Bound by HBM; a few rows by the launch.  Eight lanes a block keep every access at 16 bytes a lane (32 read as bf16)
+// and the codes of a block on one 128-byte line, and a wave holds 8 blocks, so a single row of 7168 already takes 7
+// waves.  Measured: SwiGLU of 43541 rows, I = 2048, 449 MB in 80 us (5.6 TB/s; a 4 GiB copy reaches 4.9); 4096
+// rows of 2048 to 8 rows each, 86 MB in 15 us (5.8 TB/s); 16 rows of 7168 in 2.4 us.
 #include "ft_device.h"
 #include "ft_rows.h"
 

@@ -10,6 +10,15 @@
 // stages.  Rows are 128 bytes in LDS; their eight 16-byte chunks are permuted by a key of the row so that
 // the 16 lanes that read one chunk of 16 rows touch all banks.  The permutation is applied to the global
 // addresses, which stay inside the same 128 bytes.
+//
+// What bounds it: 8192 x 4096 x 7168 with 256 x 256 tiles takes 205 - 255 us (1.9 - 2.35 PFLOP/s; the clock falls to
+// about 1.5 GHz under it, and the time follows the clock the card gives).  Matrix instructions fill 58 - 65 % of
+// the cycles.  Of 244 us, leaving out the loads gave 202, the LDS reads 223, the fp32 multiply-adds 222: no single one
+// bounds it.  Registers only, the loop's matrix instructions with their multiply-adds run at 3.7 PFLOP/s.
+// A wave's 128 x 64 results (256 x 256 tiles) read 24 KB of LDS per 32 matrix instructions, 64 x 64 read 16 KB per 16:
+// larger tiles a wave need more than the 256 registers that two waves a SIMD have.
+//
+// Exact products (WIDE) convert codes to bf16 and take twice the matrix cycles: 8192 x 4096 x 7168 in 450 us.
 #pragma once
 #include <type_traits>
 
