@@ -205,23 +205,32 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_tile_kernel(Fp8MatmulArgs a) {
 }
 
 template <class C, bool BF16>
-hipError_t launch_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
+hipError_t launch_dense_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
   static LaunchCache cache;
   LaunchFacts f;
   const long long ntn = (a.N + C::BN - 1) / C::BN, ntm = (a.M + C::BM - 1) / C::BM;
-  if (a.E == 0) {
-    hipError_t e = cache.get((const void*)fp8_tile_kernel<C, BF16, false>, C::NT, C::LDS, &f);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((fp8_tile_kernel<C, BF16, false>), dim3((uint32_t)((ntn * ntm + 7) / 8 * 8)), dim3(C::NT), C::LDS, s, a);
-    return hipGetLastError();
-  }
-  static LaunchCache gcache;
+  hipError_t e = cache.get((const void*)fp8_tile_kernel<C, BF16, false>, C::NT, C::LDS, &f);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((fp8_tile_kernel<C, BF16, false>), dim3((uint32_t)((ntn * ntm + 7) / 8 * 8)), dim3(C::NT), C::LDS, s, a);
+  return hipGetLastError();
+}
+
+template <class C, bool BF16>
+hipError_t launch_grouped_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
+  static LaunchCache cache;
+  LaunchFacts f;
+  const long long ntn = (a.N + C::BN - 1) / C::BN, ntm = (a.M + C::BM - 1) / C::BM;
   const size_t lds = C::LDS + group_lds_bytes(a.E);
-  hipError_t e = gcache.get((const void*)fp8_tile_kernel<C, BF16, true>, C::NT, lds, &f);
+  hipError_t e = cache.get((const void*)fp8_tile_kernel<C, BF16, true>, C::NT, lds, &f);
   if (e != hipSuccess) return e;
   const long long upper = ((ntm + (a.E < a.M ? a.E : a.M)) * ntn + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
   hipLaunchKernelGGL((fp8_tile_kernel<C, BF16, true>), dim3((uint32_t)(upper < most ? upper : most)), dim3(C::NT), lds, s, a);
   return hipGetLastError();
+}
+
+template <class C, bool BF16>
+hipError_t launch_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
+  return a.E == 0 ? launch_dense_tiles<C, BF16>(a, s) : launch_grouped_tiles<C, BF16>(a, s);
 }
 
 // Which kernel: the one whose blocks, taken in rounds of the 256 compute units (or as many times that as fit),
@@ -235,10 +244,17 @@ hipError_t launch_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
 //   128x128     -      43     43     43     43     43     49     368
 //   128x256     -      47     48     49     49     50     -      263 - 311
 //   256x256     -      -      -      71     74     74     -      206 - 249
-// and fp32 results:  16x32 88 at 256 rows, 64x64 19.3 / 21.7 / 73 at 64 / 256 / 1024, 128x128 64 / 66 / 71 and 450 at 8192.
+// and fp32 results:  16x32 88 at 256 rows, 64x64 19.3 / 21.7 / 73 at 64 / 256 / 1024, 128x128 64 / 66 / 71 and 434 - 505 at 8192
+// (128x256 449 - 516).  By expert, `group` where rounds follow each other, `light` where a group fills half a tile or less (waves
+// without rows wait only; bound by the weights' bytes).  fp32 results, 128 experts of 1536 x 2048, top 8, us for T tokens:
+//   T           4      16     64     256    1024        top 8 of 256, 96 held, 4096 x 7168:  T   64     256    1024   8192
+//   16x32       21.5   49.8   81.7   122    362                                                  427    552    1433   -
+//   64x64       29.5   70.3   108    110    160                                                  512    574    620    -
+//   128x128     32.9   60.3   92.3   93.8   109                                                  573    590    607    1880
+//   128x256     24.4   46.5   80.1   84.7   112                                                  466    493    515    1765
 struct Choice {
   int rows, cols, per;
-  float step, full;
+  float step, full, group, light;
   int lds;  // of the tiles kernels, 0 for the others
 };
 using Solo = TileCfg<64, 64, 1, 1, 2, false, 4>;
@@ -248,18 +264,21 @@ using T128 = TileCfg<128, 128, 2, 2, 4, false>;
 using T128x256 = TileCfg<128, 256, 2, 4, 3, false>;
 using T256 = TileCfg<256, 256, 2, 4, 2, false>;
 using TWide = TileCfg<128, 128, 2, 2, 2, true>;
+using TWide256 = TileCfg<128, 256, 2, 4, 3, true>;  // by expert only
 constexpr int kLds = 160 * 1024;  // of a compute unit
-constexpr Choice kBf16[] = {{16, 16, 1, 0.18f, 0.18f, 0},
-                            {16, 32, 1, 0.26f, 0.26f, 0},
-                            {64, 64, 1, 0.29f, 0.32f, Solo::LDS},
-                            {64, 128, 2, 0.71f, 0.86f, T64::LDS},
-                            {128, 128, 1, 0.78f, 0.82f, T128::LDS},
-                            {128, 256, 1, 0.88f, 1.25f, T128x256::LDS},
-                            {256, 256, 1, 1.3f, 2.2f, T256::LDS}};
-constexpr Choice kF32[] = {{16, 16, 1, 0.18f, 0.18f, 0},
-                           {16, 32, 1, 0.26f, 0.26f, 0},
-                           {64, 64, 1, 0.35f, 0.33f, SoloWide::LDS},
-                           {128, 128, 2, 1.2f, 2.0f, TWide::LDS}};
+constexpr float kNever = 1e30f;
+constexpr Choice kBf16[] = {{16, 16, 1, 0.18f, 0.18f, 0.18f, 0.18f, 0},
+                            {16, 32, 1, 0.26f, 0.26f, 0.26f, 0.26f, 0},
+                            {64, 64, 1, 0.29f, 0.32f, 0.32f, 0.32f, Solo::LDS},
+                            {64, 128, 2, 0.71f, 0.86f, 0.86f, 0.86f, T64::LDS},
+                            {128, 128, 1, 0.78f, 0.82f, 0.82f, 0.82f, T128::LDS},
+                            {128, 256, 1, 0.88f, 1.25f, 1.25f, 1.25f, T128x256::LDS},
+                            {256, 256, 1, 1.3f, 2.2f, 2.2f, 2.2f, T256::LDS}};
+constexpr Choice kF32[] = {{16, 16, 1, 0.18f, 0.18f, 0.18f, 0.18f, 0},
+                           {16, 32, 1, 0.26f, 0.26f, 0.19f, 0.19f, 0},
+                           {64, 64, 1, 0.35f, 0.33f, 0.5f, 0.46f, SoloWide::LDS},
+                           {128, 128, 2, 1.2f, 2.0f, 2.15f, 1.7f, TWide::LDS},
+                           {128, 256, 1, 1.5f, kNever, 1.95f, 1.45f, TWide256::LDS}};
 
 // Rows with a slot and groups that have any, where only the device knows: as if experts were drawn evenly.
 struct Spread {
@@ -270,8 +289,6 @@ Spread spread(const Fp8MatmulArgs& a) {
   return {std::max(1.0, held * a.M), std::max(1.0, held * a.E * (1.0 - std::exp(-(double)a.M / a.E)))};
 }
 
-constexpr double kNever = 1e30;
-
 double cost(const Choice& c, const Fp8MatmulArgs& a) {
   if (c.lds + (a.E > 0 ? group_lds_bytes(a.E) : 0) > kLds) return kNever;
   // Counts that have to fit: the threads of a dense launch (at most 512 a block) in 32 bits, the tiles of all groups
@@ -280,13 +297,14 @@ double cost(const Choice& c, const Fp8MatmulArgs& a) {
   if (a.E == 0 ? ((a.M + c.rows - 1) / c.rows) * ntn >= 1 << 23
                : (a.M / c.rows + 2.0) * (a.E / 2 + 1) * ntn >= 2147483648.0)
     return kNever;
-  double chunks = (a.M + c.rows - 1) / c.rows;
+  double chunks = (a.M + c.rows - 1) / c.rows, round = c.full;
   if (a.E > 0) {  // each group has half a chunk to spare
     const Spread p = spread(a);
     chunks = std::max(p.groups, p.rows / c.rows + 0.5 * p.groups);
+    round = 2 * p.rows <= c.rows * p.groups ? c.light : c.group;
   }
   const double blocks = chunks * ntn;
-  return blocks <= 256 ? c.step : std::ceil(blocks / (256.0 * c.per)) * c.full;
+  return blocks <= 256 && round < kNever ? c.step : std::ceil(blocks / (256.0 * c.per)) * round;
 }
 
 // -1: none fits
@@ -316,7 +334,8 @@ hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
       case 0: return launch_rows<1, false>(a, s);
       case 1: return launch_rows<2, false>(a, s);
       case 2: return launch_tiles<SoloWide, false>(a, s);
-      default: return launch_tiles<TWide, false>(a, s);
+      case 3: return launch_tiles<TWide, false>(a, s);
+      default: return launch_grouped_tiles<TWide256, false>(a, s);
     }
   }
   switch (choose<true>(a)) {
