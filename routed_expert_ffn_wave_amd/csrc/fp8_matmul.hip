@@ -235,23 +235,38 @@ hipError_t launch_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
 
 // Which kernel: the one whose blocks, taken in rounds of the 256 compute units (or as many times that as fit),
 // are through first.  `step` is the measured time of one 128-block of K in a round, in us on an MI355X; `full`
-// where rounds follow each other.  M rows x 4096 columns, K = 7168, us a call (bf16 results):
-//   M           16     32     64     128    256    512    1024   8192
-//   16x16       10.2   18.3   34     65     -      -      -      -
-//   16x32       14.0   13.4   24     46     88     -      -      -
-//   64x64       15.3   15.1   15.9   18.2   19.1   35.7   68.8   533
-//   64x128      -      39     39     39     40     41     -      384
-//   128x128     -      43     43     43     43     43     49     368
-//   128x256     -      47     48     49     49     50     -      263 - 311
-//   256x256     -      -      -      71     74     74     -      206 - 249
-// and fp32 results:  16x32 88 at 256 rows, 64x64 19.3 / 21.7 / 73 at 64 / 256 / 1024, 128x128 64 / 66 / 71 and 434 - 505 at 8192
-// (128x256 449 - 516).  By expert, `group` where rounds follow each other, `light` where a group fills half a tile or less (waves
-// without rows wait only; bound by the weights' bytes).  fp32 results, 128 experts of 1536 x 2048, top 8, us for T tokens:
-//   T           4      16     64     256    1024        top 8 of 256, 96 held, 4096 x 7168:  T   64     256    1024   8192
-//   16x32       21.5   49.8   81.7   122    362                                                  427    552    1433   -
-//   64x64       29.5   70.3   108    110    160                                                  512    574    620    -
-//   128x128     32.9   60.3   92.3   93.8   109                                                  573    590    607    1880
-//   128x256     24.4   46.5   80.1   84.7   112                                                  466    493    515    1765
+// where rounds follow each other.  M rows x 4096 columns, K = 7168, us a call (bf16 results; / 2, / 4: that many shares of K):
+//   M             16     32     64     128    256    512    1024   2048   4096   8192
+//   16x16         10.2   18.3   34     65     -      -      -      -      -      -
+//   16x32         14.0   13.4   24     46     88     -      -      -      -      -
+//   64x64 / 4     15.3   15.1   16.1   18.5   19.3   34.8   67     131    261    533
+//   64x128 / 2    -      -      25     25     26     27     50     98     194    -
+//   128x128 / 2   -      -      -      36     36     36     38     75     147    -
+//   128x256       -      47     48     49     49     50     50     60     117    263 - 311
+//   256x256       -      -      -      71     74     75     75     79     99     206 - 249
+// and fp32 results:
+//   16x32         -      -      -      -      88     -      -      -      -      -
+//   64x64 / 4     -      -      20     21     23     44     81     153    -      -
+//   128x128 / 2   -      -      53     55     56     58     62     121    -      -
+//   128x128       -      -      64     65     67     71     72     117    -      434 - 505
+// A block alone on its compute unit waits for its loads: two shares of K, each with stages and waves of its own, keep twice as many in
+// flight (64x128 and 128x128 without: 41 and 45 at 256 rows).  By expert the unshared tiles serve better, two or more to a
+// compute unit (64 tokens below: 74 us for 64x128 against 83 with shares).
+//
+// By expert, `group` where rounds follow each other, `light` where a group fills half a tile or less (waves
+// without rows wait only; bound by the weights' bytes).  us for T tokens, top 8:
+//   128 experts of 1536 x 2048, T =  4      16     64     256    1024     256 experts, 96 held, of 4096 x 7168, T =  64     256    1024   8192
+//   16x32                            21.4   50.7   83     125    362                                                 427    549    1430   -
+//   64x64 / 4                        25     63     102    105    149                                                 504    552    588    -
+//   64x128                           20.9   43.6   74     77     104                                                 433    471    509    1747
+//   128x128                          28.8   54.2   85     87     98                                                  437    484    497    1331
+//   128x256                          18.9   42.7   75     78     90                                                  428    464    482    1066
+//   256x256                          23.3   52.7   89     90     101                                                 530    558    578    1062
+// and fp32 results:
+//   16x32                            21.5   49.8   82     122    362                                                 427    552    1433   -
+//   64x64 / 4                        29.5   70.3   108    110    160                                                 512    574    620    -
+//   128x128                          32.9   60.3   92     94     109                                                 573    590    607    1880
+//   128x256                          24.4   46.5   80     85     112                                                 466    493    515    1765
 struct Choice {
   int rows, cols, per;
   float step, full, group, light;
@@ -259,8 +274,11 @@ struct Choice {
 };
 using Solo = TileCfg<64, 64, 1, 1, 2, false, 4>;
 using SoloWide = TileCfg<64, 64, 1, 1, 2, true, 4>;
-using T64 = TileCfg<64, 128, 1, 2, 3, false>;
-using T128 = TileCfg<128, 128, 2, 2, 4, false>;
+using Pair64 = TileCfg<64, 128, 1, 2, 3, false, 2>;    // dense only, as kNever says
+using Pair128 = TileCfg<128, 128, 2, 2, 2, false, 2>;  // dense only
+using PairWide = TileCfg<128, 128, 2, 2, 2, true, 2>;  // dense only
+using T64 = TileCfg<64, 128, 1, 2, 3, false>;          // by expert only
+using T128 = TileCfg<128, 128, 2, 2, 4, false>;        // by expert only
 using T128x256 = TileCfg<128, 256, 2, 4, 3, false>;
 using T256 = TileCfg<256, 256, 2, 4, 2, false>;
 using TWide = TileCfg<128, 128, 2, 2, 2, true>;
@@ -269,14 +287,17 @@ constexpr int kLds = 160 * 1024;  // of a compute unit
 constexpr float kNever = 1e30f;
 constexpr Choice kBf16[] = {{16, 16, 1, 0.18f, 0.18f, 0.18f, 0.18f, 0},
                             {16, 32, 1, 0.26f, 0.26f, 0.26f, 0.26f, 0},
-                            {64, 64, 1, 0.29f, 0.32f, 0.32f, 0.32f, Solo::LDS},
-                            {64, 128, 2, 0.71f, 0.86f, 0.86f, 0.86f, T64::LDS},
-                            {128, 128, 1, 0.78f, 0.82f, 0.82f, 0.82f, T128::LDS},
-                            {128, 256, 1, 0.88f, 1.25f, 1.25f, 1.25f, T128x256::LDS},
-                            {256, 256, 1, 1.3f, 2.2f, 2.2f, 2.2f, T256::LDS}};
+                            {64, 64, 1, 0.33f, 0.31f, 0.32f, 0.32f, Solo::LDS},
+                            {64, 128, 1, 0.48f, 0.44f, kNever, kNever, Pair64::LDS},
+                            {128, 128, 1, 0.66f, 0.66f, kNever, kNever, Pair128::LDS},
+                            {64, 128, 2, 0.71f, kNever, 0.86f, 0.86f, T64::LDS},
+                            {128, 128, 1, 0.78f, kNever, 0.82f, 0.82f, T128::LDS},
+                            {128, 256, 1, 0.93f, 1.15f, 1.25f, 1.25f, T128x256::LDS},
+                            {256, 256, 1, 1.4f, 2.0f, 2.2f, 2.2f, T256::LDS}};
 constexpr Choice kF32[] = {{16, 16, 1, 0.18f, 0.18f, 0.18f, 0.18f, 0},
                            {16, 32, 1, 0.26f, 0.26f, 0.19f, 0.19f, 0},
-                           {64, 64, 1, 0.35f, 0.33f, 0.5f, 0.46f, SoloWide::LDS},
+                           {64, 64, 1, 0.37f, 0.36f, 0.5f, 0.46f, SoloWide::LDS},
+                           {128, 128, 1, 1.05f, 1.08f, kNever, kNever, PairWide::LDS},
                            {128, 128, 2, 1.2f, 2.0f, 2.15f, 1.7f, TWide::LDS},
                            {128, 256, 1, 1.5f, kNever, 1.95f, 1.45f, TWide256::LDS}};
 
@@ -334,7 +355,8 @@ hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
       case 0: return launch_rows<1, false>(a, s);
       case 1: return launch_rows<2, false>(a, s);
       case 2: return launch_tiles<SoloWide, false>(a, s);
-      case 3: return launch_tiles<TWide, false>(a, s);
+      case 3: return launch_dense_tiles<PairWide, false>(a, s);
+      case 4: return launch_tiles<TWide, false>(a, s);
       default: return launch_grouped_tiles<TWide256, false>(a, s);
     }
   }
@@ -343,9 +365,11 @@ hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
     case 0: return launch_rows<1, true>(a, s);
     case 1: return launch_rows<2, true>(a, s);
     case 2: return launch_tiles<Solo, true>(a, s);
-    case 3: return launch_tiles<T64, true>(a, s);
-    case 4: return launch_tiles<T128, true>(a, s);
-    case 5: return launch_tiles<T128x256, true>(a, s);
+    case 3: return launch_dense_tiles<Pair64, true>(a, s);
+    case 4: return launch_dense_tiles<Pair128, true>(a, s);
+    case 5: return launch_grouped_tiles<T64, true>(a, s);
+    case 6: return launch_grouped_tiles<T128, true>(a, s);
+    case 7: return launch_tiles<T128x256, true>(a, s);
     default: return launch_tiles<T256, true>(a, s);
   }
 }

@@ -58,8 +58,8 @@ template <int BM_, int BN_, int WM_, int WN_, int NS_, bool WIDE_, int KG_ = 1>
 struct TileCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;  // NS: stages in LDS
   static constexpr bool WIDE = WIDE_;  // codes widened to bf16 (exact products), else 8-bit matrix instructions
-  // KG > 1: the block is KG single waves, each with the whole tile, a share of K and stages of its own; they run
-  // without barriers and their results are added at the end, in the order of K.
+  // KG > 1: the block is KG groups of waves, each with the whole tile, a share of K and stages of its own; their
+  // results are added at the end, in the order of K.  Groups of one wave run without barriers.
   static constexpr int KG = KG_, GW = WM * WN;  // waves of a group
   static constexpr int NT = 64 * GW * KG;
   static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;  // fragments of a wave
@@ -71,7 +71,7 @@ struct TileCfg {
   static constexpr int GROUP = SW + 2 * 256, LDS = KG * GROUP;
   static constexpr int PITCH = BN + 4;           // floats of a row of results in LDS (KG > 1), over the stages
   static_assert(BM % RQ == 0 && BN % RQ == 0 && BM % 64 == 0 && (BM / 64 < GW || (BM == 64 && GW == 1)), "load passes");
-  static_assert(KG == 1 || (GW == 1 && BM == 64 && BN == 64 && BM * PITCH * 4 <= GROUP), "single waves share K");
+  static_assert(KG == 1 || BM * PITCH * 4 <= GROUP, "a group's results lie over its stages");
   static_assert(NS >= 2 && NS <= 4, "the scales of 4 steps are held twice");
   static_assert(NF == 4 && 128 % (BN / WN) == 0, "a wave's 64 weight rows share one scale");
 };
@@ -203,6 +203,12 @@ __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& 
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if constexpr (C::GW > 1) asm volatile("s_barrier" ::: "memory");
     }
+  };
+
+  // Groups of several waves share the block's barrier: each passes it as often as the one with most to do.
+  auto even_out = [&] {
+    if constexpr (C::KG > 1 && C::GW > 1)
+      for (int i = b1 - b0 + (b0 <= nfull && nfull < b1); i < (nb + C::KG - 1) / C::KG + (nfull < nb); ++i) asm volatile("s_barrier" ::: "memory");
   };
 
   if (C::KG > 1 && b0 == b1) {
@@ -382,11 +388,13 @@ __device__ __forceinline__ void fp8_tile(const Fp8MatmulArgs& a, const TileJob& 
   } else {
     // every wave's results over its own stages, then the sums in the order of K
     float* mine = (float*)lds;
+    even_out();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if constexpr (C::GW > 1) asm volatile("s_barrier" ::: "memory");
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
-      for (int f = 0; f < NF; ++f) *(f32x4*)(mine + (16 * m + r) * C::PITCH + 16 * g + 4 * f) = acc[m][f];
+      for (int f = 0; f < NF; ++f) *(f32x4*)(mine + (arow + 16 * m) * C::PITCH + wn * 16 * NF + 16 * g + 4 * f) = acc[m][f];
     __syncthreads();
     for (int i = threadIdx.x; i < C::BM * C::BN / 16; i += C::NT) {
       const int row = i / (C::BN / 16), n = i % (C::BN / 16) * 16;

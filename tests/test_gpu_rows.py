@@ -643,3 +643,14 @@ def test_outputs_made_for_another_stream_wait_for_nobody():
         got = ft.ft_moe_quant_fp8(x, stream=side)
         torch.cuda.synchronize()
         assert same_bits(got[0], want[0]) and same_bits(got[1], want[1])
+
+
+# sizes where blocks share K between groups of waves: shares of no, one and several blocks, with and without a short one
+SHARED = [(400, 4100, 16), (400, 4100, 128), (400, 4100, 144), (390, 4100, 256), (400, 4100, 400), (400, 4090, 1040), (1000, 4096, 16),
+          (1000, 4096, 272), (970, 4090, 384), (1000, 4096, 656)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M, N, K", SHARED)
+def test_product_with_shares_of_k(M, N, K, dtype):
+    test_product(M, N, K, dtype)
