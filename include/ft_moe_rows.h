@@ -102,7 +102,7 @@ int ft_moe_combine_grad(const void* dout, const uint16_t* y_sorted, const int32_
  * With fp32 results the code products of a block are exact and are added in fp32.  With FT_OUT_BF16 and
  * more than a few rows they are added by the 8-bit matrix instructions, which cut each product in a group of 8 at
  * 2^-13 of the group's largest before adding: at most 7 * 2^-13 of the sum of the products' magnitudes, and
- * about 1.3e-5 of the result's norm for normally distributed values, under the 2^-9 of bf16's own rounding.
+ * about 1.3e-5 of the result's norm for normally distributed values, under the 2^-8 that bf16 rounds to.
  * A gradient with respect to the rows is the same call with the transposed codes and scales.
  */
 int ft_moe_fp8_matmul(const uint8_t* a, const float* a_scales, int M, const uint8_t* w, const float* w_scales, int N,
