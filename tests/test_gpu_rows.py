@@ -654,3 +654,41 @@ SHARED = [(400, 4100, 16), (400, 4100, 128), (400, 4100, 144), (390, 4100, 256),
 @pytest.mark.parametrize("M, N, K", SHARED)
 def test_product_with_shares_of_k(M, N, K, dtype):
     test_product(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("P, N, K", [(3, 128, 256), (90, 272, 400), (700, 1040, 528)])
+def test_gradient_of_the_rows_is_the_product_with_the_transposed_matrix(P, N, K):
+    """For out = rows . w^T and a gradient in 8-bit rows g: d rows = g . w, dense and by expert, against the formula's own
+    gradient and against differences (out is linear: exact up to the products' roundings)."""
+    g = gen(P + N)
+    E = 3
+    w, sw = ref.random_weights(g, E, N, K)
+    wt, swt = w.view(torch.uint8).transpose(1, 2).contiguous().view(E4), sw.transpose(1, 2).contiguous()
+    dout, sd = ref.random_rows(g, P, N)
+    cut = P // 3
+    offsets = torch.tensor([0, cut, cut, P], dtype=torch.int32)
+    slot = torch.tensor([2, 1, 0], dtype=torch.int32)
+    dense = ft.ft_moe_fp8_matmul(dout.cuda(), sd.cuda(), wt[1].cuda(), swt[1].cuda(), out_dtype=F32).cpu().double()
+    by = ft.ft_moe_fp8_grouped_matmul(dout.cuda(), sd.cuda(), wt.cuda(), swt.cuda(), offsets.cuda(), slot.cuda(), out_dtype=F32).cpu().double()
+    a, sa = ref.random_rows(g, P, K)
+    dy = ref.values(dout, sd)
+    for got, parts in ((dense, [(0, P, 1)]), (by, [(0, cut, 2), (cut, P, 0)])):
+        for lo, hi, s in parts:
+            if lo == hi:
+                continue
+            x = ref.values(a[lo:hi], sa[lo:hi]).requires_grad_()
+            y = ref.weight_values(w[s], sw[s])
+            ((x @ y.t()) * dy[lo:hi]).sum().backward()
+            want, mag = ref.product(dout[lo:hi], sd[lo:hi], wt[s], swt[s])
+            bound = ref.product_bound(want, mag, N, False)
+            assert ((got[lo:hi] - x.grad).abs() <= bound).all()
+            # differences between these rows and others
+            b, sb = ref.random_rows(g, hi - lo, K)
+            up, mu = ref.product(b, sb, w[s], sw[s])
+            dn, md = ref.product(a[lo:hi], sa[lo:hi], w[s], sw[s])
+            o = [ft.ft_moe_fp8_matmul(c.cuda(), sc.cuda(), w[s].cuda(), sw[s].cuda(), out_dtype=F32).cpu().double()
+                 for c, sc in ((b, sb), (a[lo:hi].contiguous(), sa[lo:hi].contiguous()))]
+            step = ref.values(b, sb) - x.detach()
+            slack = ((ref.product_bound(up, mu, K, False) + ref.product_bound(dn, md, K, False)) * dy[lo:hi].abs()).sum(1)
+            lhs, rhs = ((o[0] - o[1]) * dy[lo:hi]).sum(1), (got[lo:hi] * step).sum(1)
+            assert ((lhs - rhs).abs() <= slack + (bound * step.abs()).sum(1)).all()
