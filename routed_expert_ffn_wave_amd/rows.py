@@ -5,7 +5,8 @@ The functions carry the C ABI's names.  Unlike the C calls they see the tensors'
 refuse (FtError, FT_E_INVAL) a tensor of another type, shape, device or layout than the call reads.
 Work is enqueued on the current stream of the tensors' device, or on `stream` (a stream of that device);
 outputs that are not given come from that stream's memory, and a tensor that other streams use too is the
-caller's to order and to keep (Tensor.record_stream), as with any work of torch's.  8-bit codes are
+caller's to order and to keep (Tensor.record_stream), as with any work of torch's.  The calls are not
+recorded by autograd: the gradients are calls of their own.  8-bit codes are
 torch.float8_e4m3fn tensors (uint8 is taken too)."""
 from __future__ import annotations
 
@@ -115,6 +116,8 @@ def _pairs(ids, inv, slot_of_expert, E, T, dev: int):
         E = n
     elif E is None:
         _refuse("E is needed when slot_of_expert is not given")
+    if E < 1:
+        _refuse(f"E must be >= 1 (got {E})")
     return pi, pv, ps, T, E, k
 
 
@@ -280,8 +283,9 @@ class Fp8MoELayer:
         _take(s2, "s2", (_F32,), (self.n_slots, nb(self.d), nb(self.I)), dev)
         _first(slot_of_expert, "slot_of_expert", 1, (_I32,))
         _take(slot_of_expert, "slot_of_expert", (_I32,), slot_of_expert.shape, dev)
-        if T < 0 or I2 % 2 or not 1 <= k <= min(slot_of_expert.shape[0], 32):
-            _refuse(f"invalid layer shape T={T}, k={k}, E={slot_of_expert.shape[0]}, w13 rows={I2}")
+        E = slot_of_expert.shape[0]
+        if T < 0 or T * k > 1 << 30 or I2 % 32 or self.d % 16 or self.d * self.I == 0 or self.n_slots < 1 or E > 1024 or not 1 <= k <= min(E, 32):
+            _refuse(f"invalid layer shape T={T}, k={k}, E={E}, d={self.d}, w13 rows={I2}, slots={self.n_slots}")
         self.dev = dev
         self.w13, self.s13, self.w2, self.s2, self.slot_of = w13, s13, w2, s2, slot_of_expert
         self.E, self.k, self.T, self.flags = slot_of_expert.shape[0], k, T, FT_OUT_BF16 if out_bf16 else 0

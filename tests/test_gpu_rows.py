@@ -692,3 +692,21 @@ def test_gradient_of_the_rows_is_the_product_with_the_transposed_matrix(P, N, K)
             slack = ((ref.product_bound(up, mu, K, False) + ref.product_bound(dn, md, K, False)) * dy[lo:hi].abs()).sum(1)
             lhs, rhs = ((o[0] - o[1]) * dy[lo:hi]).sum(1), (got[lo:hi] * step).sum(1)
             assert ((lhs - rhs).abs() <= slack + (bound * step.abs()).sum(1)).all()
+
+
+def test_refusals_before_anything_is_allocated():
+    z = lambda *s, dtype=BF: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    x, ids = z(4, 64), z(4, 2, dtype=torch.int32)
+    for E in (0, -1):
+        with pytest.raises(ft.FtError, match="E must be"):
+            ft.ft_moe_combine_grad(x, z(8, 64), ids, z(4, 2, dtype=F32), ids, E=E)
+
+    def layer(d=64, I=32, E=4, k=2, T=4, n=2):
+        nb = lambda v: (v + 127) // 128  # noqa: E731
+        return ft.Fp8MoELayer(z(n, 2 * I, d, dtype=E4), z(n, nb(2 * I), nb(d), dtype=F32), z(n, d, I, dtype=E4), z(n, nb(d), nb(I), dtype=F32),
+                              z(E, dtype=torch.int32), k, T)
+
+    layer()
+    for kw in (dict(d=24), dict(I=8), dict(E=1025), dict(k=5), dict(k=0), dict(T=-1), dict(n=0), dict(d=0), dict(E=64, k=33)):
+        with pytest.raises(ft.FtError, match="invalid layer shape"):
+            layer(**kw)

@@ -149,3 +149,7 @@ def test_sizes_that_a_launch_cannot_count():
     for flags in (0, ft.FT_OUT_BF16):
         err(L.ft_moe_fp8_grouped_matmul(A, A, 1 << 30, A, A, 1, 1, 16, A, A, 1024, B, flags, None), ft.FT_E_UNSUPPORTED, "product too large")
     err(L.ft_moe_fp8_matmul(A, A, 1 << 30, A, A, 1, 16, B, 0, None), ft.FT_E_UNSUPPORTED, "product too large")
+
+
+def test_scale_cols_of_the_largest_size():
+    assert ft.ft_moe_fp8_scale_cols(2 ** 31 - 1) == 4 * 2 ** 22
