@@ -250,8 +250,8 @@ hipError_t launch_tiles(const Fp8MatmulArgs& a, hipStream_t s) {
 //   128x128 / 2   -      -      53     55     56     58     62     121    -      -
 //   128x128       -      -      64     65     67     71     72     117    -      434 - 505
 // A block alone on its compute unit waits for its loads: two shares of K, each with stages and waves of its own, keep twice as many in
-// flight (64x128 and 128x128 without: 41 and 45 at 256 rows).  By expert the unshared tiles serve better, two or more to a
-// compute unit (64 tokens below: 74 us for 64x128 against 83 with shares).
+// flight (64x128 and 128x128 without: 41 and 45 at 256 rows).  By expert, where tiles follow each other, the unshared
+// ones serve better (64 tokens below: 74 us for 64x128 against 83 with shares).
 //
 // By expert, `group` where rounds follow each other, `light` where a group fills half a tile or less (waves
 // without rows wait only; bound by the weights' bytes).  us for T tokens, top 8:
