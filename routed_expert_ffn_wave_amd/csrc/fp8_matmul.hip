@@ -290,9 +290,9 @@ constexpr Choice kBf16[] = {{16, 16, 1, 0.18f, 0.18f, 0.18f, 0.18f, 0},
                             {64, 64, 1, 0.33f, 0.31f, 0.32f, 0.32f, Solo::LDS},
                             {64, 128, 1, 0.48f, 0.44f, kNever, kNever, Pair64::LDS},
                             {128, 128, 1, 0.66f, 0.66f, kNever, kNever, Pair128::LDS},
-                            {64, 128, 2, 0.71f, kNever, 0.86f, 0.86f, T64::LDS},
+                            {64, 128, 2, 0.71f, kNever, 0.95f, 0.95f, T64::LDS},
                             {128, 128, 1, 0.78f, kNever, 0.82f, 0.82f, T128::LDS},
-                            {128, 256, 1, 0.93f, 1.15f, 1.25f, 1.25f, T128x256::LDS},
+                            {128, 256, 1, 0.93f, 1.15f, 1.25f, 0.85f, T128x256::LDS},
                             {256, 256, 1, 1.4f, 2.0f, 2.2f, 2.2f, T256::LDS}};
 constexpr Choice kF32[] = {{16, 16, 1, 0.18f, 0.18f, 0.18f, 0.18f, 0},
                            {16, 32, 1, 0.26f, 0.26f, 0.19f, 0.19f, 0},
