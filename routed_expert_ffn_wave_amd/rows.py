@@ -39,6 +39,7 @@ EXPORTED_ROWS = tuple(_SIG)
 _E4, _U8, _BF, _F32, _I32 = torch.float8_e4m3fn, torch.uint8, torch.bfloat16, torch.float32, torch.int32
 _CODES = (_E4, _U8)
 _FLOATS = (_BF, _F32)
+_INTS = (_I32,)
 
 # Calls of a few microseconds: the stream handle and the current device are asked for without building objects.
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -49,27 +50,30 @@ def _refuse(text: str):
     raise FtError(FT_E_INVAL, text)
 
 
-def _first(t, name: str, dims: int, dtypes, stream=None) -> int:
-    """Checks a call's first tensor, whose sizes the others follow, and its stream; returns the tensor's GPU."""
-    if not isinstance(t, torch.Tensor):
+def _first(t, name: str, dims: int, dtypes, stream=None):
+    """Checks a call's first tensor, whose sizes the others follow, and its stream; returns the tensor's GPU and sizes."""
+    try:
+        shape, dev = t.shape, t.get_device()
+        fits = len(shape) == dims and t.dtype in dtypes and t.is_contiguous()
+    except AttributeError:
         _refuse(f"{name} must be a tensor")
-    if not t.is_cuda:
+    if dev < 0:
         _refuse(f"{name} must be on a GPU (it is on {t.device})")
-    if t.dim() != dims or t.dtype not in dtypes or not t.is_contiguous():
+    if not fits:
         _refuse(f"{name} must be a contiguous tensor of {dims} dimensions and type "
                 f"{' or '.join(str(d) for d in dtypes)} (got {t.dtype}, {list(t.shape)}, strides {t.stride()})")
-    dev = t.get_device()
     if stream is not None and stream.device_index != dev:
         _refuse(f"the stream is of cuda:{stream.device_index}, {name} is on cuda:{dev}")
-    return dev
+    return dev, shape
 
 
 def _take(t, name: str, dtypes, shape, dev: int):
     """Checks one more tensor; returns its address."""
-    if not isinstance(t, torch.Tensor):
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
         _refuse(f"{name} must be a tensor")
-    if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
     if t.dtype not in dtypes:
         _refuse(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
     if t.shape != shape:
@@ -101,12 +105,12 @@ def _new(shape, dtype, dev: int, stream=None):
 
 def _pairs(ids, inv, slot_of_expert, E, T, dev: int):
     """The pair tables: (their addresses, E, k); T None: as many tokens as ids has rows."""
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or (T is not None and ids.shape[0] != T):
+    shape = ids.shape if isinstance(ids, torch.Tensor) else ()
+    if len(shape) != 2 or (T is not None and shape[0] != T):
         _refuse(f"ids must be a tensor of shape [{'T' if T is None else T}, k]")
-    T, k = ids.shape
-    pi = _take(ids, "ids", (_I32,), (T, k), dev)
-    flat = isinstance(inv, torch.Tensor) and inv.dim() == 1
-    pv = _take(inv, "inv", (_I32,), (T * k,) if flat else (T, k), dev)
+    T, k = shape
+    pi = _take(ids, "ids", _INTS, shape, dev)
+    pv = _take(inv, "inv", _INTS, (T * k,) if isinstance(inv, torch.Tensor) and inv.dim() == 1 else shape, dev)
     ps = None
     if slot_of_expert is not None:
         n = slot_of_expert.shape[0] if isinstance(slot_of_expert, torch.Tensor) and slot_of_expert.dim() == 1 else -1
@@ -141,8 +145,7 @@ def _rows_out(codes, scales, rows: int, K: int, dev: int, stream):
 def ft_moe_quant_fp8(x, codes=None, scales=None, stream=None):
     """bf16 or fp32 rows [rows][K] -> (codes [rows][K], scales fp32 [rows][S]): per block of 128 the scale is the
     largest magnitude / 448 and the codes are the nearest e4m3 values of x / scale."""
-    dev = _first(x, "x", 2, _FLOATS, stream)
-    rows, K = x.shape
+    dev, (rows, K) = _first(x, "x", 2, _FLOATS, stream)
     codes, scales, pc, ps = _rows_out(codes, scales, rows, K, dev, stream)
     _run(lib.ft_moe_quant_fp8, dev, stream, x.data_ptr(), rows, K, pc, ps, FT_ROWS_F32 if x.dtype is _F32 else 0)
     return codes, scales
@@ -150,8 +153,7 @@ def ft_moe_quant_fp8(x, codes=None, scales=None, stream=None):
 
 def ft_moe_swiglu_fp8(gu, codes=None, scales=None, stream=None):
     """bf16 rows [rows][2 I] = [gate | up] -> the 8-bit rows (codes [rows][I], scales) of SiLU(gate) * up."""
-    dev = _first(gu, "gu", 2, (_BF,), stream)
-    rows, I2 = gu.shape
+    dev, (rows, I2) = _first(gu, "gu", 2, (_BF,), stream)
     if I2 % 2:
         _refuse(f"gu must have gate and up columns (got {I2})")
     codes, scales, pc, ps = _rows_out(codes, scales, rows, I2 // 2, dev, stream)
@@ -161,8 +163,7 @@ def ft_moe_swiglu_fp8(gu, codes=None, scales=None, stream=None):
 
 def ft_moe_dispatch(x, ids, inv, E=None, slot_of_expert=None, x_sorted=None, stream=None):
     """Token rows [T][d] (bf16 or fp32) to their places in expert order [T*k][d]."""
-    dev = _first(x, "x", 2, _FLOATS, stream)
-    T, d = x.shape
+    dev, (T, d) = _first(x, "x", 2, _FLOATS, stream)
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
     if x_sorted is None:
         x_sorted = _new((T * k, d), x.dtype, dev, stream)
@@ -173,8 +174,7 @@ def ft_moe_dispatch(x, ids, inv, E=None, slot_of_expert=None, x_sorted=None, str
 
 def ft_moe_dispatch_fp8(x, ids, inv, E=None, slot_of_expert=None, codes=None, scales=None, stream=None):
     """Token rows [T][d] (bf16 or fp32) to 8-bit rows in expert order: (codes [T*k][d], scales [T*k][S])."""
-    dev = _first(x, "x", 2, _FLOATS, stream)
-    T, d = x.shape
+    dev, (T, d) = _first(x, "x", 2, _FLOATS, stream)
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
     codes, scales, pc, ps = _rows_out(codes, scales, T * k, d, dev, stream)
     _run(lib.ft_moe_dispatch_fp8, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, pc, ps,
@@ -184,14 +184,14 @@ def ft_moe_dispatch_fp8(x, ids, inv, E=None, slot_of_expert=None, codes=None, sc
 
 def ft_moe_dispatch_grad(dx_sorted, ids, inv, E=None, slot_of_expert=None, dx=None, stream=None):
     """Gradient of ft_moe_dispatch: the sum [T][d] of every token's rows of dx_sorted [T*k][d]."""
-    dev = _first(dx_sorted, "dx_sorted", 2, _FLOATS, stream)
+    dev, (P, d) = _first(dx_sorted, "dx_sorted", 2, _FLOATS, stream)
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, None, dev)
-    d = dx_sorted.shape[1]
-    src = _take(dx_sorted, "dx_sorted", _FLOATS, (T * k, d), dev)
+    if P != T * k:
+        _refuse(f"dx_sorted must have {T * k} rows (got {P})")
     if dx is None:
         dx = _new((T, d), dx_sorted.dtype, dev, stream)
     out = _take(dx, "dx", (dx_sorted.dtype,), (T, d), dev)
-    _run(lib.ft_moe_dispatch_grad, dev, stream, src, pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if dx_sorted.dtype is _F32 else 0)
+    _run(lib.ft_moe_dispatch_grad, dev, stream, dx_sorted.data_ptr(), pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if dx_sorted.dtype is _F32 else 0)
     return dx
 
 
@@ -199,8 +199,7 @@ def ft_moe_combine_grad(dout, y_sorted, ids, w, inv, E=None, slot_of_expert=None
                         want_dlogits: bool = True, stream=None):
     """Gradient of ft_moe_combine for dout [T][d] (fp32 or bf16): (dy_sorted bf16 [T*k][d], dw fp32 [T][k],
     dlogits fp32 [T][E] through the renormalised softmax of the chosen logits, or None)."""
-    dev = _first(dout, "dout", 2, _FLOATS, stream)
-    T, d = dout.shape
+    dev, (T, d) = _first(dout, "dout", 2, _FLOATS, stream)
     pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
     py = _take(y_sorted, "y_sorted", (_BF,), (T * k, d), dev)
     pw = _take(w, "w", (_F32,), (T, k), dev)
@@ -228,8 +227,7 @@ def _product_out(out, out_dtype, shape, dev: int, stream):
 def ft_moe_fp8_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """8-bit rows a [M][K] (scales [M][S]) times w [N][K] transposed (fp32 scales [ceil(N/128)][ceil(K/128)]):
     [M][N] in bf16, or in fp32 with out_dtype=torch.float32 (or an fp32 `out`)."""
-    dev = _first(a, "a", 2, _CODES, stream)
-    M, K = a.shape
+    dev, (M, K) = _first(a, "a", 2, _CODES, stream)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         _refuse("w must be a tensor of shape [N, K]")
     N = w.shape[0]
@@ -246,8 +244,7 @@ def ft_moe_fp8_grouped_matmul(a, a_scales, w, w_scales, offsets, slot_of_expert,
     """8-bit rows a [P][K] in expert order, each expert's rows times its matrix of w [n_slots][N][K] transposed
     (fp32 scales [n_slots][ceil(N/128)][ceil(K/128)]): [P][N] in bf16 or fp32.  Rows of experts without a slot
     are left as they were (with out=None: unset)."""
-    dev = _first(a, "a", 2, _CODES, stream)
-    P, K = a.shape
+    dev, (P, K) = _first(a, "a", 2, _CODES, stream)
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         _refuse("w must be a tensor of shape [n_slots, N, K]")
     n_slots, N, _ = w.shape
@@ -274,8 +271,7 @@ class Fp8MoELayer:
     where MoELayer carries two.  One forward() at a time: its results and buffers are the next one's."""
 
     def __init__(self, w13, s13, w2, s2, slot_of_expert, k: int, T: int, out_bf16: bool = False):
-        dev = _first(w13, "w13", 3, _CODES)
-        self.n_slots, I2, self.d = w13.shape
+        dev, (self.n_slots, I2, self.d) = _first(w13, "w13", 3, _CODES)
         self.I = I2 // 2
         nb = lambda v: (v + 127) // 128  # noqa: E731
         _take(w2, "w2", _CODES, (self.n_slots, self.d, self.I), dev)
