@@ -710,3 +710,11 @@ def test_refusals_before_anything_is_allocated():
     for kw in (dict(d=24), dict(I=8), dict(E=1025), dict(k=5), dict(k=0), dict(T=-1), dict(n=0), dict(d=0), dict(E=64, k=33)):
         with pytest.raises(ft.FtError, match="invalid layer shape"):
             layer(**kw)
+
+
+def test_sparse_tensors_are_refused():
+    x = torch.ones(4, 64, device="cuda").to(BF)
+    with pytest.raises(ft.FtError, match="must be"):
+        ft.ft_moe_quant_fp8(x.to_sparse())
+    with pytest.raises(ft.FtError, match="must be"):
+        ft.ft_moe_quant_fp8(x, scales=torch.ones(4, 4, device="cuda").to_sparse())
