@@ -76,6 +76,11 @@ enum ft_weight_format {
 /* ft_moe_combine / ft_moe_layer flags */
 #define FT_OUT_BF16 0x4   /* write `out` as bf16 instead of fp32 */
 
+/* Flag of the calls that are given a slot table but no bank (ft_moe_combine and the calls of ft_moe_rows.h that
+ * take pairs): slot_of_expert entries outside [0, n) count as not resident, as in the calls that know the
+ * bank's n slots.  Without it every entry that is not negative counts as resident.  1 <= n < 2^23. */
+#define FT_N_SLOTS(n) ((n) << 8)
+
 /* ft_moe_layer flags */
 #define FT_LAYER_UNFUSED 0x8  /* always run the four calls' kernels, never the fused decode kernels */
 
@@ -194,7 +199,9 @@ int ft_moe_grouped_ffn(const ft_moe_bank* bank, const int32_t* slot_of_expert, i
 /*
  * Weighted combine back to token order, and the residual mask of non-resident experts
  * ([walk-through] section 五: experts not resident on the GPU are left to another path).
- *   out[t][c] = sum over j ascending with slot_of_expert[ids[t][j]] >= 0 of
+ *   out[t][c] = sum over j ascending with slot_of_expert[ids[t][j]] >= 0 (and below n with
+ *               FT_N_SLOTS(n): the rows of other experts are none that ft_moe_grouped_ffn or
+ *               ft_moe_fp8_grouped_matmul wrote) of
  *               w[t][j] * y_sorted[inv[t*k+j]][c]   (+ y_shared[t][c] when y_shared != NULL)
  *   residual_mask[t] bit j = 1 iff expert ids[t][j] is not resident (may be NULL)
  * Weights are not renormalised over the resident subset: the masked share belongs to the other

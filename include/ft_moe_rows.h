@@ -58,7 +58,10 @@ int ft_moe_swiglu_fp8(const uint16_t* gu, int rows, int I, uint8_t* codes, float
  * Token rows in expert order.  For every pair (t, j) that has a row: x_sorted[inv[t*k+j]] = x[t].
  * ids, inv as ft_moe_route and ft_moe_permute give them.  A pair has a row when ids[t*k+j] lies in [0, E),
  * inv[t*k+j] in [0, T*k), and slot_of_expert (int32 [E]; NULL: every expert counts) is not negative for
- * its expert; rows of other pairs are left as they were.  x, x_sorted bf16 (FT_ROWS_F32: fp32), d % 8 == 0.
+ * its expert, nor past the bank where the flags hold FT_N_SLOTS(n); rows of other pairs are left as they were.
+ * x, x_sorted bf16 (FT_ROWS_F32: fp32), d % 8 == 0.  (This call, ft_moe_dispatch_fp8, ft_moe_dispatch_grad and
+ * ft_moe_combine_grad read the same table: beside ft_moe_fp8_grouped_matmul, which skips slots outside its n_slots,
+ * give them its n_slots, so that rows it left alone are not read.)
  */
 int ft_moe_dispatch(const void* x, const int32_t* ids, const int32_t* inv, const int32_t* slot_of_expert, int T,
                     int E, int k, int d, void* x_sorted, int flags, hipStream_t stream);

@@ -25,6 +25,14 @@ FT_PATH_MASK = 3
 LAYER_MAX_T = 16   # largest T of the fused decode kernels
 FT_NOALLOC_SCRATCH_BYTES = 8 << 20   # static scratch of ft_moe_layer_noalloc, per device
 
+
+def FT_N_SLOTS(n: int) -> int:
+    """Flag: slot-table entries outside [0, n) count as not resident (calls given a slot table but no bank)."""
+    if not 1 <= n < 1 << 23:
+        raise FtError(FT_E_INVAL, f"n_slots must be in [1, 2^23) (got {n})")
+    return n << 8
+
+
 STATUS_NAMES = {0: "FT_OK", 1: "FT_E_INVAL", 2: "FT_E_UNSUPPORTED", 3: "FT_E_WORKSPACE", 4: "FT_E_HIP",
                 5: "FT_E_INTERNAL"}
 
@@ -336,6 +344,7 @@ def ft_moe_grouped_ffn(bank: DeviceBank, slot_of_expert, x, k: int, offsets, gat
 
 def ft_moe_combine(y_sorted, y_shared, ids, w, inv, slot_of_expert, d: int, out=None, residual_mask=None,
                    flags: int = 0, want_mask: bool = True, stream=None):
+    """flags: FT_OUT_BF16, and FT_N_SLOTS(n) beside a call that skips slots outside its bank's n."""
     T, k = ids.shape
     E = slot_of_expert.shape[0]
     dev = ids.device
@@ -387,6 +396,8 @@ class MoELayer:
         else:
             pws = lib.ft_moe_permute_workspace(T, E, k)
             self.perm_ws = torch.empty(max(pws, 256), dtype=torch.uint8, device=dev)
+            # the combine has no bank to compare the table with (a bank past the flag's range fits no GPU)
+            self.combine_flags = self.out_flags | FT_N_SLOTS(bank.n_slots)
             fws = lib.ft_moe_grouped_ffn_workspace(bank.ref, T, E, k, shared_slot, flags)
             self.ffn_ws = torch.empty(max(fws, 256), dtype=torch.uint8, device=dev)
 
@@ -439,7 +450,7 @@ class MoELayer:
                                       _ptr(self.ffn_ws), self.ffn_ws.numel(), self.flags, s))
         _check(lib.ft_moe_combine(_ptr(self.y_sorted), _ptr(self.y_shared), _ptr(self.ids), _ptr(self.w),
                                   _ptr(self.inv), _ptr(self.slot_of), T, E, k, self.bank.d, _ptr(self.out),
-                                  _ptr(self.mask), self.out_flags, s))
+                                  _ptr(self.mask), self.combine_flags, s))
         return self.out[:T], self.mask[:T]
 
 

@@ -363,7 +363,7 @@ int ft_moe_combine(const uint16_t* y_sorted, const uint16_t* y_shared, const int
     int rc = check_tek(T, E, k);
     if (rc) return rc;
     REQUIRE(d > 0 && d % 8 == 0, FT_E_INVAL, "d must be a positive multiple of 8 (got %d)", d);
-    REQUIRE((flags & ~FT_OUT_BF16) == 0, FT_E_INVAL, "unknown flags 0x%x", flags);
+    REQUIRE((flags & ~(FT_OUT_BF16 | kSlotFlags)) == 0, FT_E_INVAL, "unknown flags 0x%x", flags);
     if (T == 0) return ok();
     CHECK_PTR(y_sorted, "y_sorted");
     if (y_shared) CHECK_PTR(y_shared, "y_shared");
@@ -373,8 +373,9 @@ int ft_moe_combine(const uint16_t* y_sorted, const uint16_t* y_shared, const int
     CHECK_PTR(slot_of_expert, "slot_of_expert");
     CHECK_PTR(out, "out");
     if (residual_mask) CHECK_PTR(residual_mask, "residual_mask");
-    return hip_status(ftk::launch_combine(y_sorted, y_shared, ids, w, inv, slot_of_expert, INT_MAX, T, E, k, d, out,
-                                          residual_mask,
+    const int n_slots = flag_slots(flags);
+    return hip_status(ftk::launch_combine(y_sorted, y_shared, ids, w, inv, slot_of_expert, n_slots ? n_slots : INT_MAX, T,
+                                          E, k, d, out, residual_mask,
                                           (flags & FT_OUT_BF16) != 0, stream),
                       "ft_moe_combine launch");
   } catch (...) {

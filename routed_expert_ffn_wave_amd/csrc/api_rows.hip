@@ -41,7 +41,13 @@ int check_pairs(int T, int E, int k, int d, int multiple) {
     CHECK_PTR(ids, "ids");                                 \
     CHECK_PTR(inv, "inv");                                 \
     if (slot_of_expert) CHECK_PTR(slot_of_expert, "slot_of_expert"); \
+    REQUIRE(slot_of_expert || flag_slots(flags) == 0, FT_E_INVAL, "FT_N_SLOTS without slot_of_expert"); \
   } while (0)
+
+PairTab pair_tab(const int32_t* ids, const int32_t* inv, const int32_t* slot_of, int T, int E, int k, int flags) {
+  const int n = flag_slots(flags);
+  return PairTab{ids, inv, slot_of, E, k, T * k, n ? (uint32_t)n : 0x80000000u};
+}
 
 int check_matmul(int rows, const char* rows_name, int N, int K, int E, int flags) {
   int rc = check_flags(flags, FT_OUT_BF16);
@@ -101,12 +107,12 @@ int ft_moe_dispatch(const void* x, const int32_t* ids, const int32_t* inv, const
   try {
     int rc = check_pairs(T, E, k, d, 8);
     if (rc) return rc;
-    if ((rc = check_flags(flags, FT_ROWS_F32))) return rc;
+    if ((rc = check_flags(flags, FT_ROWS_F32 | kSlotFlags))) return rc;
     if (T == 0) return ok();
     CHECK_PTR(x, "x");
     CHECK_TAB();
     CHECK_PTR(x_sorted, "x_sorted");
-    const PairTab tab{ids, inv, slot_of_expert, E, k, T * k};
+    const PairTab tab = pair_tab(ids, inv, slot_of_expert, T, E, k, flags);
     return hip_status(launch_dispatch(x, tab, T, d, x_sorted, (flags & FT_ROWS_F32) != 0, stream), "ft_moe_dispatch launch");
   } catch (...) {
     return fail(FT_E_INTERNAL, "ft_moe_dispatch: unexpected exception");
@@ -119,13 +125,13 @@ int ft_moe_dispatch_fp8(const void* x, const int32_t* ids, const int32_t* inv, c
     int rc = check_pairs(T, E, k, d, 16);
     if (rc) return rc;
     if ((rc = check_rows_fp8(T, d, "T", "d"))) return rc;
-    if ((rc = check_flags(flags, FT_ROWS_F32))) return rc;
+    if ((rc = check_flags(flags, FT_ROWS_F32 | kSlotFlags))) return rc;
     if (T == 0) return ok();
     CHECK_PTR(x, "x");
     CHECK_TAB();
     CHECK_PTR(codes, "codes");
     CHECK_PTR(scales, "scales");
-    const PairTab tab{ids, inv, slot_of_expert, E, k, T * k};
+    const PairTab tab = pair_tab(ids, inv, slot_of_expert, T, E, k, flags);
     return hip_status(launch_rows_fp8(flags & FT_ROWS_F32 ? ROWS_F32 : ROWS_BF16, x, T, d, codes, scales, &tab, stream),
                       "ft_moe_dispatch_fp8 launch");
   } catch (...) {
@@ -138,12 +144,12 @@ int ft_moe_dispatch_grad(const void* dx_sorted, const int32_t* ids, const int32_
   try {
     int rc = check_pairs(T, E, k, d, 8);
     if (rc) return rc;
-    if ((rc = check_flags(flags, FT_ROWS_F32))) return rc;
+    if ((rc = check_flags(flags, FT_ROWS_F32 | kSlotFlags))) return rc;
     if (T == 0) return ok();
     CHECK_PTR(dx_sorted, "dx_sorted");
     CHECK_TAB();
     CHECK_PTR(dx, "dx");
-    const PairTab tab{ids, inv, slot_of_expert, E, k, T * k};
+    const PairTab tab = pair_tab(ids, inv, slot_of_expert, T, E, k, flags);
     return hip_status(launch_dispatch_grad(dx_sorted, tab, T, d, dx, (flags & FT_ROWS_F32) != 0, stream),
                       "ft_moe_dispatch_grad launch");
   } catch (...) {
@@ -157,7 +163,7 @@ int ft_moe_combine_grad(const void* dout, const uint16_t* y_sorted, const int32_
   try {
     int rc = check_pairs(T, E, k, d, 8);
     if (rc) return rc;
-    if ((rc = check_flags(flags, FT_OUT_BF16))) return rc;
+    if ((rc = check_flags(flags, FT_OUT_BF16 | kSlotFlags))) return rc;
     REQUIRE(T < (1 << 24), FT_E_UNSUPPORTED, "T too large (%d tokens, a block of 256 threads each)", T);
     if (T == 0) return ok();
     CHECK_PTR(dout, "dout");
@@ -167,7 +173,7 @@ int ft_moe_combine_grad(const void* dout, const uint16_t* y_sorted, const int32_
     CHECK_PTR(dy_sorted, "dy_sorted");
     CHECK_PTR(dw, "dw");
     if (dlogits) CHECK_PTR(dlogits, "dlogits");
-    const PairTab tab{ids, inv, slot_of_expert, E, k, T * k};
+    const PairTab tab = pair_tab(ids, inv, slot_of_expert, T, E, k, flags);
     return hip_status(launch_combine_grad(dout, y_sorted, w, tab, T, d, dy_sorted, dw, dlogits, (flags & FT_OUT_BF16) != 0,
                                           stream),
                       "ft_moe_combine_grad launch");

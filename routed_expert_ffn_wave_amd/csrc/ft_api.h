@@ -45,6 +45,10 @@ inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
     if (!aligned16(p)) return fail(FT_E_INVAL, "%s is not 16-byte aligned", name); \
   } while (0)
 
+// The n of FT_N_SLOTS(n) in a call's flags; 0: not given.
+constexpr int kSlotFlags = 0x7fffff00;
+inline int flag_slots(int flags) { return (flags & kSlotFlags) >> 8; }
+
 inline int check_tek(int T, int E, int k) {
   REQUIRE(T >= 0, FT_E_INVAL, "T must be >= 0 (got %d)", T);
   REQUIRE(E >= 1 && E <= 1024, FT_E_INVAL, "E must be in [1, 1024] (got %d)", E);

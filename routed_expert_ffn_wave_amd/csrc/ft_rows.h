@@ -11,11 +11,12 @@ struct PairTab {
   const int32_t* inv;      // [T][k]
   const int32_t* slot_of;  // [E], or null: every expert counts
   int E, k, TK;            // TK = T * k
+  uint32_t slots;          // entries of slot_of outside [0, slots) name no matrix
   // row of flat pair f, or -1 when it has none; nothing is read out of bounds for any table contents
   __device__ __forceinline__ int row(int f) const {
     const int e = ids[f];
     if ((unsigned)e >= (unsigned)E) return -1;
-    if (slot_of && slot_of[e] < 0) return -1;
+    if (slot_of && (uint32_t)slot_of[e] >= slots) return -1;
     const int r = inv[f];
     return (unsigned)r < (unsigned)TK ? r : -1;
   }

@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from . import FT_E_INVAL, FT_OUT_BF16, FtError, _check, lib
+from . import FT_E_INVAL, FT_N_SLOTS, FT_OUT_BF16, FtError, _check, lib
 
 FT_ROWS_F32 = 0x20
 
@@ -103,8 +103,8 @@ def _new(shape, dtype, dev: int, stream=None):
         return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
 
 
-def _pairs(ids, inv, slot_of_expert, E, T, dev: int):
-    """The pair tables: (their addresses, E, k); T None: as many tokens as ids has rows."""
+def _pairs(ids, inv, slot_of_expert, E, T, dev: int, n_slots=None):
+    """The pair tables: (their addresses, T, E, k, the flags of n_slots); T None: as many tokens as ids has rows."""
     shape = ids.shape if isinstance(ids, torch.Tensor) else ()
     if len(shape) != 2 or (T is not None and shape[0] != T):
         _refuse(f"ids must be a tensor of shape [{'T' if T is None else T}, k]")
@@ -122,7 +122,11 @@ def _pairs(ids, inv, slot_of_expert, E, T, dev: int):
         _refuse("E is needed when slot_of_expert is not given")
     if E < 1:
         _refuse(f"E must be >= 1 (got {E})")
-    return pi, pv, ps, T, E, k
+    if n_slots is None:
+        return pi, pv, ps, T, E, k, 0
+    if ps is None:
+        _refuse("n_slots is given without slot_of_expert")
+    return pi, pv, ps, T, E, k, FT_N_SLOTS(n_slots)
 
 
 def _cols(K: int) -> int:
@@ -161,46 +165,49 @@ def ft_moe_swiglu_fp8(gu, codes=None, scales=None, stream=None):
     return codes, scales
 
 
-def ft_moe_dispatch(x, ids, inv, E=None, slot_of_expert=None, x_sorted=None, stream=None):
-    """Token rows [T][d] (bf16 or fp32) to their places in expert order [T*k][d]."""
+def ft_moe_dispatch(x, ids, inv, E=None, slot_of_expert=None, x_sorted=None, stream=None, n_slots=None):
+    """Token rows [T][d] (bf16 or fp32) to their places in expert order [T*k][d].  n_slots, here and in the calls
+    below: slots outside [0, n_slots) count as not resident too, as in ft_moe_fp8_grouped_matmul."""
     dev, (T, d) = _first(x, "x", 2, _FLOATS, stream)
-    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
+    pi, pv, pt, T, E, k, fl = _pairs(ids, inv, slot_of_expert, E, T, dev, n_slots)
     if x_sorted is None:
         x_sorted = _new((T * k, d), x.dtype, dev, stream)
     out = _take(x_sorted, "x_sorted", (x.dtype,), (T * k, d), dev)
-    _run(lib.ft_moe_dispatch, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if x.dtype is _F32 else 0)
+    _run(lib.ft_moe_dispatch, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, out,
+         fl | (FT_ROWS_F32 if x.dtype is _F32 else 0))
     return x_sorted
 
 
-def ft_moe_dispatch_fp8(x, ids, inv, E=None, slot_of_expert=None, codes=None, scales=None, stream=None):
+def ft_moe_dispatch_fp8(x, ids, inv, E=None, slot_of_expert=None, codes=None, scales=None, stream=None, n_slots=None):
     """Token rows [T][d] (bf16 or fp32) to 8-bit rows in expert order: (codes [T*k][d], scales [T*k][S])."""
     dev, (T, d) = _first(x, "x", 2, _FLOATS, stream)
-    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
+    pi, pv, pt, T, E, k, fl = _pairs(ids, inv, slot_of_expert, E, T, dev, n_slots)
     codes, scales, pc, ps = _rows_out(codes, scales, T * k, d, dev, stream)
     _run(lib.ft_moe_dispatch_fp8, dev, stream, x.data_ptr(), pi, pv, pt, T, E, k, d, pc, ps,
-         FT_ROWS_F32 if x.dtype is _F32 else 0)
+         fl | (FT_ROWS_F32 if x.dtype is _F32 else 0))
     return codes, scales
 
 
-def ft_moe_dispatch_grad(dx_sorted, ids, inv, E=None, slot_of_expert=None, dx=None, stream=None):
+def ft_moe_dispatch_grad(dx_sorted, ids, inv, E=None, slot_of_expert=None, dx=None, stream=None, n_slots=None):
     """Gradient of ft_moe_dispatch: the sum [T][d] of every token's rows of dx_sorted [T*k][d]."""
     dev, (P, d) = _first(dx_sorted, "dx_sorted", 2, _FLOATS, stream)
-    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, None, dev)
+    pi, pv, pt, T, E, k, fl = _pairs(ids, inv, slot_of_expert, E, None, dev, n_slots)
     if P != T * k:
         _refuse(f"dx_sorted must have {T * k} rows (got {P})")
     if dx is None:
         dx = _new((T, d), dx_sorted.dtype, dev, stream)
     out = _take(dx, "dx", (dx_sorted.dtype,), (T, d), dev)
-    _run(lib.ft_moe_dispatch_grad, dev, stream, dx_sorted.data_ptr(), pi, pv, pt, T, E, k, d, out, FT_ROWS_F32 if dx_sorted.dtype is _F32 else 0)
+    _run(lib.ft_moe_dispatch_grad, dev, stream, dx_sorted.data_ptr(), pi, pv, pt, T, E, k, d, out,
+         fl | (FT_ROWS_F32 if dx_sorted.dtype is _F32 else 0))
     return dx
 
 
 def ft_moe_combine_grad(dout, y_sorted, ids, w, inv, E=None, slot_of_expert=None, dy_sorted=None, dw=None, dlogits=None,
-                        want_dlogits: bool = True, stream=None):
+                        want_dlogits: bool = True, stream=None, n_slots=None):
     """Gradient of ft_moe_combine for dout [T][d] (fp32 or bf16): (dy_sorted bf16 [T*k][d], dw fp32 [T][k],
     dlogits fp32 [T][E] through the renormalised softmax of the chosen logits, or None)."""
     dev, (T, d) = _first(dout, "dout", 2, _FLOATS, stream)
-    pi, pv, pt, T, E, k = _pairs(ids, inv, slot_of_expert, E, T, dev)
+    pi, pv, pt, T, E, k, fl = _pairs(ids, inv, slot_of_expert, E, T, dev, n_slots)
     py = _take(y_sorted, "y_sorted", (_BF,), (T * k, d), dev)
     pw = _take(w, "w", (_F32,), (T, k), dev)
     if dy_sorted is None:
@@ -212,7 +219,7 @@ def ft_moe_combine_grad(dout, y_sorted, ids, w, inv, E=None, slot_of_expert=None
     pl = None if dlogits is None else _take(dlogits, "dlogits", (_F32,), (T, E), dev)
     _run(lib.ft_moe_combine_grad, dev, stream, dout.data_ptr(), py, pi, pw, pv, pt, T, E, k, d,
          _take(dy_sorted, "dy_sorted", (_BF,), (T * k, d), dev), _take(dw, "dw", (_F32,), (T, k), dev), pl,
-         FT_OUT_BF16 if dout.dtype is _BF else 0)
+         fl | (FT_OUT_BF16 if dout.dtype is _BF else 0))
     return dy_sorted, dw, dlogits
 
 
@@ -266,8 +273,8 @@ class Fp8MoELayer:
     route, permute, token rows to 8-bit rows in expert order, gate/up product, SwiGLU to 8-bit rows, down product,
     weighted combine.  w13 [n_slots][2I][d] ([gate ; up] rows) and w2 [n_slots][d][I] are e4m3 codes with
     fp32 scales per 128 x 128 block (s13, s2); slot_of_expert int32 [E], -1 for experts that are not resident
-    (left to the residual mask).  Every buffer is allocated here for a fixed (T, k): forward() allocates
-    nothing and can be captured into a graph.  The accuracy is that of one e4m3 term per activation,
+    (left to the residual mask; entries outside [0, n_slots) count as -1).  Every buffer is allocated here for a
+    fixed (T, k): forward() allocates nothing and can be captured into a graph.  The accuracy is that of one e4m3 term per activation,
     where MoELayer carries two.  One forward() at a time: its results and buffers are the next one's."""
 
     def __init__(self, w13, s13, w2, s2, slot_of_expert, k: int, T: int, out_bf16: bool = False):
@@ -280,11 +287,12 @@ class Fp8MoELayer:
         _first(slot_of_expert, "slot_of_expert", 1, (_I32,))
         _take(slot_of_expert, "slot_of_expert", (_I32,), slot_of_expert.shape, dev)
         E = slot_of_expert.shape[0]
-        if T < 0 or T * k > 1 << 30 or I2 % 32 or self.d % 16 or self.d * self.I == 0 or self.n_slots < 1 or E > 1024 or not 1 <= k <= min(E, 32):
+        if T < 0 or T * k > 1 << 30 or I2 % 32 or self.d % 16 or self.d * self.I == 0 or not 1 <= self.n_slots < 1 << 23 or E > 1024 or not 1 <= k <= min(E, 32):
             _refuse(f"invalid layer shape T={T}, k={k}, E={E}, d={self.d}, w13 rows={I2}, slots={self.n_slots}")
         self.dev = dev
         self.w13, self.s13, self.w2, self.s2, self.slot_of = w13, s13, w2, s2, slot_of_expert
-        self.E, self.k, self.T, self.flags = slot_of_expert.shape[0], k, T, FT_OUT_BF16 if out_bf16 else 0
+        self.E, self.k, self.T, self.slots = E, k, T, FT_N_SLOTS(self.n_slots)
+        self.flags = self.slots | (FT_OUT_BF16 if out_bf16 else 0)
         new = lambda *shape, dtype: _new(shape, dtype, dev)  # noqa: E731
         P, e4, f32, bf, i32 = T * k, _E4, _F32, _BF, _I32
         self.ids, self.w, self.inv = new(T, k, dtype=i32), new(T, k, dtype=f32), new(max(P, 1), dtype=i32)
@@ -311,7 +319,8 @@ class Fp8MoELayer:
         _run(lib.ft_moe_route, dev, stream, pl, T, E, k, pi, pw)
         _run(lib.ft_moe_permute, dev, stream, pi, T, E, k, self.counts.data_ptr(), self.offsets.data_ptr(),
              self.gather.data_ptr(), pv, self.perm_ws.data_ptr(), self.perm_ws.numel())
-        _run(lib.ft_moe_dispatch_fp8, dev, stream, px, pi, pv, pt, T, E, k, self.d, self.x8.data_ptr(), self.xs.data_ptr(), 0)
+        _run(lib.ft_moe_dispatch_fp8, dev, stream, px, pi, pv, pt, T, E, k, self.d, self.x8.data_ptr(), self.xs.data_ptr(),
+             self.slots)
         ft_moe_fp8_grouped_matmul(self.x8, self.xs, self.w13, self.s13, self.offsets, slot, out=self.gu, stream=stream)
         ft_moe_swiglu_fp8(self.gu, codes=self.h8, scales=self.hs, stream=stream)
         ft_moe_fp8_grouped_matmul(self.h8, self.hs, self.w2, self.s2, self.offsets, slot, out=self.y_sorted, stream=stream)

@@ -718,3 +718,73 @@ def test_sparse_tensors_are_refused():
         ft.ft_moe_quant_fp8(x.to_sparse())
     with pytest.raises(ft.FtError, match="must be"):
         ft.ft_moe_quant_fp8(x, scales=torch.ones(4, 4, device="cuda").to_sparse())
+
+
+# ---------------------------------------------------------------------------------------------- slots past the bank
+
+def past_the_bank(slot, n):
+    """The same table with entries at and past the bank's n slots in place of some, and with -1 there."""
+    past, none = slot.clone(), slot.clone()
+    held = torch.nonzero(slot >= 0)[:, 0]
+    for e, v in zip(held[:3].tolist(), (n, n + 5, 2 ** 31 - 1)):
+        past[e], none[e] = v, -1
+    return past, none
+
+
+@pytest.mark.parametrize("T, out_bf16", [(1, False), (40, True), (300, False)])
+def test_layer_with_slots_past_the_bank(T, out_bf16):
+    """They count as not resident in every step: the rows that the products leave alone reach no output, and the pair
+    is left to the residual mask."""
+    E, k, d, I, held = 8, 4, 256, 128, 6
+    w13, s13, w2, s2, slot, logits, x = layer_inputs(T, T, E, k, d, I, held)
+    got = []
+    for table in past_the_bank(slot.cpu(), held):
+        layer = ft.Fp8MoELayer(w13, s13, w2, s2, table.cuda(), k, T, out_bf16=out_bf16)
+        for b in (layer.gu, layer.y_sorted):
+            b.fill_(float("nan"))
+        got.append([v.clone() for v in layer.forward(logits, x)])
+    assert torch.isfinite(got[0][0].float()).all()
+    assert same_bits(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_pair_calls_with_slots_past_the_bank(dtype):
+    g = gen(21)
+    T, E, k, d, held = 30, 9, 4, 272, 6
+    r = ref.routing(g, T, E, k, held)
+    past, none = past_the_bank(r["slot"], held)
+    rows = ref.pair_rows(r["ids"], r["inv"], E, none)
+    away = torch.ones(T * k, dtype=torch.bool)
+    away[rows[rows >= 0]] = False
+    x, dout = torch.randn(T, d, generator=g).to(dtype).cuda(), torch.randn(T, d, generator=g).to(dtype).cuda()
+    y, dxs = torch.randn(T * k, d, generator=g).to(BF), torch.randn(T * k, d, generator=g).to(dtype)
+    y[away], dxs[away] = float("nan"), float("nan")
+    y, dxs, ids, inv, w = y.cuda(), dxs.cuda(), r["ids"].cuda(), r["inv"].cuda(), r["w"].cuda()
+    got = []
+    for table, kw in ((past.cuda(), dict(n_slots=held)), (none.cuda(), {})):
+        kw["slot_of_expert"] = table
+        out = [ft.ft_moe_dispatch(x, ids, inv, x_sorted=filled(T * k, d, dtype=dtype), **kw)]
+        out += ft.ft_moe_dispatch_fp8(x, ids, inv, codes=filled(T * k, d, dtype=E4), scales=filled(T * k, ref.cols(d), dtype=F32), **kw)
+        out += [ft.ft_moe_dispatch_grad(dxs, ids, inv, **kw)]
+        out += ft.ft_moe_combine_grad(dout, y, ids, w, inv, dy_sorted=filled(T * k, d, dtype=BF), **kw)
+        out += ft.ft_moe_combine(y, None, ids, w, inv, table, d, flags=ft.FT_N_SLOTS(held) if "n_slots" in kw else 0)
+        got.append(out)
+    assert torch.isfinite(got[0][3].float()).all() and torch.isfinite(got[0][5]).all() and torch.isfinite(got[0][6]).all()
+    assert all(same_bits(a, b) for a, b in zip(*got))
+
+
+def test_four_calls_with_slots_past_the_bank():
+    """MoELayer's two modes agree on such a table."""
+    import synth
+    from gpu_util import device_bank
+    w = synth.Workload("slots_past_the_bank", 93, T=16, d=256, E=8, k=4, I=128, fmt=synth.FMT_BF16)
+    li = synth.layer_inputs(w, layer=0, T=16)
+    bank = device_bank(li.bank)
+    past, none = past_the_bank(li.slot_of_expert.cpu(), li.bank.n_slots)
+    got = []
+    for table in (past, none):
+        layer = ft.MoELayer(bank, table.cuda(), w.k, 16, mode="calls")
+        layer.y_sorted.fill_(float("nan"))
+        got.append([v.clone() for v in layer.forward(li.logits.cuda(), li.x.cuda())])
+    assert torch.isfinite(got[0][0]).all()
+    assert same_bits(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

@@ -153,3 +153,22 @@ def test_sizes_that_a_launch_cannot_count():
 
 def test_scale_cols_of_the_largest_size():
     assert ft.ft_moe_fp8_scale_cols(2 ** 31 - 1) == 4 * 2 ** 22
+
+
+def test_slot_counts_in_flags():
+    assert re.search(r"#define FT_N_SLOTS\(n\) \(\(n\) << 8\)", open(os.path.join(ROOT, "include", "ft_moe.h")).read())
+    assert ft.FT_N_SLOTS(5) == 5 << 8 and ft.FT_N_SLOTS((1 << 23) - 1) == 0x7FFFFF00
+    for n in (0, -1, 1 << 23):
+        with pytest.raises(ft.FtError, match="n_slots must be"):
+            ft.FT_N_SLOTS(n)
+    for name in ("dispatch", "dispatch_fp8", "dispatch_grad", "combine_grad"):
+        err(_one(name, flags=ft.FT_N_SLOTS(5)), ft.FT_E_INVAL, "FT_N_SLOTS without slot_of_expert")
+        err(_one(name, flags=ft.FT_N_SLOTS(5), slot=A, out=None), ft.FT_E_INVAL, "is null")
+        err(_one(name, flags=-(2 ** 31), slot=A), ft.FT_E_INVAL, "unknown flags 0x80000000")
+        assert _one(name, T=0, flags=ft.FT_N_SLOTS(5)) == ft.FT_OK
+    # calls that know the bank, or take no table, do not take the flag
+    err(L.ft_moe_quant_fp8(A, 4, 64, B, B, ft.FT_N_SLOTS(5), None), ft.FT_E_INVAL, "unknown flags 0x500")
+    err(L.ft_moe_fp8_grouped_matmul(A, A, 4, A, A, 3, 64, 64, A, A, 8, B, ft.FT_N_SLOTS(3), None), ft.FT_E_INVAL, "unknown flags 0x300")
+    call = lambda flags, out=None: L.ft_moe_combine(A, None, A, A, A, A, 4, 8, 2, 256, out, None, flags, None)  # noqa: E731
+    err(call(ft.FT_N_SLOTS(5) | ft.FT_OUT_BF16), ft.FT_E_INVAL, "out is null")
+    err(call(-(2 ** 31)), ft.FT_E_INVAL, "unknown flags 0x80000000")
