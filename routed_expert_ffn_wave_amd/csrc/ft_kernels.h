@@ -9,11 +9,11 @@
 namespace ftk {
 
 // What a kernel's launch code reuses from call to call: the device's CU count and the blocks of the
-// kernel one CU holds at the largest dynamic-LDS size it has been given on that device (so the count
-// never exceeds what a smaller request allows).  One instance per kernel; every read and update is
-// under its mutex, so host threads may launch concurrently on any devices.
+// kernel one CU holds at a dynamic-LDS size.  The blocks are kept by size, as the size depends on the call (on
+// its experts, for one): a call's grid is the same whatever calls came before it.  One instance per kernel; every
+// read and update is under its mutex, so host threads may launch concurrently on any devices.
 struct LaunchFacts {
-  int per_cu;  // blocks per CU
+  int per_cu;  // blocks per CU at the call's dynamic LDS
   int cus;     // compute units of the current device
 };
 class LaunchCache {
@@ -30,24 +30,36 @@ class LaunchCache {
       cus_[dev] = 0;
       return hipGetLastError();
     }
-    if (per_cu_[dev] == 0 || lds > lds_[dev]) {
-      int per_cu = 0;
+    for (const Known& k : known_[dev])
+      if (k.per_cu != 0 && k.lds == lds) {
+        *out = LaunchFacts{k.per_cu, cus_[dev]};
+        return hipSuccess;
+      }
+    int per_cu = 0;
+    if (limit_[dev] == 0 || lds > limit_[dev]) {
       if (hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
         return hipGetLastError();
-      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, threads, lds) != hipSuccess)
-        return hipGetLastError();
-      per_cu_[dev] = per_cu > 0 ? per_cu : 1;
-      lds_[dev] = lds;
+      limit_[dev] = lds;
     }
-    *out = LaunchFacts{per_cu_[dev], cus_[dev]};
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kern, threads, lds) != hipSuccess)
+      return hipGetLastError();
+    if (per_cu < 1) per_cu = 1;
+    known_[dev][next_[dev]] = Known{lds, per_cu};
+    next_[dev] = (next_[dev] + 1) % SIZES;
+    *out = LaunchFacts{per_cu, cus_[dev]};
     return hipSuccess;
   }
 
  private:
-  static constexpr int MAXDEV = 64;
+  static constexpr int MAXDEV = 64, SIZES = 8;  // the sizes asked for last
+  struct Known {
+    size_t lds;
+    int per_cu;  // 0: no entry
+  };
   std::mutex mu_;
-  size_t lds_[MAXDEV] = {};
-  int per_cu_[MAXDEV] = {};
+  size_t limit_[MAXDEV] = {};
+  Known known_[MAXDEV][SIZES] = {};
+  int next_[MAXDEV] = {};
   int cus_[MAXDEV] = {};
 };
 
