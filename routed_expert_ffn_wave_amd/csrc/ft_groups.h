@@ -7,6 +7,7 @@
 // 全链路剖析", section 五) keeps only hot experts on the GPU and hands the others to another path.
 #pragma once
 #include "ft_device.h"
+#include "ft_group_lds.h"
 
 namespace ftk {
 
@@ -26,10 +27,6 @@ struct GroupList {
   int* item0;  // exclusive prefix of work items; item0[n] = total
   int n;
 };
-
-// LDS bytes of a group list for E experts: slot, row0, cnt and item0 arrays of E + 2 ints each, and
-// a few ints of scratch, rounded up to 16 bytes.
-__host__ __device__ inline size_t group_lds_bytes(int E) { return (((size_t)4 * (E + 2) + 4) * 4 + 15) & ~(size_t)15; }
 
 // Build the group list in LDS with wave 0 (ascending expert order, shared group last).
 // entry(e, slot, row0, cnt) gives expert e's slot (negative: none) and rows for e in [0, last);
