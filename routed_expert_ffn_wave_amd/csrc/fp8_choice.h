@@ -47,6 +47,7 @@ struct Choice {
   int rows, cols, per;
   float step, full, group, light;
   int lds;  // of the tiles kernels, 0 for the others
+  float many;  // > 0: a round of one block a unit from kManyExperts on
 };
 using Solo = TileCfg<64, 64, 1, 1, 2, false, 4>;
 using SoloWide = TileCfg<64, 64, 1, 1, 2, true, 4>;
@@ -60,13 +61,24 @@ using T256 = TileCfg<256, 256, 2, 4, 2, false>;
 using TWide = TileCfg<128, 128, 2, 2, 2, true>;
 using TWide256 = TileCfg<128, 256, 2, 4, 3, true>;  // by expert only
 constexpr int kLds = 160 * 1024;  // of a compute unit
+// From 350 experts on their table leaves room for one 64x128 block where two fit beside fewer.  256 blocks alone took 0.92 - 1.0 us
+// a step, half of 512 two by two 0.66 - 0.77, 256 64x64 blocks of as many experts 0.54 - 0.6: `many`, to the scale of the
+// constants they stand beside.  512 tokens, top 8 of 384 experts of 520 x 1040: 55 us with 128x256, chosen so, against 75 for
+// 64x128; 4096 tokens 94 with 128x128 against 144; over 280 sizes of 384 to 1024 experts 2 % less time, none slower.  (fp32 128x128
+// fits once from 735 experts on; counting that chose slower kernels for 768 and 1024 experts, 2 % more time over 130 sizes.)
+constexpr int many_experts() {
+  int E = 1;
+  while (2 * (T64::LDS + group_lds_bytes(E)) <= kLds) ++E;
+  return E;
+}
+constexpr int kManyExperts = many_experts();
 constexpr float kNever = 1e30f;
 constexpr Choice kBf16[] = {{16, 16, 1, 0.18f, 0.18f, 0.18f, 0.18f, 0},
                             {16, 32, 1, 0.26f, 0.26f, 0.26f, 0.26f, 0},
-                            {64, 64, 1, 0.33f, 0.31f, 0.32f, 0.32f, Solo::LDS},
+                            {64, 64, 1, 0.33f, 0.31f, 0.32f, 0.32f, Solo::LDS, 0.4f},
                             {64, 128, 1, 0.48f, 0.44f, kNever, kNever, Pair64::LDS},
                             {128, 128, 1, 0.66f, 0.66f, kNever, kNever, Pair128::LDS},
-                            {64, 128, 2, 0.71f, kNever, 0.95f, 0.95f, T64::LDS},
+                            {64, 128, 2, 0.71f, kNever, 0.95f, 0.95f, T64::LDS, 0.57f},
                             {128, 128, 1, 0.78f, kNever, 0.82f, 0.82f, T128::LDS},
                             {128, 256, 1, 0.93f, 1.15f, 1.25f, 0.85f, T128x256::LDS},
                             {256, 256, 1, 1.4f, 2.0f, 2.2f, 2.2f, T256::LDS}};
@@ -95,13 +107,15 @@ inline double cost(const Choice& c, const Fp8MatmulArgs& a) {
                : (a.M / c.rows + 2.0) * (a.E / 2 + 1) * ntn >= 2147483648.0)
     return kNever;
   double chunks = (a.M + c.rows - 1) / c.rows, round = c.full;
+  int per = c.per;
   if (a.E > 0) {  // each group has half a chunk to spare
     const Spread p = spread(a);
     chunks = std::max(p.groups, p.rows / c.rows + 0.5 * p.groups);
     round = 2 * p.rows <= c.rows * p.groups ? c.light : c.group;
+    if (a.E >= kManyExperts && c.many > 0) round = c.many, per = 1;
   }
   const double blocks = chunks * ntn;
-  return blocks <= 256 && round < kNever ? c.step : std::ceil(blocks / (256.0 * c.per)) * round;
+  return blocks <= 256 && round < kNever ? c.step : std::ceil(blocks / (256.0 * per)) * round;
 }
 
 // -1: none fits

@@ -15,3 +15,7 @@ def run_host(tmp_path, name):
 
 def test_blocks_per_unit_follow_the_call(tmp_path):
     run_host(tmp_path, "launch_cache")
+
+
+def test_choice_among_the_8_bit_products(tmp_path):
+    run_host(tmp_path, "fp8_choice")
