@@ -13,8 +13,8 @@
  * reentrant and capturable into a graph.  No call here needs a workspace or keeps any state, and no
  * result depends on the order in which blocks or atomics run: the same inputs give the same bits.
  * Outputs must not overlap inputs or each other.  Sizes of 0 rows or tokens are no-ops.  Sizes that one launch
- * cannot count are refused with FT_E_UNSUPPORTED: 2^29 scales, 2^26 pieces of 1024 values of token rows, 2^24
- * tokens (ft_moe_combine_grad), 2^23 tiles of a product.
+ * cannot count are refused with FT_E_UNSUPPORTED: more than 2^29 - 32 scales, 2^26 - 4 pieces of 1024 values of token
+ * rows, 2^24 - 1 tokens (ft_moe_combine_grad), 2^23 - 8 tiles of a product.
  *
  * 8-bit rows.  A row of K values (K % 16 == 0) is K e4m3fn codes and S = ft_moe_fp8_scale_cols(K) fp32
  * scales: scale b covers values 128 b .. 128 b + 127 (the last block may be shorter) and the columns

@@ -20,9 +20,8 @@ int check_rows_fp8(int rows, int K, const char* rows_name, const char* K_name) {
   REQUIRE(rows >= 0, FT_E_INVAL, "%s must be >= 0 (got %d)", rows_name, rows);
   REQUIRE(K > 0 && K % 16 == 0 && K <= (1 << 20), FT_E_INVAL, "%s must be a positive multiple of 16, at most 2^20 (got %d)",
           K_name, K);
-  // 8 lanes per scale, under the 2^32 threads of a launch
-  REQUIRE((long long)rows * fp8_scale_cols(K) < (1LL << 29), FT_E_UNSUPPORTED, "%s too large (%d rows of %d values)",
-          rows_name, rows, K);
+  REQUIRE(launch_fits((long long)rows * fp8_scale_cols(K), kRowsScales, kRowsThreads), FT_E_UNSUPPORTED,
+          "%s too large (%d rows of %d values)", rows_name, rows, K);
   return FT_OK;
 }
 
@@ -31,8 +30,9 @@ int check_pairs(int T, int E, int k, int d, int multiple) {
   if (rc) return rc;
   REQUIRE(d > 0 && d % multiple == 0 && d <= (1 << 20), FT_E_INVAL,
           "d must be a positive multiple of %d, at most 2^20 (got %d)", multiple, d);
-  // a wave per token and 4 KiB of a row, under the 2^32 threads of a launch
-  REQUIRE((long long)T * ((d + 1023) / 1024) < (1LL << 26), FT_E_UNSUPPORTED, "T too large (%d tokens of %d values)", T, d);
+  // 1024 values: 4 KiB in fp32
+  REQUIRE(launch_fits((long long)T * ((d + 1023) / 1024), kDispatchWaves, kDispatchThreads), FT_E_UNSUPPORTED,
+          "T too large (%d tokens of %d values)", T, d);
   return FT_OK;
 }
 

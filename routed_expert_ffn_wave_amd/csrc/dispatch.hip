@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const void* __restric
 hipError_t launch_dispatch(const void* x, const PairTab& tab, int T, int d, void* xs, bool f32, hipStream_t s) {
   const int pieces = d / 8 * (f32 ? 2 : 1);
   const uint32_t nseg = (uint32_t)(pieces + 64 * SEG_U - 1) / (64 * SEG_U), nwork = (uint32_t)T * nseg;
-  hipLaunchKernelGGL(dispatch_kernel, dim3((nwork + 3) / 4), dim3(256), 0, s, (const u32x4*)x, tab, nwork, nseg, pieces,
+  hipLaunchKernelGGL(dispatch_kernel, dim3((nwork + kDispatchWaves - 1) / kDispatchWaves), dim3(kDispatchThreads), 0, s, (const u32x4*)x, tab, nwork, nseg, pieces,
                      (u32x4*)xs);
   return hipGetLastError();
 }
@@ -235,7 +235,7 @@ hipError_t launch_dispatch(const void* x, const PairTab& tab, int T, int d, void
 hipError_t launch_dispatch_grad(const void* dxs, const PairTab& tab, int T, int d, void* dx, bool f32, hipStream_t s) {
   const int pieces = d / 8 * (f32 ? 2 : 1);
   const uint32_t nseg = (uint32_t)(pieces + 64 * SEG_U - 1) / (64 * SEG_U), nwork = (uint32_t)T * nseg;
-  const dim3 grid((nwork + 3) / 4), block(256);
+  const dim3 grid((nwork + kDispatchWaves - 1) / kDispatchWaves), block(kDispatchThreads);
   if (f32)
     hipLaunchKernelGGL(dispatch_grad_kernel<true>, grid, block, 0, s, (const u32x4*)dxs, tab, nwork, nseg, pieces,
                        (u32x4*)dx);

@@ -100,10 +100,11 @@ inline Spread spread(const Fp8MatmulArgs& a) {
 
 inline double cost(const Choice& c, const Fp8MatmulArgs& a) {
   if (c.lds + (a.E > 0 ? group_lds_bytes(a.E) : 0) > kLds) return kNever;
-  // Counts that have to fit: the threads of a dense launch (at most 512 a block) in 32 bits, the tiles of all groups
-  // in an int whatever the table holds (one that does not ascend can give all rows to every second expert).
+  // Counts that have to fit: the threads of a dense launch (at most 512 a block, blocks in multiples of 8) in 32 bits, the
+  // tiles of all groups in an int whatever the table holds (one that does not ascend can give all rows to every second
+  // expert).
   const double ntn = (a.N + c.cols - 1) / c.cols;
-  if (a.E == 0 ? ((a.M + c.rows - 1) / c.rows) * ntn >= 1 << 23
+  if (a.E == 0 ? ((a.M + c.rows - 1) / c.rows) * ntn > (1 << 23) - 8
                : (a.M / c.rows + 2.0) * (a.E / 2 + 1) * ntn >= 2147483648.0)
     return kNever;
   double chunks = (a.M + c.rows - 1) / c.rows, round = c.full;

@@ -132,7 +132,7 @@ hipError_t launch_rows_fp8(int kind, const void* x, int rows, int K, uint8_t* co
                            hipStream_t s) {
   const int S = fp8_scale_cols(K);
   const uint32_t n = (uint32_t)rows * (uint32_t)S;  // the caller checked that it fits
-  const dim3 grid((n + 31) / 32), block(256);
+  const dim3 grid((n + kRowsScales - 1) / kRowsScales), block(kRowsThreads);
   const PairTab t = tab ? *tab : PairTab{};
 #define LAUNCH(KIND, SORT) \
   hipLaunchKernelGGL((rows_fp8_kernel<KIND, SORT>), grid, block, 0, s, x, n, K, S, codes, scales, t)

@@ -24,6 +24,15 @@ struct PairTab {
 
 inline __host__ __device__ int fp8_scale_cols(int K) { return (K + 511) / 512 * 4; }
 
+// Whether `items` fit a launch of blocks of `threads` threads with `per` items each: a launch counts its threads, whole
+// blocks of them, in 32 bits.
+inline bool launch_fits(long long items, int per, int threads) {
+  return (items + per - 1) / per * threads < (1LL << 32);
+}
+
+constexpr int kRowsThreads = 256, kRowsScales = 32;      // a block of the 8-bit rows: 8 lanes a scale
+constexpr int kDispatchThreads = 256, kDispatchWaves = 4;  // a block of the dispatch: a wave moves 4 KiB of a token's row
+
 enum { ROWS_BF16 = 0, ROWS_F32 = 1, ROWS_SWIGLU = 2 };
 // 8-bit rows of `rows` rows of K values; tab: null, or the pairs whose rows get them
 hipError_t launch_rows_fp8(int kind, const void* x, int rows, int K, uint8_t* codes, float* scales, const PairTab* tab,

@@ -37,7 +37,23 @@ static void blocks_that_fit() {
   }
 }
 
+// A dense launch's threads, blocks in multiples of 8, stay under 2^32.
+static void dense_launches() {
+  Fp8MatmulArgs a{};
+  a.K = 16, a.n_slots = 1;
+  for (int tiles = (1 << 23) - 18; tiles <= (1 << 23); tiles += 2) {
+    a.N = 512, a.M = (tiles / 2 - 1) * 256 + 1;  // so many tiles of the largest kernel, more of every other one
+    for (int bf16 = 0; bf16 < 2; ++bf16) {
+      const int got = bf16 ? choose<true>(a) : choose<false>(a);
+      const bool fits = bf16 && (tiles + 7) / 8 * 8LL * T256::NT < 1LL << 32;
+      EXPECT((got >= 0) == fits, "%d tiles, bf16 %d: kernel %d", tiles, bf16, got);
+    }
+  }
+  EXPECT(launch_fits((1LL << 29) - 32, 32, 256) && !launch_fits((1LL << 29) - 31, 32, 256), "launch_fits");
+}
+
 int main() {
   blocks_that_fit();
+  dense_launches();
   return g_bad;
 }

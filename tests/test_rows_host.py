@@ -172,3 +172,22 @@ def test_slot_counts_in_flags():
     call = lambda flags, out=None: L.ft_moe_combine(A, None, A, A, A, A, 4, 8, 2, 256, out, None, flags, None)  # noqa: E731
     err(call(ft.FT_N_SLOTS(5) | ft.FT_OUT_BF16), ft.FT_E_INVAL, "out is null")
     err(call(-(2 ** 31)), ft.FT_E_INVAL, "unknown flags 0x80000000")
+
+
+def test_last_sizes_that_a_launch_counts():
+    """Whole blocks count: the last sizes below a launch's 2^32 threads pass the check (and fail at the next one, a null
+    pointer), the sizes after them are refused."""
+    quant = lambda rows, K: L.ft_moe_quant_fp8(None, rows, K, B, B, 0, None)  # noqa: E731
+    swiglu = lambda rows, K: L.ft_moe_swiglu_fp8(None, rows, K, B, B, None)  # noqa: E731
+    for call in (quant, swiglu):
+        err(call((1 << 27) - 8, 512), ft.FT_E_INVAL, "is null")
+        for rows in range((1 << 27) - 7, (1 << 27) + 1):
+            err(call(rows, 512), ft.FT_E_UNSUPPORTED, "rows too large")
+    for name in ("dispatch", "dispatch_grad", "dispatch_fp8"):
+        err(_one(name, T=(1 << 26) - 4, d=1024, k=1, x=None) if name != "dispatch_fp8" else _one(name, T=(1 << 26) - 4, d=512, k=1, x=None),
+            ft.FT_E_INVAL, "is null")
+        for T in range((1 << 26) - 3, (1 << 26) + 1):
+            err(_one(name, T=T, d=1024, k=1, x=None), ft.FT_E_UNSUPPORTED, "T too large")
+    err(_one("combine_grad", T=(1 << 24) - 1, d=8, k=1, x=None), ft.FT_E_INVAL, "is null")
+    # 47 x 178481 tiles of 256 x 256: one less than 2^23, but blocks are launched in multiples of 8
+    err(L.ft_moe_fp8_matmul(A, A, 178480 * 256 + 1, A, A, 47 * 256, 16, B, ft.FT_OUT_BF16, None), ft.FT_E_UNSUPPORTED, "product too large")
