@@ -275,7 +275,10 @@ class Fp8MoELayer:
     fp32 scales per 128 x 128 block (s13, s2); slot_of_expert int32 [E], -1 for experts that are not resident
     (left to the residual mask; entries outside [0, n_slots) count as -1).  Every buffer is allocated here for a
     fixed (T, k): forward() allocates nothing and can be captured into a graph.  The accuracy is that of one e4m3 term per activation,
-    where MoELayer carries two.  One forward() at a time: its results and buffers are the next one's."""
+    where MoELayer carries two.  One forward() at a time: its results and buffers are the next one's.  forward() runs on
+    any stream: the buffers are free of earlier work when the layer is made (that waits for the current stream), and
+    their memory is kept for the streams they were used on (Tensor.record_stream) when the layer goes; a graph that
+    holds a forward() needs the layer as long as it is replayed."""
 
     def __init__(self, w13, s13, w2, s2, slot_of_expert, k: int, T: int, out_bf16: bool = False):
         dev, (self.n_slots, I2, self.d) = _first(w13, "w13", 3, _CODES)
@@ -304,6 +307,19 @@ class Fp8MoELayer:
         self.h8, self.hs = new(P, self.I, dtype=e4), new(P, S(self.I), dtype=f32)
         self.y_sorted = new(P, self.d, dtype=bf)
         self.out, self.mask = new(T, self.d, dtype=bf if out_bf16 else f32), new(max(T, 1), dtype=i32)
+        self._buffers = (self.ids, self.w, self.inv, self.counts, self.offsets, self.gather, self.perm_ws, self.x8, self.xs, self.gu,
+                         self.h8, self.hs, self.y_sorted, self.out, self.mask)
+        # The buffers are memory of the stream that is current here, whose work on tensors freed before may still run.
+        self._streams = {_raw_stream(dev)}
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+
+    def _use_on(self, stream):
+        """Keeps the buffers' memory, once they are freed, until the work on `stream` is done."""
+        for b in self._buffers:
+            b.record_stream(stream)
+        self._streams.add(stream.cuda_stream)
 
     def forward(self, logits, x, stream=None):
         """logits fp32 [T][E], x bf16 [T][d] -> (out [T][d], residual mask [T])."""
@@ -314,6 +330,8 @@ class Fp8MoELayer:
         pl = _take(logits, "logits", (_F32,), (T, E), dev)
         if T == 0:
             return self.out, self.mask[:0]
+        if (_raw_stream(dev) if stream is None else stream.cuda_stream) not in self._streams:
+            self._use_on(torch.cuda.current_stream(dev) if stream is None else stream)
         inv, slot = self.inv.view(T, k), self.slot_of
         pi, pw, pv, pt = self.ids.data_ptr(), self.w.data_ptr(), inv.data_ptr(), slot.data_ptr()
         _run(lib.ft_moe_route, dev, stream, pl, T, E, k, pi, pw)

@@ -788,3 +788,58 @@ def test_four_calls_with_slots_past_the_bank():
         got.append([v.clone() for v in layer.forward(li.logits.cuda(), li.x.cuda())])
     assert torch.isfinite(got[0][0]).all()
     assert same_bits(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ---------------------------------------------------------------------------------------------- the layer's buffers and streams
+
+def zeroed_copies(layer):
+    """Tensors of the buffers' sizes, zeroed on the current stream (zeros are harmless tables)."""
+    return [torch.zeros_like(b.view(torch.uint8)) for b in layer._buffers]
+
+
+def long_work():
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(8):
+        busy = busy @ busy * 1e-3
+
+
+def test_layer_made_while_its_stream_is_busy():
+    """Work that still writes freed tensors of the buffers' sizes does not reach a forward() on another stream."""
+    T, E, k, d, I = 64, 8, 4, 256, 128
+    w13, s13, w2, s2, slot, logits, x = layer_inputs(5, T, E, k, d, I, E)
+    first = ft.Fp8MoELayer(w13, s13, w2, s2, slot, k, T)
+    want = first.forward(logits, x)[0].clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for use in (lambda ly: ly.forward(logits, x, stream=side), None):
+        long_work()
+        late = zeroed_copies(first)
+        del late
+        layer = ft.Fp8MoELayer(w13, s13, w2, s2, slot, k, T)
+        if use:
+            out, _ = use(layer)
+        else:
+            with torch.cuda.stream(side):
+                out, _ = layer.forward(logits, x)
+        torch.cuda.synchronize()
+        assert same_bits(out, want)
+
+
+def test_layer_freed_while_another_stream_uses_it():
+    """Tensors made on the constructing stream after the layer is gone do not overwrite what a forward() on another
+    stream still works on."""
+    T, E, k, d, I = 64, 8, 4, 256, 128
+    w13, s13, w2, s2, slot, logits, x = layer_inputs(6, T, E, k, d, I, E)
+    first = ft.Fp8MoELayer(w13, s13, w2, s2, slot, k, T)
+    want = first.forward(logits, x)[0].clone()
+    side = torch.cuda.Stream()
+    for given in (True, False):
+        layer = ft.Fp8MoELayer(w13, s13, w2, s2, slot, k, T)
+        with torch.cuda.stream(side):
+            long_work()
+            out = (layer.forward(logits, x, stream=side) if given else layer.forward(logits, x))[0]
+        del layer
+        over = zeroed_copies(first)
+        torch.cuda.synchronize()
+        assert same_bits(out, want)
+        del over

@@ -191,3 +191,47 @@ def test_last_sizes_that_a_launch_counts():
     err(_one("combine_grad", T=(1 << 24) - 1, d=8, k=1, x=None), ft.FT_E_INVAL, "is null")
     # 47 x 178481 tiles of 256 x 256: one less than 2^23, but blocks are launched in multiples of 8
     err(L.ft_moe_fp8_matmul(A, A, 178480 * 256 + 1, A, A, 47 * 256, 16, B, ft.FT_OUT_BF16, None), ft.FT_E_UNSUPPORTED, "product too large")
+
+
+def test_layer_orders_its_buffers_with_the_streams(monkeypatch):
+    """With stand-ins for the GPU: making a layer waits for the current stream, and a forward on a stream that did not make
+    it records every buffer for that stream, once."""
+    import contextlib
+    import types
+
+    from routed_expert_ffn_wave_amd import rows
+    made, waits, used = [], [], []
+
+    class Buffer(torch.Tensor):
+        def record_stream(self, stream):
+            used.append((id(self), stream.cuda_stream))
+
+    def new(shape, dtype, dev, stream=None):
+        made.append(torch.zeros(shape).to(dtype).as_subclass(Buffer))
+        return made[-1]
+
+    streams = {n: types.SimpleNamespace(cuda_stream=n, device_index=0, synchronize=lambda n=n: waits.append(n)) for n in (1, 2, 3)}
+    current = [1]
+    monkeypatch.setattr(rows, "_new", new)
+    monkeypatch.setattr(rows, "_first", lambda t, name, dims, dtypes, stream=None: (0, t.shape))
+    monkeypatch.setattr(rows, "_take", lambda t, name, dtypes, shape, dev: t.data_ptr())
+    monkeypatch.setattr(rows, "_run", lambda *a: None)
+    monkeypatch.setattr(rows, "_raw_stream", lambda dev: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: streams[current[0]])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    z = lambda *s, dtype=torch.float8_e4m3fn: torch.zeros(s).to(dtype)  # noqa: E731
+    layer = rows.Fp8MoELayer(z(2, 64, 64), z(2, 1, 1, dtype=torch.float32), z(2, 64, 32), z(2, 1, 1, dtype=torch.float32),
+                             torch.zeros(4, dtype=torch.int32), 2, 4)
+    assert waits == [1] and len(made) == 15
+    args = (torch.zeros(4, 4), torch.zeros(4, 64, dtype=torch.bfloat16))
+    layer.forward(*args)
+    assert used == []
+    layer.forward(*args, stream=streams[2])
+    assert sorted(used) == sorted((id(b), 2) for b in made)
+    layer.forward(*args, stream=streams[2])
+    current[0] = 3
+    layer.forward(*args)
+    layer.forward(*args)
+    assert sorted(used) == sorted((id(b), n) for b in made for n in (2, 3))
+    assert waits == [1]
