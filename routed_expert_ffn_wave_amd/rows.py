@@ -41,9 +41,10 @@ _CODES = (_E4, _U8)
 _FLOATS = (_BF, _F32)
 _INTS = (_I32,)
 
-# Calls of a few microseconds: the stream handle and the current device are asked for without building objects.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# Calls of a few microseconds: the stream handle and the current device are asked for without building objects, where
+# this torch has the functions for it (a build without GPU support has not).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _refuse(text: str):

@@ -4,6 +4,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -235,3 +236,17 @@ def test_layer_orders_its_buffers_with_the_streams(monkeypatch):
     layer.forward(*args)
     assert sorted(used) == sorted((id(b), n) for b in made for n in (2, 3))
     assert waits == [1]
+
+
+def test_import_without_torchs_inner_functions():
+    """The package imports under a torch build that lacks them, and asks torch's public functions instead."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import types\n"
+            "torch.cuda.current_stream = lambda dev: types.SimpleNamespace(cuda_stream=40 + dev)\n"
+            "import routed_expert_ffn_wave_amd as ft\n"
+            "from routed_expert_ffn_wave_amd import rows\n"
+            "assert rows._raw_stream(2) == 42 and rows._current_device is torch.cuda.current_device\n"
+            "assert ft.ft_moe_fp8_scale_cols(513) == 8\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
