@@ -10,8 +10,12 @@
 namespace ftk {
 
 // Which kernel: the one whose blocks, taken in rounds of the 256 compute units (or as many times that as fit),
-// are through first.  `step` is the measured time of one 128-block of K in a round, in us on an MI355X; `full`
-// where rounds follow each other.  M rows x 4096 columns, K = 7168, us a call (bf16 results; / 2, / 4: that many shares of K):
+// are through first.  `step` stands for the time of one 128-block of K in a round, in us on an MI355X; `full`
+// where rounds follow each other.  The constants are fitted to the times below, so that the fastest kernel there has the least
+// cost: only their order within a list counts (the 16x32 kernel has 0.26 beside the bf16 kernels by expert and 0.19 beside the
+// fp32 ones, and takes the same time).  By expert, over 800 measured sizes (4 to 256 experts, N of 256 to 4096, K of 256
+// to 7168, 1 to 4096 tokens) the kernel chosen takes 7 % more time than the fastest on average, and over 15 % more at every
+// sixth size.  M rows x 4096 columns, K = 7168, us a call (bf16 results; / 2, / 4: that many shares of K):
 //   M             16     32     64     128    256    512    1024   2048   4096   8192
 //   16x16         10.2   18.3   34     65     -      -      -      -      -      -
 //   16x32         14.0   13.4   24     46     88     -      -      -      -      -
@@ -125,7 +129,8 @@ int choose(const Fp8MatmulArgs& a) {
   const Choice* c = BF16 ? kBf16 : kF32;
   // A few rows a group: bound by the weights' bytes, and with long rows 16 x 32 blocks stream them fastest (top 8 of
   // 256 experts, 96 resident, K = 7168, 16 / 32 tokens: 176 - 198 / 281 us, 5.9 TB/s; 64 x 128 tiles 207 / 293,
-  // 64 x 64 210; with K = 2048 and 4 / 16 tokens 21 / 52 us against 20 / 44 for 64 x 128)
+  // 64 x 64 210; with K = 2048 and 4 / 16 tokens 21 / 52 us against 20 / 44 for 64 x 128; where between the two lengths
+  // the border lies was not measured)
   if (a.E > 0 && a.K >= 4096) {
     const Spread p = spread(a);
     if (p.rows <= 3 * p.groups && cost(c[1], a) < kNever) return 1;

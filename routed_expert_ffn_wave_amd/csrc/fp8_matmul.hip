@@ -5,8 +5,8 @@
 // fp8_rows_kernel: few rows.  A block takes 16 NF weight rows and up to 16 activation rows over the whole of
 // K; its 8 waves take the 128-blocks in turn and their sums meet in LDS in a fixed order, so a single row
 // already keeps 8 waves a block busy with weight loads.  Codes are widened to bf16 (exact) and
-// multiplied on v_mfma_f32_16x16x32_bf16: products exact, fp32 sums.  Bound by the weights' bytes: 38 experts
-// of 4096 x 7168 with one to three rows each in 183 us, 5.9 TB/s.  (More rows a block do not pay: a lane's
+// multiplied on v_mfma_f32_16x16x32_bf16: products exact, fp32 sums.  Bound by the weights' bytes: 37 experts
+// of 4096 x 7168 with one to three rows each, 1087 MB, in 183 us, 5.9 TB/s.  (More rows a block do not pay: a lane's
 // 16-byte chunks of 16 different rows cost the address unit 64 cycles a load, where 8 lanes a row cost 16;
 // 64 x 32 blocks of 128 rows took 28 us against 18 for the 64 x 64 tiles loaded through LDS.)
 #include "fp8_choice.h"

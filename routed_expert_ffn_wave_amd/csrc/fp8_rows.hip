@@ -8,7 +8,8 @@
 // top = m 2^e, y = x * (448 / 2^e) is exact for bf16 x (8 + 3 significant bits), q0 = y * rcp(m), and one
 // residual step q = q0 + (y - q0 m) * rcp(m).  For bf16 x a quotient is either a rounding border of
 // e4m3 or at least 2^-13 away from one (numerator 11 bits, denominator 8, border 5), and a border is hit
-// exactly by the residual step, so the codes are the exact ones.
+// exactly by the residual step, so the codes are the exact ones.  (For fp32 x, y is rounded too: quotients are off by
+// up to 3 roundings, and a code may be the other neighbour of a border that close.)
 //
 // In expert order a token's row is quantised once and its codes are stored at each of its k rows:
 // x is read once instead of k times.

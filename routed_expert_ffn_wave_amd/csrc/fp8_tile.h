@@ -19,8 +19,9 @@
 // larger tiles a wave need more than the 256 registers that two waves a SIMD have.
 //
 // Exact products (WIDE) convert codes to bf16 and take twice the matrix cycles: 8192 x 4096 x 7168 in 434 - 505 us.
-// The conversions and multiply-adds do not run beside these matrix instructions (459 k cycles of matrix
-// instructions and 395 k of others add up in 946 k), so a loop ordered by hand like the 8-bit one took the same time.
+// In its loop the conversions and multiply-adds do not run beside the matrix instructions (459 k cycles of matrix
+// instructions and 395 k of others add up in 946 k), though the 8-bit loop's multiply-adds do; every wave converts operands that
+// up to four waves share.  A loop ordered by hand like the 8-bit one took the same time; why is not known.
 #pragma once
 #include <type_traits>
 

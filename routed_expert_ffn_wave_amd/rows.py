@@ -234,7 +234,9 @@ def _product_out(out, out_dtype, shape, dev: int, stream):
 
 def ft_moe_fp8_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """8-bit rows a [M][K] (scales [M][S]) times w [N][K] transposed (fp32 scales [ceil(N/128)][ceil(K/128)]):
-    [M][N] in bf16, or in fp32 with out_dtype=torch.float32 (or an fp32 `out`)."""
+    [M][N] in bf16, or in fp32 with out_dtype=torch.float32 (or an fp32 `out`).  fp32 results add exact products in
+    fp32; bf16 results of more than a few rows cut each product at 2^-13 of the largest of its group of 8 before adding,
+    which shows where products cancel."""
     dev, (M, K) = _first(a, "a", 2, _CODES, stream)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         _refuse("w must be a tensor of shape [N, K]")
@@ -250,8 +252,8 @@ def ft_moe_fp8_matmul(a, a_scales, w, w_scales, out=None, out_dtype=torch.bfloat
 def ft_moe_fp8_grouped_matmul(a, a_scales, w, w_scales, offsets, slot_of_expert, out=None, out_dtype=torch.bfloat16,
                               stream=None):
     """8-bit rows a [P][K] in expert order, each expert's rows times its matrix of w [n_slots][N][K] transposed
-    (fp32 scales [n_slots][ceil(N/128)][ceil(K/128)]): [P][N] in bf16 or fp32.  Rows of experts without a slot
-    are left as they were (with out=None: unset)."""
+    (fp32 scales [n_slots][ceil(N/128)][ceil(K/128)]): [P][N] in bf16 or fp32, as in ft_moe_fp8_matmul.  Rows of
+    experts without a slot are left as they were (with out=None: unset)."""
     dev, (P, K) = _first(a, "a", 2, _CODES, stream)
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         _refuse("w must be a tensor of shape [n_slots, N, K]")
