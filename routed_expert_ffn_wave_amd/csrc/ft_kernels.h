@@ -51,7 +51,7 @@ class LaunchCache {
   }
 
  private:
-  static constexpr int MAXDEV = 64, SIZES = 8;  // the sizes asked for last
+  static constexpr int MAXDEV = 64, SIZES = 32;  // the sizes asked for last (the decode layer has one for each of up to 16 tokens)
   struct Known {
     size_t lds;
     int per_cu;  // 0: no entry

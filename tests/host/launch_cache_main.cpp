@@ -42,7 +42,12 @@ int main() {
   const int known = g_queries;
   expect(70000, 2);
   if (g_queries != known) bad = 1, std::printf("asked again for a known size\n");
-  for (size_t lds = 1000; lds < 31000; lds += 1000) expect(lds, (int)(163840 / (lds + 1)));  // more sizes than are kept
+  for (int pass = 0; pass < 2; ++pass) {  // a size for each of 16 batches in turn, two shapes
+    const int before = g_queries;
+    for (int q = 1; q <= 16; ++q) expect(1000 * q, 163840 / (1000 * q + 1)), expect(1000 * q + 500, 163840 / (1000 * q + 501));
+    if (pass && g_queries != before) bad = 1, std::printf("asked again for 32 sizes\n");
+  }
+  for (size_t lds = 1000; lds < 60000; lds += 1000) expect(lds, (int)(163840 / (lds + 1)));  // more sizes than are kept
   expect(70000, 2);
   expect(163839, 1);
   expect(400000, 1);  // the caller's launch fails, not the count
