@@ -1,0 +1,119 @@
+// Products of bf16 rows with one matrix per expert, the gradient of the rows and the gradient of the matrices: what the
+// expert FFN of a training step is made of (the expert groups of the FreeToken walk-through
+// "深入FreeToken架构…全链路剖析", section 五).
+//   forward        out[p][n]   = sum_k a[p][k] w[e][n][k]
+//   rows           da[p][k]    = sum_n dout[p][n] w[e][n][k]
+//   matrices       dw[e][n][k] = sum_{p of e} dout[p][n] a[p][k]
+// bf16 products are exact in fp32 and added there by the matrix instructions; results are rounded once.
+#include "bf16_tile.h"
+#include "ft_groups.h"
+#include "ft_kernels.h"
+#include "ft_products.h"
+
+namespace ftk {
+namespace {
+
+__device__ __forceinline__ bool group_of(const RowGroups& s, int e, int& slot, int& row0, int& cnt) {
+  slot = s.slot_of ? s.slot_of[e] : e;
+  row0 = min(max(s.offsets[e], 0), s.P);
+  cnt = max(min(max(s.offsets[e + 1], 0), s.P) - row0, 0);
+  return (uint32_t)slot < s.n_slots;
+}
+
+template <class ItemsOf>
+__device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, int* tmp, ItemsOf items_of) {
+  build_group_list(
+      s.E, g, tmp, [&](int e, int& slot, int& row0, int& cnt) { return e < s.E && group_of(s, e, slot, row0, cnt) && cnt > 0; }, items_of);
+}
+
+// Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the tile list, so that tiles that run
+// together share rows and matrices through its L2.
+template <class C, bool GRAD, bool BF16>
+__global__ __launch_bounds__(C::NT, 2) void grouped_tile_kernel(GroupedArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
+  const int ntn = (cols + C::BN - 1) / C::BN;
+  const int E2 = a.g.E + 2;
+  int* li = (int*)(lds + C::LDS);
+  GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
+  list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + C::BM - 1) / C::BM * ntn; });
+  const int nitems = gl.item0[gl.n];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = gridDim.x / 8, lb = (blockIdx.x % 8) * per + blockIdx.x / 8;  // gridDim.x % 8 == 0
+  for (int it = lb; it < nitems; it += gridDim.x) {
+    const int gi = find_group(gl.item0, gl.n, it);
+    const int local = __builtin_amdgcn_readfirstlane(it - gl.item0[gi]);
+    const int slot = __builtin_amdgcn_readfirstlane(gl.slot[gi]);
+    const int row0 = __builtin_amdgcn_readfirstlane(gl.row0[gi]), cnt = __builtin_amdgcn_readfirstlane(gl.cnt[gi]);
+    const int m0 = local / ntn * C::BM, n0 = local % ntn * C::BN, rows = min(C::BM, cnt - m0);
+    const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
+    f32x4 acc[C::MF][C::NF];
+    const Operand ro{a.a + (size_t)(row0 + m0) * red, red, rows};
+    const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0)};
+    bf16_tile<C, false, GRAD>(ro, co, red, lds, acc);
+    uint8_t* out = (uint8_t*)a.out + (size_t)(row0 + m0) * cols * (BF16 ? 2 : 4);
+    store_rows<C::MF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 64, cols, lane);
+  }
+}
+
+template <class C, bool BF16, bool ADD>
+__global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int ntm = (a.N + C::BM - 1) / C::BM, ntn = (a.K + C::BN - 1) / C::BN, tiles = ntm * ntn;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e = blockIdx.x / tiles, t = blockIdx.x % tiles;
+  int slot, row0, cnt;
+  if (!group_of(a.g, e, slot, row0, cnt)) return;
+  row0 = __builtin_amdgcn_readfirstlane(row0), cnt = __builtin_amdgcn_readfirstlane(cnt);
+  if (ADD && cnt == 0) return;
+  const int m0 = t / ntn * C::BM, n0 = t % ntn * C::BN;
+  f32x4 acc[C::MF][C::NF];
+  const Operand ro{a.dout + (size_t)row0 * a.N + m0, a.N, min(C::BM, a.N - m0)};
+  const Operand co{a.a + (size_t)row0 * a.K + n0, a.K, min(C::BN, a.K - n0)};
+  bf16_tile<C, true, true>(ro, co, cnt, lds, acc);
+  uint8_t* out = (uint8_t*)a.dw + ((size_t)e * a.N + m0) * a.K * (BF16 ? 2 : 4);
+  store_rows<C::MF, BF16, ADD>(acc, out, a.K, wv / C::WN * 16 * C::MF, ro.rows, n0 + wv % C::WN * 64, a.K, lane);
+}
+
+template <class C, bool GRAD, bool BF16>
+hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
+  static LaunchCache cache;
+  LaunchFacts f;
+  const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
+  const long long ntn = (cols + C::BN - 1) / C::BN, ntm = (P + C::BM - 1) / C::BM;
+  if ((P / C::BM + 2LL) * (E / 2 + 1) * ntn >= 1LL << 31) return hipErrorNotSupported;
+  const size_t lds = C::LDS + group_lds_bytes(E);
+  hipError_t e = cache.get((const void*)grouped_tile_kernel<C, GRAD, BF16>, C::NT, lds, &f);
+  if (e != hipSuccess) return e;
+  const long long upper = ((ntm + (E < P ? E : P)) * ntn + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
+  hipLaunchKernelGGL((grouped_tile_kernel<C, GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(C::NT), lds, s, a);
+  return hipGetLastError();
+}
+
+template <class C, bool BF16, bool ADD>
+hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
+  static LaunchCache cache;
+  LaunchFacts f;
+  const long long blocks = (long long)((a.N + C::BM - 1) / C::BM) * ((a.K + C::BN - 1) / C::BN) * a.g.E;
+  if (blocks * C::NT >= 1LL << 32) return hipErrorNotSupported;
+  hipError_t e = cache.get((const void*)wgrad_tile_kernel<C, BF16, ADD>, C::NT, C::LDS, &f);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((wgrad_tile_kernel<C, BF16, ADD>), dim3((uint32_t)blocks), dim3(C::NT), C::LDS, s, a);
+  return hipGetLastError();
+}
+
+using T128 = Bf16Cfg<128, 128, 2, 2, 2>;
+
+}  // namespace
+
+hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s) {
+  if (kind == 0) return a.out_bf16 ? launch_tiles<T128, false, true>(a, s) : launch_tiles<T128, false, false>(a, s);
+  return a.out_bf16 ? launch_tiles<T128, true, true>(a, s) : launch_tiles<T128, true, false>(a, s);
+}
+
+hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {
+  if (a.out_bf16) return launch_wgrad_tiles<T128, true, false>(a, s);
+  return a.add ? launch_wgrad_tiles<T128, false, true>(a, s) : launch_wgrad_tiles<T128, false, false>(a, s);
+}
+
+}  // namespace ftk

@@ -1,0 +1,319 @@
+"""Product calls on the GPU against their definitions in 64 bits (products_ref.py holds the references and derives the
+bounds)."""
+import pytest
+import torch
+
+import products_ref as ref
+import routed_expert_ffn_wave_amd as ft
+import rows_ref
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+FILL = 7.0  # what a call leaves alone holds
+NAN = float("nan")
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def filled(*shape, dtype):
+    return torch.full(shape, FILL, device="cuda").to(dtype)
+
+
+def normal(g, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=g) * scale).to(BF)
+
+
+def same_bits(a, b):
+    a, b = a.cpu().contiguous(), b.cpu().contiguous()
+    return a.dtype == b.dtype and torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def sizes(g, E, P, empty=0.3):
+    """Offsets of E experts with P rows in all, some without any and some with most."""
+    cuts = torch.randint(0, P + 1, (E - 1,), generator=g)
+    cuts[torch.rand(E - 1, generator=g) < empty] = 0
+    return torch.cat([torch.zeros(1), torch.sort(cuts)[0], torch.full((1,), P)]).int()
+
+
+def check_forward(a, w, off, slot, dtype, grad):
+    """grad: the rows' gradient, a being dout [P][N]."""
+    P = a.shape[0]
+    wt = w.transpose(1, 2).contiguous() if grad else w
+    has, want, mag = ref.forward(torch.nan_to_num(a), wt, off, slot, None)
+    a = a.clone()
+    a[~has] = NAN  # rows of experts without a matrix are not read into a result
+    out = filled(P, wt.shape[1], dtype=dtype)
+    call = ft.ft_moe_grouped_matmul_grad if grad else ft.ft_moe_grouped_matmul
+    kw = {"da": out} if grad else {"out": out}
+    got = call(a.cuda(), w.cuda(), off.cuda(), slot_of_expert=dev(slot), **kw)
+    assert got is out and torch.equal(out[~has.cuda()].cpu(), torch.full((int((~has).sum()), wt.shape[1]), FILL).to(dtype))
+    err = (out.cpu().double() - want).abs()[has]
+    assert (err <= ref.sum_bound(want, mag, a.shape[1], dtype)[has]).all(), err.max()
+
+
+# P, E, held (None: no table), N, K
+GROUPS = [(1, 1, None, 8, 8), (3, 4, 2, 16, 24), (8, 128, 128, 72, 64), (17, 5, 3, 136, 72), (64, 2, 2, 128, 128), (129, 3, 3, 264, 200),
+          (300, 7, None, 520, 136), (333, 64, 40, 256, 520), (700, 9, 6, 1032, 776), (2000, 16, 16, 384, 1160), (5000, 4, 4, 1544, 328),
+          (16, 256, 96, 64, 2056), (1500, 1024, 700, 40, 48)]
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("P, E, held, N, K", GROUPS)
+def test_grouped_product(P, E, held, N, K, dtype, grad):
+    g = gen(P * E + N)
+    slot = None if held is None else rows_ref.routing(g, 0, E, 1, held)["slot"]
+    w = normal(g, E if held is None else held, N, K)
+    check_forward(normal(g, P, N if grad else K), w, sizes(g, E, P), slot, dtype, grad)
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("P", [1, 5, 90, 700])
+def test_grouped_product_of_odd_tables(P, grad):
+    """Slots past the bank and below -1, a matrix that three experts share, offsets below 0 and past P."""
+    g = gen(P)
+    E, N, K = 12, 72, 152
+    off = sizes(g, E, P, 0.0)
+    off[0], off[-1] = -5, P + 1000
+    slot = torch.tensor([0, 3, 3, -1, 5, 4, -2 ** 31, 2 ** 31 - 1, 1, 3, 2, 0]).int()  # of 5
+    check_forward(normal(g, P, N if grad else K), normal(g, 5, N, K), off, slot, BF, grad)
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_grouped_product_of_a_table_that_does_not_ascend(grad):
+    """Each value of a row that several experts have is the result of one of them."""
+    g = gen(3)
+    P, E, N, K = 600, 6, 72, 136
+    off = torch.tensor([0, 500, 100, 600, 50, 590, 700]).int()
+    a, w = normal(g, P, N if grad else K), normal(g, E, N, K)
+    call = ft.ft_moe_grouped_matmul_grad if grad else ft.ft_moe_grouped_matmul
+    got = call(a.cuda(), w.cuda(), off.cuda(), out_dtype=F32).cpu().double()
+    fits = torch.zeros(got.shape, dtype=torch.bool)
+    for e, r0, r1, s in ref.groups(off, None, E, P, E):
+        y = w[s].double() if grad else w[s].double().t()
+        want, mag = a[r0:r1].double() @ y, a[r0:r1].double().abs() @ y.abs()
+        fits[r0:r1] |= (got[r0:r1] - want).abs() <= ref.sum_bound(want, mag, a.shape[1], F32)
+    assert fits.all()
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("P", [6, 200])
+def test_special_values_stay_in_their_rows(P, grad):
+    """A NaN or an infinity in a row shows in that row only, one in a matrix in its expert's column only; the reduction's
+    ragged end (not a multiple of 64) adds nothing to them."""
+    g = gen(P)
+    E, N, K = 3, 88, 104
+    off = torch.tensor([0, P // 3, P // 3, P]).int()
+    a, w = normal(g, P, N if grad else K), normal(g, E, N, K)
+    a[1, 5], a[P - 1, 70] = NAN, float("inf")
+    w[2, N - 1, 3] = -float("inf")
+    call = ft.ft_moe_grouped_matmul_grad if grad else ft.ft_moe_grouped_matmul
+    got = call(a.cuda(), w.cuda(), off.cuda(), out_dtype=F32).cpu()
+    want = torch.zeros_like(got)
+    for e, r0, r1, s in ref.groups(off, None, E, P, E):
+        y = w[s].double() if grad else w[s].double().t()
+        want[r0:r1] = (a[r0:r1].double() @ y).float()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.isinf(got), torch.isinf(want))
+    assert torch.equal(got[torch.isinf(got)], want[torch.isinf(want)])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "add"])
+@pytest.mark.parametrize("P, E, held, N, K", GROUPS)
+def test_matrix_gradient(P, E, held, N, K, kind):
+    g = gen(P * E + K)
+    slot = None if held is None else rows_ref.routing(g, 0, E, 1, held)["slot"]
+    off = sizes(g, E, P)
+    dout, a = normal(g, P, N), normal(g, P, K)
+    dtype = BF if kind == "bf16" else F32
+    has, want, mag, most = ref.matrix_gradient(dout, a, off, slot, E if held is None else held)
+    for e in range(E):  # rows of experts that do not count are not read
+        if not has[e]:
+            dout[off[e]:off[e + 1]], a[off[e]:off[e + 1]] = NAN, NAN
+    old = torch.randn(E, N, K, generator=g).to(dtype) if kind == "add" else torch.full((E, N, K), FILL).to(dtype)
+    dw = old.cuda()
+    got = ft.ft_moe_grouped_matmul_wgrad(dout.cuda(), a.cuda(), off.cuda(), slot_of_expert=dev(slot), dw=dw, add=kind == "add")
+    assert got is dw and same_bits(dw[~has.cuda()], old[~has])
+    if kind == "add":
+        want, mag = want + old.double(), mag + old.double().abs()
+    err = (dw.cpu().double() - want).abs()[has]
+    assert (err <= ref.sum_bound(want, mag, most + 1, dtype)[has]).all(), err.max()
+    if kind == "add":
+        none = has & (off[1:] == off[:-1])
+        assert same_bits(dw[none.cuda()], old[none])
+
+
+def test_matrix_gradient_without_rows():
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    empty = lambda n: torch.zeros(0, n, dtype=BF, device="cuda")  # noqa: E731
+    dw = filled(3, 16, 24, dtype=F32)
+    ft.ft_moe_grouped_matmul_wgrad(empty(16), empty(24), off, dw=dw, add=True)
+    assert (dw == FILL).all()
+    slot = torch.tensor([0, -1, 5], dtype=torch.int32, device="cuda")
+    ft.ft_moe_grouped_matmul_wgrad(empty(16), empty(24), off, slot_of_expert=slot, dw=dw, n_slots=4)
+    assert (dw[0] == 0).all() and (dw[1:] == FILL).all()
+
+
+def test_matrix_gradient_keeps_neighbours_apart():
+    """The rows before and behind an expert's are other experts': NaN there stays there."""
+    g = gen(8)
+    off = torch.tensor([0, 3, 70, 71, 200]).int()
+    dout, a = normal(g, 200, 40), normal(g, 200, 136)
+    dout[:3], a[70], dout[199, 5] = NAN, NAN, NAN
+    dw = ft.ft_moe_grouped_matmul_wgrad(dout.cuda(), a.cuda(), off.cuda()).cpu()
+    assert torch.isnan(dw[0]).all() and not torch.isnan(dw[1]).any() and torch.isnan(dw[2]).all()
+    bad = torch.zeros(40, 136, dtype=torch.bool)
+    bad[5] = True
+    assert torch.equal(torch.isnan(dw[3]), bad)
+
+
+def test_offsets_past_32_bits():
+    """Rows, matrices, results and gradients whose byte (and value) offsets pass 2^32; checked at the ends."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    P, N, K = (1 << 21) + 200, 8, 2056
+    a = torch.empty(P, K, dtype=BF, device="cuda").normal_(generator=g)
+    w = torch.empty(2, N, K, dtype=BF, device="cuda").normal_(generator=g)
+    off = torch.tensor([0, P - 150, P], dtype=torch.int32, device="cuda")
+    out = ft.ft_moe_grouped_matmul(a, w, off, out_dtype=F32)
+    for s, rows in ((0, slice(0, 3)), (0, slice(P - 153, P - 150)), (1, slice(P - 150, P))):
+        x, y = a[rows].cpu().double(), w[s].cpu().double()
+        want, mag = x @ y.t(), x.abs() @ y.abs().t()
+        assert ((out[rows].cpu().double() - want).abs() <= ref.sum_bound(want, mag, K, F32)).all()
+    dout = torch.empty(P, N, dtype=BF, device="cuda").normal_(generator=g)
+    da = ft.ft_moe_grouped_matmul_grad(dout, w, off)
+    rows = slice(P - 3, P)
+    x, y = dout[rows].cpu().double(), w[1].cpu().double()
+    assert ((da[rows].cpu().double() - x @ y).abs() <= ref.sum_bound(x @ y, x.abs() @ y.abs(), N, BF)).all()
+    dw = ft.ft_moe_grouped_matmul_wgrad(dout, a, off)
+    x, y = dout[P - 150:].cpu().double(), a[P - 150:].cpu().double()
+    assert ((dw[1].cpu().double() - x.t() @ y).abs() <= ref.sum_bound(x.t() @ y, x.abs().t() @ y.abs(), 150, F32)).all()
+    del a, da, out
+    n, N, K = 600, 2048, 2056  # 2.5e9 values
+    w = torch.empty(n, N, K, dtype=BF, device="cuda")
+    w[n - 1].normal_(generator=g)
+    a = torch.empty(5, K, dtype=BF, device="cuda").normal_(generator=g)
+    off = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    slot = torch.tensor([n - 1], dtype=torch.int32, device="cuda")
+    out = ft.ft_moe_grouped_matmul(a, w, off, slot_of_expert=slot, out_dtype=F32)
+    x, y = a.cpu().double(), w[n - 1].cpu().double()
+    assert ((out.cpu().double() - x @ y.t()).abs() <= ref.sum_bound(x @ y.t(), x.abs() @ y.abs().t(), K, F32)).all()
+    del w
+    off = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    off[n] = 5
+    dout = torch.empty(5, N, dtype=BF, device="cuda").normal_(generator=g)
+    dw = ft.ft_moe_grouped_matmul_wgrad(dout, a, off, out_dtype=BF)
+    x, y = dout.cpu().double(), a.cpu().double()
+    assert ((dw[n - 1].cpu().double() - x.t() @ y).abs() <= ref.sum_bound(x.t() @ y, x.abs().t() @ y.abs(), 5, BF)).all()
+    assert not dw[n - 2].any()
+
+
+# ---------------------------------------------------------------------------------------------- SwiGLU
+
+ROWS = [(1, 8), (5, 136), (17, 768), (130, 2048), (1000, 264), (3, 7168)]
+
+
+@pytest.mark.parametrize("rows, I", ROWS)
+def test_swiglu_and_gradient(rows, I):
+    g = gen(I)
+    gu, dh = normal(g, rows, 2 * I, scale=3.0), normal(g, rows, I)
+    h = ft.ft_moe_swiglu(gu.cuda())
+    want, off = ref.swiglu(gu)
+    assert h.dtype == BF and ((h.cpu().double() - want).abs() <= off * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY).all()
+    dgu = ft.ft_moe_swiglu_grad(gu.cuda(), dh.cuda())
+    want, off = ref.swiglu_gradient(gu, dh)
+    assert ((dgu.cpu().double() - want).abs() <= off * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY).all()
+    own = gu.cuda()
+    assert same_bits(ft.ft_moe_swiglu_grad(own, dh.cuda(), dgu=own), dgu)
+
+
+def test_swiglu_far_gates_and_special_values():
+    g = torch.tensor([-200.0, -95.0, -88.0, -60.0, -1.28125, 0.0, -0.0, 20.0, 90.0, 200.0, 3e38, -3e38]).to(BF)
+    u = torch.tensor([3.0, -2.0, 1.5, 0.5]).to(BF)
+    gu = torch.cat([g.repeat(4), u.repeat_interleave(12)])[None]
+    dh = torch.full((1, 48), 0.75).to(BF)
+    for got, (want, off) in ((ft.ft_moe_swiglu(gu.cuda()), ref.swiglu(gu)), (ft.ft_moe_swiglu_grad(gu.cuda(), dh.cuda()), ref.swiglu_gradient(gu, dh))):
+        inside = want.abs() < 3e38
+        err = (got.cpu().double() - want).abs()
+        assert (err <= off * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY)[inside].all()
+        assert not torch.isnan(got[:, inside[0].cuda()]).any()
+    gu[0, 3], gu[0, 48 + 9] = NAN, NAN
+    assert torch.equal(torch.isnan(ft.ft_moe_swiglu(gu.cuda()))[0].nonzero()[:, 0].cpu(), torch.tensor([3, 9]))
+    assert torch.isnan(ft.ft_moe_swiglu_grad(gu.cuda(), dh.cuda()))[0].nonzero()[:, 0].tolist() == [3, 9, 51]
+
+
+# ---------------------------------------------------------------------------------------------- adapters
+
+# T, E, held (None: no table), r, N, K
+ADAPTERS = [(1, 1, None, 8, 8, 8), (1, 3, 2, 16, 264, 520), (5, 40, 24, 8, 136, 2056), (16, 16, 16, 16, 4096, 2048), (33, 2, 1, 24, 72, 1032),
+            (131, 40, 24, 64, 520, 264), (300, 5, None, 72, 1288, 776), (1000, 3, 2, 128, 256, 136), (70, 1024, 500, 256, 24, 48),
+            (2500, 6, 5, 40, 648, 1544)]
+
+
+def adapter_rows(g, T, E, without=0.2):
+    """offsets [E + 1] and gather [T]: rows by adapter, those without one (number E) behind."""
+    ids = torch.randint(0, E, (T,), generator=g)
+    ids[torch.rand(T, generator=g) < without] = E
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = torch.bincount(ids, minlength=E + 1)[:E].cumsum(0)
+    return off, torch.sort(ids, stable=True)[1].int()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T, E, held, r, N, K", ADAPTERS)
+def test_adapters(T, E, held, r, N, K, dtype):
+    g = gen(T + E + r)
+    n = E if held is None else held
+    slot = None if held is None else rows_ref.routing(g, 0, E, 1, held)["slot"]
+    off, gather = adapter_rows(g, T, E)
+    base = torch.randn(T, N, generator=g).to(dtype)
+    x, a, b = normal(g, T, K), normal(g, n, r, K, scale=K ** -0.5), normal(g, n, N, r)
+    scale = torch.rand(n, generator=g) * 2 if E % 2 else None
+    want, bound = ref.adapters(base, x, a, b, off, gather, slot, scale)
+    args = [dev(t) for t in (base, x, a, b, off, gather)]
+    out = ft.ft_moe_lora(*args, slot_of_adapter=dev(slot), scale=dev(scale), out=filled(T, N, dtype=dtype))
+    err = (out.cpu().double() - want).abs()
+    assert (err <= bound).all(), (err - bound).max()
+    bare = (bound == 0).all(1)
+    assert same_bits(out[bare.cuda()], base[bare])
+    ws = torch.full((max(ft.ft_moe_lora_workspace(T, E, r, K), 16),), 255, dtype=torch.uint8, device="cuda")
+    again = ft.ft_moe_lora(*args, slot_of_adapter=dev(slot), scale=dev(scale), out=args[0], ws=ws)
+    assert again is args[0] and same_bits(again, out)
+
+
+def test_adapters_with_odd_tables():
+    """gather entries outside [0, T), offsets below 0 and past T, slots past the bank: rows that are not named stay."""
+    g = gen(2)
+    T, E, r, N, K = 60, 4, 16, 40, 72
+    off = torch.tensor([-3, 20, 20, 50, 900]).int()
+    gather = torch.randperm(T, generator=g).int()
+    lost = gather[[4, 25, 55]].long()
+    gather[4], gather[25], gather[55] = -1, T, 2 ** 31 - 1
+    slot = torch.tensor([1, 0, 7, 0]).int()
+    base = torch.randn(T, N, generator=g)
+    x, a, b = normal(g, T, K), normal(g, 2, r, K, scale=0.1), normal(g, 2, N, r)
+    want, bound = ref.adapters(base, x, a, b, off, gather, slot, None)
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)], slot_of_adapter=slot.cuda(), out=filled(T, N, dtype=F32)).cpu()
+    assert (out[lost] == FILL).all()
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[lost] = False
+    assert ((out.double() - want).abs() <= bound)[rest].all()
+
+
+def test_adapters_special_values_stay_in_their_rows():
+    g = gen(4)
+    T, E, r, N, K = 40, 3, 8, 72, 136
+    off, gather = adapter_rows(g, T, E, 0.0)
+    base = torch.randn(T, N, generator=g)
+    x, a, b = normal(g, T, K), normal(g, E, r, K, scale=0.1), normal(g, E, N, r)
+    x[7, 3] = NAN
+    base[9, 5] = float("inf")
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)]).cpu()
+    bad = torch.zeros(T, N, dtype=torch.bool)
+    bad[7] = True
+    assert torch.equal(torch.isnan(out), bad)
+    assert torch.isinf(out).sum() == 1 and out[9, 5] == float("inf")

@@ -1,0 +1,140 @@
+"""Product calls without a GPU: exports, argument checks of the C ABI and of the binding, and the reference formulas
+against differences."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import products_ref as ref
+import routed_expert_ffn_wave_amd as ft
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "ft_moe_products.h")
+A, B = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x20000)  # aligned, never dereferenced
+MIS = ctypes.c_void_p(0x10008)
+L = ft.lib
+
+
+def err(rc, status, text):
+    assert rc == status, (rc, ft.ft_moe_last_error())
+    assert text in ft.ft_moe_last_error(), ft.ft_moe_last_error()
+
+
+def test_every_declared_symbol_is_exported():
+    src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"^\s*(?:int|size_t)\s+(ft_moe_\w+)\s*\(", src, flags=re.M)))
+    assert names == sorted(ft.EXPORTED_PRODUCTS)
+    out = subprocess.run(["nm", "-D", "--defined-only", ft.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert set(names) <= set(re.findall(r"\sT\s(ft_moe_\w+)", out))
+    assert int(re.search(r"#define FT_ADD_TO_OUT (0x\w+)", open(HEADER).read()).group(1), 16) == ft.FT_ADD_TO_OUT
+
+
+def grouped(name, a=A, P=4, w=A, n=8, N=64, K=64, off=A, slot=None, E=8, out=B, f=0):
+    return getattr(L, "ft_moe_grouped_matmul" + name)(a, P, w, n, N, K, off, slot, E, out, f, None)
+
+
+def wgrad(d=A, a=A, P=4, N=64, K=64, off=A, slot=None, E=8, dw=B, f=0):
+    return L.ft_moe_grouped_matmul_wgrad(d, a, P, N, K, off, slot, E, dw, f, None)
+
+
+def lora(base=A, x=A, T=4, a=A, b=A, s=None, n=8, r=16, N=64, K=64, off=A, ga=A, slot=None, E=8, out=B, ws=B, nb=1 << 20, f=0):
+    return L.ft_moe_lora(base, x, T, a, b, s, n, r, N, K, off, ga, slot, E, out, ws, nb, f, None)
+
+
+SIZES = [(dict(E=0), "E must be"), (dict(E=1025), "E must be"), (dict(N=0), "N must be"), (dict(N=12), "N must be"),
+         (dict(N=(1 << 20) + 8), "N must be"), (dict(K=-8), "K must be"), (dict(K=4), "K must be"), (dict(K=(1 << 20) + 8), "K must be"),
+         (dict(f=1), "unknown flags 0x1")]
+
+
+@pytest.mark.parametrize("name, a, out", [("", "a", "out"), ("_grad", "dout", "da")])
+def test_grouped_refusals(name, a, out):
+    for kw, text in SIZES + [(dict(P=-1), "P must be"), (dict(P=(1 << 30) + 1), "P must be"), (dict(n=0), "n_slots must be"),
+                             (dict(n=7), "slot_of_expert is needed"), (dict(a=None), a + " is null"), (dict(w=MIS), "w is not 16"),
+                             (dict(off=None), "offsets is null"), (dict(slot=MIS), "slot_of_expert is not 16"), (dict(out=None), out + " is null"),
+                             (dict(f=ft.FT_ADD_TO_OUT), "unknown flags 0x40"), (dict(f=ft.FT_N_SLOTS(3), slot=A), "unknown flags 0x300")]:
+        err(grouped(name, **kw), ft.FT_E_INVAL, text)
+    assert grouped(name, P=0, a=None, w=None, off=None, out=None) == ft.FT_OK
+    # a table that does not ascend may give all rows to 512 of 1024 experts: more tiles than are counted
+    err(grouped(name, P=1 << 30, N=1 << 20, K=1 << 20, E=1024, n=1024), ft.FT_E_UNSUPPORTED, "product too large")
+
+
+def test_wgrad_refusals():
+    for kw, text in SIZES + [(dict(P=-1), "P must be"), (dict(d=None), "dout is null"), (dict(a=MIS), "a is not 16"),
+                             (dict(off=None), "offsets is null"), (dict(slot=MIS), "slot_of_expert is not 16"), (dict(dw=None), "dw is null"),
+                             (dict(f=ft.FT_ADD_TO_OUT | ft.FT_OUT_BF16), "FT_ADD_TO_OUT needs"),
+                             (dict(f=ft.FT_N_SLOTS(3)), "FT_N_SLOTS without")]:
+        err(wgrad(**kw), ft.FT_E_INVAL, text)
+    assert wgrad(P=0, d=None, a=None, off=None, dw=None, f=ft.FT_ADD_TO_OUT) == ft.FT_OK
+    err(wgrad(P=0, d=None, a=None, dw=None), ft.FT_E_INVAL, "dw is null")  # without rows dw is zeroed
+    err(wgrad(N=1 << 20, K=1 << 20, E=1024), ft.FT_E_UNSUPPORTED, "gradient too large")
+
+
+def test_swiglu_refusals():
+    f = lambda gu=A, rows=4, I=64, h=B: L.ft_moe_swiglu(gu, rows, I, h, None)  # noqa: E731
+    g = lambda gu=A, rows=4, I=64, h=B: L.ft_moe_swiglu_grad(gu, A, rows, I, h, None)  # noqa: E731
+    for call in (f, g):
+        for kw, text in [(dict(rows=-1), "rows must be"), (dict(I=0), "I must be"), (dict(I=12), "I must be"), (dict(I=(1 << 20) + 8), "I must be"),
+                         (dict(gu=None), "gu is null"), (dict(h=MIS), "is not 16")]:
+            err(call(**kw), ft.FT_E_INVAL, text)
+        err(call(rows=1 << 30, I=64), ft.FT_E_UNSUPPORTED, "rows too large")
+        assert call(rows=0, gu=None, h=None) == ft.FT_OK
+    err(L.ft_moe_swiglu_grad(A, None, 4, 64, B, None), ft.FT_E_INVAL, "dh is null")
+
+
+def test_lora_refusals():
+    for kw, text in SIZES + [(dict(T=-1), "T must be"), (dict(r=0), "r must be"), (dict(r=4), "r must be"), (dict(r=264), "r must be"),
+                             (dict(n=0), "n_slots must be"), (dict(n=7), "slot_of_adapter is needed"), (dict(base=None), "base is null"),
+                             (dict(x=MIS), "x is not 16"), (dict(a=None), "a is null"), (dict(b=None), "b is null"), (dict(s=MIS), "scale is not"),
+                             (dict(off=None), "offsets is null"), (dict(ga=None), "gather is null"), (dict(slot=MIS), "slot_of_adapter is not"),
+                             (dict(out=None), "out is null"), (dict(ws=None), "ws is null"), (dict(f=0x40), "unknown flags 0x40")]:
+        err(lora(**kw), ft.FT_E_INVAL, text)
+    need = ft.ft_moe_lora_workspace(4, 8, 16, 64)
+    assert need >= 4 * 16 * 4
+    err(lora(nb=need - 1), ft.FT_E_WORKSPACE, "workspace of")
+    err(lora(T=1 << 24), ft.FT_E_UNSUPPORTED, "T too large")
+    assert lora(T=0, base=None, x=None, a=None, b=None, off=None, ga=None, out=None, ws=None, nb=0) == ft.FT_OK
+    for bad in ((0, 8, 16, 64), (4, 0, 16, 64), (4, 1025, 16, 64), (4, 8, 0, 64), (4, 8, 264, 64), (4, 8, 16, 0)):
+        assert ft.ft_moe_lora_workspace(*bad) == 0
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    x, w, i = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(2, 64, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: ft.ft_moe_grouped_matmul(x, w, i), lambda: ft.ft_moe_grouped_matmul_grad(x, w, i),
+                 lambda: ft.ft_moe_grouped_matmul_wgrad(x, x, i), lambda: ft.ft_moe_swiglu(x), lambda: ft.ft_moe_swiglu_grad(x, x),
+                 lambda: ft.ft_moe_lora(x, x, w, w, i, i), lambda: ft.ft_moe_grouped_matmul(None, w, i)):
+        with pytest.raises(ft.FtError):
+            call()
+
+
+def test_reference_gradients_against_differences():
+    """The references' gradients of rows, matrices and SwiGLU are the differences of sum(dout * out) in fp64."""
+    g = torch.Generator().manual_seed(3)
+    P, E, N, K, h = 7, 3, 8, 8, 1e-5
+    off = torch.tensor([0, 4, 4, 7])
+    a, w, dout = (torch.randn(s, generator=g).double() for s in ((P, K), (E, N, K), (P, N)))
+
+    def loss(a, w):
+        return sum((dout[r0:r1] * (a[r0:r1] @ w[s].t())).sum() for _, r0, r1, s in ref.groups(off, None, E, P, E))
+
+    da = ref.forward(dout, w.transpose(1, 2), off, None, None)[1]
+    dw = ref.matrix_gradient(dout, a, off, None, E)[1]
+    for t, grad in ((a, da), (w, dw)):
+        for i in range(t.numel()):
+            flat, at = t.view(-1), t.view(-1)[i].item()
+            flat[i] = at + h
+            up = loss(a, w)
+            flat[i] = at - h
+            down = loss(a, w)
+            flat[i] = at
+            assert abs((up - down) / (2 * h) - grad.reshape(-1)[i]) < 1e-7
+    gu, dh = torch.randn(3, 10, generator=g).double() * 3, torch.randn(3, 5, generator=g).double()
+    dgu = ref.swiglu_gradient(gu, dh)[0]
+    for i in range(gu.numel()):
+        v = [gu.clone(), gu.clone()]
+        v[0].view(-1)[i] += h
+        v[1].view(-1)[i] -= h
+        diff = sum(sign * (dh * ref.swiglu(u)[0]).sum() for sign, u in ((1, v[0]), (-1, v[1]))) / (2 * h)
+        assert abs(diff - dgu.view(-1)[i]) < 1e-7
