@@ -26,38 +26,57 @@ __device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, in
       s.E, g, tmp, [&](int e, int& slot, int& row0, int& cnt) { return e < s.E && group_of(s, e, slot, row0, cnt) && cnt > 0; }, items_of);
 }
 
-// Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the tile list, so that tiles that run
-// together share rows and matrices through its L2.
-template <class C, bool GRAD, bool BF16>
-__global__ __launch_bounds__(C::NT, 2) void grouped_tile_kernel(GroupedArgs a) {
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+// A tile of up to BM rows takes the least of these heights that holds its rows.
+template <int BM, bool GRAD, bool BF16>
+__device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
+  using C = Bf16Cfg<BM, 256, 2, 4, BM == 64 ? 3 : 2, 1>;
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
-  const int ntn = (cols + C::BN - 1) / C::BN;
-  const int E2 = a.g.E + 2;
-  int* li = (int*)(lds + C::LDS);
-  GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
-  list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + C::BM - 1) / C::BM * ntn; });
-  const int nitems = gl.item0[gl.n];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
+  f32x4 acc[C::MF][C::NF];
+  const Operand ro{a.a + (size_t)row0 * red, red, rows};
+  const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0)};
+  bf16_tile<C, false, GRAD>(ro, co, red, lds, acc);
+  uint8_t* out = (uint8_t*)a.out + (size_t)row0 * cols * (BF16 ? 2 : 4);
+  store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, lane);
+}
+
+constexpr int kTileLds = 2 * (256 + 256) * 128;
+
+// Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the tile list, so that tiles that run
+// together share rows and matrices through its L2: bands of 4 row tiles, column tiles within a band in turn.
+template <bool GRAD, bool BF16>
+__global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int cols = GRAD ? a.K : a.N;
+  const int ntn = (cols + 255) / 256;
+  const int E2 = a.g.E + 2;
+  int* li = (int*)(lds + kTileLds);
+  GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
+  list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + 255) / 256 * ntn; });
+  const int nitems = gl.item0[gl.n];
   const int per = gridDim.x / 8, lb = (blockIdx.x % 8) * per + blockIdx.x / 8;  // gridDim.x % 8 == 0
   for (int it = lb; it < nitems; it += gridDim.x) {
     const int gi = find_group(gl.item0, gl.n, it);
     const int local = __builtin_amdgcn_readfirstlane(it - gl.item0[gi]);
     const int slot = __builtin_amdgcn_readfirstlane(gl.slot[gi]);
     const int row0 = __builtin_amdgcn_readfirstlane(gl.row0[gi]), cnt = __builtin_amdgcn_readfirstlane(gl.cnt[gi]);
-    const int m0 = local / ntn * C::BM, n0 = local % ntn * C::BN, rows = min(C::BM, cnt - m0);
-    const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
-    f32x4 acc[C::MF][C::NF];
-    const Operand ro{a.a + (size_t)(row0 + m0) * red, red, rows};
-    const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0)};
-    bf16_tile<C, false, GRAD>(ro, co, red, lds, acc);
-    uint8_t* out = (uint8_t*)a.out + (size_t)(row0 + m0) * cols * (BF16 ? 2 : 4);
-    store_rows<C::MF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 64, cols, lane);
+    constexpr int BAND = 4;
+    const int band = local / (BAND * ntn), h = min(BAND, (cnt + 255) / 256 - band * BAND), in = local - band * BAND * ntn;
+    const int m0 = (band * BAND + in % h) * 256, n0 = in / h * 256, rows = min(256, cnt - m0);
+    if (rows > 192)
+      grouped_tile<256, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+    else if (rows > 128)
+      grouped_tile<192, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+    else if (rows > 64)
+      grouped_tile<128, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+    else
+      grouped_tile<64, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
   }
 }
 
 template <class C, bool BF16, bool ADD>
-__global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
+__global__ __launch_bounds__(C::NT, C::PER * C::GW / 4) void wgrad_tile_kernel(WgradArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int ntm = (a.N + C::BM - 1) / C::BM, ntn = (a.K + C::BN - 1) / C::BN, tiles = ntm * ntn;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -72,21 +91,21 @@ __global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
   const Operand co{a.a + (size_t)row0 * a.K + n0, a.K, min(C::BN, a.K - n0)};
   bf16_tile<C, true, true>(ro, co, cnt, lds, acc);
   uint8_t* out = (uint8_t*)a.dw + ((size_t)e * a.N + m0) * a.K * (BF16 ? 2 : 4);
-  store_rows<C::MF, BF16, ADD>(acc, out, a.K, wv / C::WN * 16 * C::MF, ro.rows, n0 + wv % C::WN * 64, a.K, lane);
+  store_rows<C::MF, C::NF, BF16, ADD>(acc, out, a.K, wv / C::WN * 16 * C::MF, ro.rows, n0 + wv % C::WN * 16 * C::NF, a.K, lane);
 }
 
-template <class C, bool GRAD, bool BF16>
+template <bool GRAD, bool BF16>
 hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
   static LaunchCache cache;
   LaunchFacts f;
   const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
-  const long long ntn = (cols + C::BN - 1) / C::BN, ntm = (P + C::BM - 1) / C::BM;
-  if ((P / C::BM + 2LL) * (E / 2 + 1) * ntn >= 1LL << 31) return hipErrorNotSupported;
-  const size_t lds = C::LDS + group_lds_bytes(E);
-  hipError_t e = cache.get((const void*)grouped_tile_kernel<C, GRAD, BF16>, C::NT, lds, &f);
+  const long long ntn = (cols + 255) / 256, ntm = (P + 255) / 256;
+  if ((P / 256 + 2LL) * (E / 2 + 1) * ntn >= 1LL << 31) return hipErrorNotSupported;
+  const size_t lds = kTileLds + group_lds_bytes(E);
+  hipError_t e = cache.get((const void*)grouped_tile_kernel<GRAD, BF16>, 512, lds, &f);
   if (e != hipSuccess) return e;
   const long long upper = ((ntm + (E < P ? E : P)) * ntn + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
-  hipLaunchKernelGGL((grouped_tile_kernel<C, GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(C::NT), lds, s, a);
+  hipLaunchKernelGGL((grouped_tile_kernel<GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(512), lds, s, a);
   return hipGetLastError();
 }
 
@@ -102,18 +121,18 @@ hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-using T128 = Bf16Cfg<128, 128, 2, 2, 2>;
+using T256 = Bf16Cfg<256, 256, 2, 4, 2, 1>;
 
 }  // namespace
 
 hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s) {
-  if (kind == 0) return a.out_bf16 ? launch_tiles<T128, false, true>(a, s) : launch_tiles<T128, false, false>(a, s);
-  return a.out_bf16 ? launch_tiles<T128, true, true>(a, s) : launch_tiles<T128, true, false>(a, s);
+  if (kind == 0) return a.out_bf16 ? launch_tiles<false, true>(a, s) : launch_tiles<false, false>(a, s);
+  return a.out_bf16 ? launch_tiles<true, true>(a, s) : launch_tiles<true, false>(a, s);
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {
-  if (a.out_bf16) return launch_wgrad_tiles<T128, true, false>(a, s);
-  return a.add ? launch_wgrad_tiles<T128, false, true>(a, s) : launch_wgrad_tiles<T128, false, false>(a, s);
+  if (a.out_bf16) return launch_wgrad_tiles<T256, true, false>(a, s);
+  return a.add ? launch_wgrad_tiles<T256, false, true>(a, s) : launch_wgrad_tiles<T256, false, false>(a, s);
 }
 
 }  // namespace ftk
