@@ -158,8 +158,8 @@ int ft_moe_lora(const void* base, const uint16_t* x, int T, const uint16_t* a, c
     CHECK_PTR(offsets, "offsets");
     CHECK_PTR(gather, "gather");
     CHECK_PTR(out, "out");
-    CHECK_PTR(ws, "ws");
     const size_t need = lora_ws(T, E, r, K);
+    if (need) CHECK_PTR(ws, "ws");
     REQUIRE(ws_bytes >= need, FT_E_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
     const LoraArgs args{{offsets, slot_of_adapter, E, T, (uint32_t)n_slots}, gather, x, a, b, scale, base, out, r, N, K,
                         (flags & FT_OUT_BF16) != 0, (float*)ws};

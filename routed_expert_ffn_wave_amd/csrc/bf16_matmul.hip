@@ -29,14 +29,14 @@ __device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, in
 // A tile of up to BM rows takes the least of these heights that holds its rows.
 template <int BM, bool GRAD, bool BF16>
 __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
-  using C = Bf16Cfg<BM, 256, 2, 4, BM == 64 ? 3 : 2, 1>;
+  using C = Bf16Cfg<BM, 256, 2, 4, BM == 64 ? 3 : 2>;
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
   f32x4 acc[C::MF][C::NF];
-  const Operand ro{a.a + (size_t)row0 * red, red, rows};
-  const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0)};
-  bf16_tile<C, false, GRAD>(ro, co, red, lds, acc);
+  const Operand ro{a.a + (size_t)row0 * red, red, rows, nullptr, 0};
+  const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0), nullptr, 0};
+  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, red, lds, acc);
   uint8_t* out = (uint8_t*)a.out + (size_t)row0 * cols * (BF16 ? 2 : 4);
   store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, lane);
 }
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
 }
 
 template <class C, bool BF16, bool ADD>
-__global__ __launch_bounds__(C::NT, C::PER * C::GW / 4) void wgrad_tile_kernel(WgradArgs a) {
+__global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int ntm = (a.N + C::BM - 1) / C::BM, ntn = (a.K + C::BN - 1) / C::BN, tiles = ntm * ntn;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -87,9 +87,9 @@ __global__ __launch_bounds__(C::NT, C::PER * C::GW / 4) void wgrad_tile_kernel(W
   if (ADD && cnt == 0) return;
   const int m0 = t / ntn * C::BM, n0 = t % ntn * C::BN;
   f32x4 acc[C::MF][C::NF];
-  const Operand ro{a.dout + (size_t)row0 * a.N + m0, a.N, min(C::BM, a.N - m0)};
-  const Operand co{a.a + (size_t)row0 * a.K + n0, a.K, min(C::BN, a.K - n0)};
-  bf16_tile<C, true, true>(ro, co, cnt, lds, acc);
+  const Operand ro{a.dout + (size_t)row0 * a.N + m0, a.N, min(C::BM, a.N - m0), nullptr, 0};
+  const Operand co{a.a + (size_t)row0 * a.K + n0, a.K, min(C::BN, a.K - n0), nullptr, 0};
+  bf16_tile<C, ACROSS, ACROSS>(ro, co, cnt, lds, acc);
   uint8_t* out = (uint8_t*)a.dw + ((size_t)e * a.N + m0) * a.K * (BF16 ? 2 : 4);
   store_rows<C::MF, C::NF, BF16, ADD>(acc, out, a.K, wv / C::WN * 16 * C::MF, ro.rows, n0 + wv % C::WN * 16 * C::NF, a.K, lane);
 }
@@ -121,7 +121,7 @@ hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-using T256 = Bf16Cfg<256, 256, 2, 4, 2, 1>;
+using T256 = Bf16Cfg<256, 256, 2, 4, 2>;
 
 }  // namespace
 

@@ -13,38 +13,49 @@
 
 namespace ftk {
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, int PER_>
+// One wave: lane l's 16 bytes at its address to LDS bytes lds + AT + 16 l.
+template <int AT>
+__device__ __forceinline__ void dma16_at(const uint8_t* from, uint32_t lds) {
+  asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds), "i"(AT) : "memory", "scc");
+}
+
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1>
 struct Bf16Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;  // NS: stages in LDS
-  static constexpr int PER = PER_;                                        // blocks per compute unit that the registers allow
-  static constexpr int GW = WM * WN, NT = 64 * GW;
+  // KG > 1: a block is KG groups of waves, each with the whole tile, a share of the reduction and stages of its own.
+  static constexpr int KG = KG_, GW = WM * WN, NT = 64 * GW * KG;
   static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;              // fragments of a wave
   static constexpr int QM = BM / (8 * GW), QN = BN / (8 * GW);            // loads of 16 bytes a lane and stage
-  static constexpr int STAGE = (BM + BN) * 128, LDS = NS * STAGE;
+  static constexpr int STAGE = (BM + BN) * 128, RING = NS * STAGE, LDS = KG * RING;  // RING: a group's stages
   static_assert(BM % (8 * GW) == 0 && BN % (8 * GW) == 0, "load passes");
-  static_assert(NF % 4 == 0, "groups of 64 columns meet in the epilogue");
   static_assert((NS - 1) * (QM + QN) <= 63, "what the load counter holds");
 };
 
+enum { DIRECT = 0, ACROSS = 1, GATHERED = 2 };  // GATHERED: DIRECT rows named by a table
+
 // One operand of a tile: `rows` rows (DIRECT) or columns (ACROSS) from `base` on, of a matrix with `ld` values a memory row.
+// GATHERED: rows gather[0 ..] of the `total` rows at base; entries outside them count as row 0.
 struct Operand {
   const uint16_t* base;
   int ld, rows;
+  const int32_t* gather;
+  int total;
 };
 
 // An operand's loads into its part of a stage, B rows or columns wide, by GW waves.
-template <bool ACROSS, int B, int GW>
+template <int MODE, int B, int GW>
 struct Loader {
   static constexpr int Q = B / (8 * GW);
-  static constexpr int CH = ACROSS ? B / 8 : 8;  // chunks of a row in LDS
-  static constexpr int RP = 64 * GW / CH;        // rows of a load pass
+  static constexpr int CH = MODE == ACROSS ? B / 8 : 8;  // chunks of a row in LDS
+  static constexpr int RP = 64 * GW / CH;                // rows of a load pass
   uint32_t off[Q];
+  const uint8_t* at[MODE == GATHERED ? Q : 1];
   const uint8_t* p;
   size_t step;  // bytes from a stage to the next
 
   // Rows 0 - 3 and 8 - 11 of an ACROSS stage are read together (32 bytes each), as are 16 rows of a DIRECT one (16 bytes).
   static __device__ __forceinline__ int key(int row) {
-    if (!ACROSS) return (row >> 1) & 7;
+    if (MODE != ACROSS) return (row >> 1) & 7;
     return B == 64 ? (row & 2) | ((row >> 1) & 4) : 2 * ((row & 3) | ((row >> 1) & 4));
   }
   static __device__ __forceinline__ int row_of(int q, int tid) { return q * RP + tid / CH; }
@@ -53,11 +64,16 @@ struct Loader {
   // red: length of the reduction.  What lies past it, or past `rows`, repeats something inside.
   __device__ __forceinline__ void open(const Operand& o, int tid, int red) {
     p = (const uint8_t*)o.base;
-    step = ACROSS ? (size_t)o.ld * 128 : 128;
+    step = MODE == ACROSS ? (size_t)o.ld * 128 : 128;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int r = row_of(q, tid), c = chunk_of(q, tid);
-      off[q] = ACROSS ? (uint32_t)min(r, red - 1) * (uint32_t)(o.ld * 2) + (uint32_t)min(c, (o.rows - 1) / 8) * 16
+      if constexpr (MODE == GATHERED) {
+        const int t = o.gather[min(r, o.rows - 1)];
+        at[q] = p + (size_t)((uint32_t)t < (uint32_t)o.total ? t : 0) * o.ld * 2 + (c * 8 < red ? c : 0) * 16;
+        continue;
+      }
+      off[q] = MODE == ACROSS ? (uint32_t)min(r, red - 1) * (uint32_t)(o.ld * 2) + (uint32_t)min(c, (o.rows - 1) / 8) * 16
                       : (uint32_t)min(r, o.rows - 1) * (uint32_t)(o.ld * 2) + (uint32_t)(c * 8 < red ? c : 0) * 16;
     }
   }
@@ -66,38 +82,54 @@ struct Loader {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int r = row_of(q, tid), c = chunk_of(q, tid);
-      if (ACROSS)
+      if (MODE == GATHERED)
+        at[q] -= (c * 8 < left ? 0 : c) * 16;
+      else if (MODE == ACROSS)
         off[q] -= (uint32_t)(r - min(r, left - 1)) * (uint32_t)(o.ld * 2);
       else
         off[q] -= (uint32_t)(c * 8 < left ? 0 : c) * 16;
     }
   }
+  template <int q, int AT>
+  __device__ __forceinline__ void issue(uint32_t lds) const {
+    if constexpr (MODE == GATHERED)
+      dma16_at<AT + q * GW * 1024>(at[q], lds);
+    else
+      dma16<AT + q * GW * 1024>(p, off[q], lds);
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (MODE == GATHERED)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) at[q] += 128;
+    else
+      p += step;
+  }
   // What a short stage holds past its end becomes 0.
   static __device__ __forceinline__ void clear(uint8_t* part, int tid, int left) {
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-      if ((ACROSS ? row_of(q, tid) : chunk_of(q, tid) * 8) >= left) *(u32x4*)(part + (q * 64 * GW + tid) * 16) = u32x4{0, 0, 0, 0};
+      if ((MODE == ACROSS ? row_of(q, tid) : chunk_of(q, tid) * 8) >= left) *(u32x4*)(part + (q * 64 * GW + tid) * 16) = u32x4{0, 0, 0, 0};
   }
 };
 
 // Reads of an operand's fragments, 16 rows or columns by 32 steps, from its part of a stage.
-template <bool ACROSS, int B, int F>
+template <int MODE, int B, int F>
 struct Reader {
-  uint32_t off[ACROSS ? F : 1];
+  uint32_t off[MODE == ACROSS ? F : 1];
   __device__ __forceinline__ void open(int first, int lane) {  // first: the wave's first row or column
     const int r = lane & 15, g = lane >> 4;
-    if constexpr (ACROSS) {
-      const int row = 8 * g + (r >> 2), key = Loader<true, B, 1>::key(row);
+    if constexpr (MODE == ACROSS) {
+      const int row = 8 * g + (r >> 2), key = Loader<ACROSS, B, 1>::key(row);
 #pragma unroll
       for (int f = 0; f < F; ++f) off[f] = row * B * 2 + (((first / 8 + 2 * f) ^ key) << 4) + (r & 3) * 8;
     } else {
-      off[0] = (first + r) * 128 + ((g ^ Loader<false, B, 1>::key(r)) << 4);
+      off[0] = (first + r) * 128 + ((g ^ Loader<DIRECT, B, 1>::key(r)) << 4);
     }
   }
   // half 0, 1: steps 0 - 31 and 32 - 63
   template <int half>
   __device__ __forceinline__ bf16x8 read(const uint8_t* part, int f) const {
-    if constexpr (ACROSS) {
+    if constexpr (MODE == ACROSS) {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4* Lds;
       const uint8_t* at = part + off[f] + half * 32 * B * 2;
@@ -111,15 +143,16 @@ struct Reader {
 };
 
 // acc = the tile of R and C over `red` steps (0: zeros).  A wave's lane (r, g) gets row 16 m + r and columns
-// 16 f + 4 g .. + 3 of its part.
+// 16 f + 4 g .. + 3 of its part.  Groups of waves pass their own operands, `red` and part of `lds`; those of one wave run
+// without barriers, and groups of several have to have the same number of stages.
 //
 // One pipeline over all stages, in halves of 32 steps: while the matrix instructions of a half run from registers, the next
 // half's fragments are read from LDS into other registers.  The turn to the next stage comes before the second half, whose
 // fragments have been read by then: from there on the buffer of this stage takes the loads of the stage NS ahead.
-template <class C, bool RACROSS, bool CACROSS>
+template <class C, int RMODE, int CMODE>
 __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, int red, uint8_t* lds, f32x4 (&acc)[C::MF][C::NF]) {
   constexpr int MF = C::MF, NF = C::NF, NS = C::NS, U = C::QM + C::QN;
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % C::GW, tid = wv * 64 + lane;
   const int wm = wv / C::WN, wn = wv % C::WN;
 #pragma unroll
   for (int m = 0; m < MF; ++m)
@@ -127,12 +160,12 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
   if (red <= 0) return;
   const int nb = (red + 63) / 64, left = red & 63;  // stages; the last has `left` steps if that is not 0
-  Loader<RACROSS, C::BM, C::GW> lr;
-  Loader<CACROSS, C::BN, C::GW> lc;
+  Loader<RMODE, C::BM, C::GW> lr;
+  Loader<CMODE, C::BN, C::GW> lc;
   lr.open(ro, tid, red);
   lc.open(co, tid, red);
-  Reader<RACROSS, C::BM, MF> rr;
-  Reader<CACROSS, C::BN, NF> rc;
+  Reader<RMODE, C::BM, MF> rr;
+  Reader<CMODE, C::BN, NF> rc;
   rr.open(wm * 16 * MF, lane);
   rc.open(wn * 16 * NF, lane);
   const uint32_t lds0 = lds_addr(lds) + wv * 1024;
@@ -147,20 +180,24 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
   auto issue_unit = [&](auto u_) {
     constexpr int u = decltype(u_)::value;
     if constexpr (u < C::QM)
-      dma16<u * C::GW * 1024>(lr.p, lr.off[u], fill_lds);
+      lr.template issue<u, 0>(fill_lds);
     else
-      dma16<C::BM * 128 + (u - C::QM) * C::GW * 1024>(lc.p, lc.off[u - C::QM], fill_lds);
+      lc.template issue<u - C::QM, C::BM * 128>(fill_lds);
   };
   auto advance = [&] {
     ++fill;
-    lr.p += lr.step;
-    lc.p += lc.step;
-    fill_lds = fill_lds + C::STAGE >= lds0 + C::LDS ? lds0 : fill_lds + C::STAGE;
+    lr.advance();
+    lc.advance();
+    fill_lds = fill_lds + C::STAGE >= lds0 + C::RING ? lds0 : fill_lds + C::STAGE;
+  };
+  auto meet = [] {
+    if constexpr (C::GW > 1) asm volatile("s_barrier" ::: "memory");
   };
   auto clear = [&](uint8_t* st) {
-    Loader<RACROSS, C::BM, C::GW>::clear(st, tid, left);
-    Loader<CACROSS, C::BN, C::GW>::clear(st + C::BM * 128, tid, left);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    Loader<RMODE, C::BM, C::GW>::clear(st, tid, left);
+    Loader<CMODE, C::BN, C::GW>::clear(st + C::BM * 128, tid, left);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    meet();
   };
   bf16x8 f0[NF + MF], f1[NF + MF];  // the fragments of a half: columns, then rows
   uint8_t* st = lds;
@@ -170,24 +207,25 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
   };
   using Half0 = std::integral_constant<int, 0>;
   using Half1 = std::integral_constant<int, 1>;
-  // Slots between a half's MM matrix instructions: fragment reads in the first three quarters, loads from the start on.
-  constexpr int MM = MF * NF, RS = (MM - MM / 4) / (NF + MF), DS = MM / 2 / U > 0 ? MM / 2 / U : 1;
-  static_assert(RS >= 1 && U * DS <= MM, "a half's reads and a stage's loads fit its matrix instructions");
+  // Slots between a half's MM matrix instructions: fragment reads in the first three quarters, loads in the first half.
+  constexpr int MM = MF * NF;
   auto half = [&](bf16x8(&now)[NF + MF], bf16x8(&next)[NF + MF], const uint8_t* from, auto h, auto loads) {
 #pragma unroll
     for (int i = 0; i < MM; ++i) {
       const int m = i / NF, f = i % NF;
       acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now[f], now[NF + m], acc[m][f], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
-      if (i % RS == 0 && i / RS < NF + MF) next[i / RS] = frag(from, h, i / RS);
+#pragma unroll
+      for (int n = 0; n < NF + MF; ++n)
+        if (n * (MM - MM / 4) / (NF + MF) == i) next[n] = frag(from, h, n);
       if constexpr (decltype(loads)::value)
         unrolled<0, U>([&](auto u) {
-          if (decltype(u)::value * DS == i) issue_unit(u);
+          if (decltype(u)::value * (MM / 2) / U == i) issue_unit(u);
         });
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto after = [&](uint8_t* s) { return s + C::STAGE >= lds + C::LDS ? lds : s + C::STAGE; };
+  auto after = [&](uint8_t* s) { return s + C::STAGE >= lds + C::RING ? lds : s + C::STAGE; };
 
   while (fill < min(NS, nb)) {
     open();
@@ -195,9 +233,10 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
     advance();
   }
   if (nb >= NS)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 1) * U) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 1) * U) : "memory");
   else
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  meet();
   if (nb == 1 && left) clear(st);
 #pragma unroll
   for (int n = 0; n < NF + MF; ++n) f0[n] = frag(st, Half0{}, n);
@@ -205,7 +244,8 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
   for (; b < nb - NS; ++b) {
     half(f0, f1, st, Half1{}, std::false_type{});
     // the next stage has landed for every wave, and every wave has read this one
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * U) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * U) : "memory");
+    meet();
     open();
     st = after(st);
     half(f1, f0, st, Half0{}, std::true_type{});
@@ -213,60 +253,144 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
   }
   for (; b < nb; ++b) {  // nothing left to load
     half(f0, f1, st, Half1{}, std::false_type{});
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    meet();
     st = after(st);
     if (b == nb - 2 && left) clear(st);
     half(f1, f0, st, Half0{}, std::false_type{});  // past the last stage: read but unused
   }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the stages are free for the next tile
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  meet();  // the stages are free for the next tile
+}
+
+// Four lanes (g = 0 .. 3) that hold 4 g .. 4 g + 3 of four fragments' 16 columns each, swapped so that lane g holds all of
+// fragment g: v[j] columns 4 j .. 4 j + 3 of it.  V: 32-bit words a lane has of a fragment.
+template <class V>
+__device__ __forceinline__ void swap_fours(V (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const auto word = v[f][i];  // a value: the cast of a vector's element in place reads element 0
+      w[f] = __builtin_bit_cast(uint32_t, word);
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const auto x = __builtin_amdgcn_permlane32_swap(w[f], w[f + 2], false, false);
+      w[f] = x[0], w[f + 2] = x[1];
+    }
+#pragma unroll
+    for (int f = 0; f < 4; f += 2) {
+      const auto x = __builtin_amdgcn_permlane16_swap(w[f], w[f + 1], false, false);
+      w[f] = x[0], w[f + 1] = x[1];
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) v[f][i] = __builtin_bit_cast(std::decay_t<decltype(v[0][0])>, w[f]);
+  }
+}
+
+// The same four registers, now with the pieces of a row in neighbouring lanes: after swap_fours, registers and the low two
+// lane bits change places.  (A memory instruction whose neighbouring lanes lie in different rows takes four times as
+// long to send off: 64 cycles for 16 bytes a lane.)
+template <class V>
+__device__ __forceinline__ void swap_quads(V (&v)[4], int lane) {
+  const bool odd = lane & 1, upper = lane & 2;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i) {
+    int w[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const auto word = v[f][i];
+      w[f] = __builtin_bit_cast(int, word);
+    }
+#pragma unroll
+    for (int f = 0; f < 4; f += 2) {
+      const int a = w[f], b = w[f + 1];
+      const int na = __builtin_amdgcn_update_dpp(0, a, 0xB1, 0xf, 0xf, true), nb = __builtin_amdgcn_update_dpp(0, b, 0xB1, 0xf, 0xf, true);
+      w[f] = odd ? nb : a;
+      w[f + 1] = odd ? b : na;
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int a = w[f], b = w[f + 2];
+      const int na = __builtin_amdgcn_update_dpp(0, a, 0x4E, 0xf, 0xf, true), nb = __builtin_amdgcn_update_dpp(0, b, 0x4E, 0xf, 0xf, true);
+      w[f] = upper ? nb : a;
+      w[f + 2] = upper ? b : na;
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) v[f][i] = __builtin_bit_cast(std::decay_t<decltype(v[0][0])>, w[f]);
+  }
+}
+
+// A wave's results of 64 columns in whole pieces of rows.  put(row, column, piece): row of the wave's part, column of
+// the 64; a piece is 4 values in fp32, or 8 in bf16 (two fragment rows at a time; MF odd: one, in halves of 4).
+template <int MF, bool BF16, class Put>
+__device__ __forceinline__ void each_piece(const f32x4 (&acc)[MF][4], int lane, Put put) {
+  const int up = lane >> 4, mid = (lane >> 2) & 3, low = lane & 3;
+  if constexpr (!BF16) {
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      f32x4 v[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) v[f] = acc[m][f];
+      swap_fours(v);
+      swap_quads(v, lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) put(16 * m + 4 * mid + j, 16 * up + 4 * low, v[j]);
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < MF; m += 2) {
+      // v[2 (f / 2) + m % 2]: the lane's columns of fragments f, f + 1, which lanes g, g + 1 swap to 8 in a row
+      u32x4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int mm = m + (k & 1) < MF ? m + (k & 1) : m;
+        uint32_t w[2][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f32x4& p = acc[mm][(k & 2) + q];
+            w[q][h] = (uint32_t)f32_to_bf16_bits(p[2 * h]) | ((uint32_t)f32_to_bf16_bits(p[2 * h + 1]) << 16);
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const auto x = __builtin_amdgcn_permlane16_swap(w[0][h], w[1][h], false, false);
+          v[k][h] = x[0], v[k][2 + h] = x[1];
+        }
+      }
+      // lane bits 5, 4: g / 2 and f % 2; after the swap f / 2 and m % 2, the registers' g / 2 and f % 2
+      swap_fours(v);
+      const u32x4 t = v[1];
+      v[1] = v[2], v[2] = t;
+      swap_quads(v, lane);  // lane bits 1, 0: f % 2 and g / 2; the registers' are the row's
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (m + (up & 1) < MF) put(16 * (m + (up & 1)) + 4 * mid + j, 32 * (up >> 1) + 8 * low, v[j]);
+    }
+  }
 }
 
 // Store a wave's results: rows m0 + 16 m + r < rows, columns from n0 on below cols (a multiple of 8) of out with ld
-// values a row.
+// values a row.  Results that are not read again soon go past the caches' own lines.
 template <int MF, int NF, bool BF16, bool ADD>
 __device__ __forceinline__ void store_rows(const f32x4 (&acc)[MF][NF], void* out, size_t ld, int m0, int rows, int n0, int cols, int lane) {
+  static_assert(NF == 4, "64 columns");
   // laundered, so that the addresses are formed here and not kept in registers through the pipeline
   asm volatile("" : "+v"(lane));
-  const int r = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int q = 0; q < MF * NF / 4; ++q) {
-    const int m = q / (NF / 4), f0 = q % (NF / 4) * 4, row = m0 + 16 * m + r, n = n0 + 16 * f0;
+  each_piece<MF, BF16>(acc, lane, [&](int row, int col, auto piece) {
+    row += m0, col += n0;
+    if (row >= rows || col >= cols) return;
     if constexpr (BF16) {
-      // four lanes hold a row's 16 columns of every fragment in fours: swapped so that each holds 16 of one fragment
-      uint32_t w[4][2];
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          w[f][h] = (uint32_t)f32_to_bf16_bits(acc[m][f0 + f][2 * h]) | ((uint32_t)f32_to_bf16_bits(acc[m][f0 + f][2 * h + 1]) << 16);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const auto x = __builtin_amdgcn_permlane32_swap(w[f][h], w[f + 2][h], false, false);
-          w[f][h] = x[0], w[f + 2][h] = x[1];
-        }
-#pragma unroll
-        for (int f = 0; f < 4; f += 2) {
-          const auto x = __builtin_amdgcn_permlane16_swap(w[f][h], w[f + 1][h], false, false);
-          w[f][h] = x[0], w[f + 1][h] = x[1];
-        }
-      }
-      uint16_t* o = (uint16_t*)out + (size_t)row * ld + n + 16 * g;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (row < rows && n + 16 * g + 8 * h < cols) *(u32x4*)(o + 8 * h) = u32x4{w[2 * h][0], w[2 * h][1], w[2 * h + 1][0], w[2 * h + 1][1]};
+      *(u32x4*)((uint16_t*)out + (size_t)row * ld + col) = piece;
     } else {
-      float* o = (float*)out + (size_t)row * ld + n + 4 * g;
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        if (row < rows && n + 16 * f + 4 * g < cols) {
-          f32x4 v = acc[m][f0 + f];
-          if (ADD) v += *(const f32x4*)(o + 16 * f);
-          *(f32x4*)(o + 16 * f) = v;
-        }
+      float* o = (float*)out + (size_t)row * ld + col;
+      if (ADD) piece += *(const f32x4*)o;
+      *(f32x4*)o = piece;
     }
-  }
+  });
 }
 
 }  // namespace ftk

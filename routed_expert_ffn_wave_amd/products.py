@@ -134,14 +134,16 @@ def ft_moe_lora(base, x, a, b, offsets, gather, slot_of_adapter=None, scale=None
     ps = None if scale is None else _take(scale, "scale", (_F32,), (n_slots,), dev)
     pf, pt, E = _groups(offsets, slot_of_adapter, "slot_of_adapter", dev)
     pg = _take(gather, "gather", (_I32,), (T,), dev)
-    need = lib.ft_moe_lora_workspace(T, E, r, K)
     if out is None:
         out = _new((T, N), base.dtype, dev, stream)
     po = _take(out, "out", (base.dtype,), (T, N), dev)
     if ws is None:
-        ws = _new((max(need, 16),), torch.uint8, dev, stream)
-    if not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        need = lib.ft_moe_lora_workspace(T, E, r, K)
+        if need:
+            ws = _new((need,), torch.uint8, dev, stream)
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         _refuse(f"ws must be a contiguous tensor on cuda:{dev}")
-    _run(lib.ft_moe_lora, dev, stream, base.data_ptr(), px, T, pa, pb, ps, n_slots, r, N, K, pf, pg, pt, E, po, ws.data_ptr(),
-         ws.numel() * ws.element_size(), FT_OUT_BF16 if base.dtype is _BF else 0)
+    pw, nw = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    _run(lib.ft_moe_lora, dev, stream, base.data_ptr(), px, T, pa, pb, ps, n_slots, r, N, K, pf, pg, pt, E, po, pw, nw,
+         FT_OUT_BF16 if base.dtype is _BF else 0)
     return out

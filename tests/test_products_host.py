@@ -89,11 +89,11 @@ def test_lora_refusals():
                              (dict(n=0), "n_slots must be"), (dict(n=7), "slot_of_adapter is needed"), (dict(base=None), "base is null"),
                              (dict(x=MIS), "x is not 16"), (dict(a=None), "a is null"), (dict(b=None), "b is null"), (dict(s=MIS), "scale is not"),
                              (dict(off=None), "offsets is null"), (dict(ga=None), "gather is null"), (dict(slot=MIS), "slot_of_adapter is not"),
-                             (dict(out=None), "out is null"), (dict(ws=None), "ws is null"), (dict(f=0x40), "unknown flags 0x40")]:
+                             (dict(out=None), "out is null"), (dict(T=300, r=72, ws=None), "ws is null"), (dict(f=0x40), "unknown flags 0x40")]:
         err(lora(**kw), ft.FT_E_INVAL, text)
-    need = ft.ft_moe_lora_workspace(4, 8, 16, 64)
-    assert need >= 4 * 16 * 4
-    err(lora(nb=need - 1), ft.FT_E_WORKSPACE, "workspace of")
+    need = ft.ft_moe_lora_workspace(300, 8, 72, 64)
+    assert need >= 300 * 72 * 4
+    err(lora(T=300, r=72, nb=need - 1), ft.FT_E_WORKSPACE, "workspace of")
     err(lora(T=1 << 24), ft.FT_E_UNSUPPORTED, "T too large")
     assert lora(T=0, base=None, x=None, a=None, b=None, off=None, ga=None, out=None, ws=None, nb=0) == ft.FT_OK
     for bad in ((0, 8, 16, 64), (4, 0, 16, 64), (4, 1025, 16, 64), (4, 8, 0, 64), (4, 8, 264, 64), (4, 8, 16, 0)):
