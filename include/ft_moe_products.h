@@ -88,10 +88,10 @@ int ft_moe_swiglu_grad(const uint16_t* gu, const uint16_t* dh, int rows, int I, 
  * does not name is left as it was, one that it names twice is formed twice (with out == base: added twice or once).
  * r % 8 == 0, r <= 256 (adapters of smaller rank: zeros behind), N % 8 == 0, K % 8 == 0, both at most 2^20.
  * The inner sums are held in fp32 and enter the outer ones as two bf16 terms, within 2^-16 of themselves.
- * ws: ft_moe_lora_workspace(T, E, r, K) bytes of device memory (0 for few rows: then ws may be NULL); contents do not matter.  Calls that may
+ * ws: ft_moe_lora_workspace(T, E, r, N, K) bytes of device memory (0 for few rows: then ws may be NULL); contents do not matter.  Calls that may
  * overlap, and graphs that may, need their own.
  */
-size_t ft_moe_lora_workspace(int T, int E, int r, int K);
+size_t ft_moe_lora_workspace(int T, int E, int r, int N, int K);
 int ft_moe_lora(const void* base, const uint16_t* x, int T, const uint16_t* a, const uint16_t* b, const float* scale,
                 int n_slots, int r, int N, int K, const int32_t* offsets, const int32_t* gather,
                 const int32_t* slot_of_adapter, int E, void* out, void* ws, size_t ws_bytes, int flags, hipStream_t stream);

@@ -54,7 +54,7 @@ int check_swiglu(int rows, int I) {
   return FT_OK;
 }
 
-size_t lora_ws(int T, int E, int r, int K) { return (size_t)lora_splits(T, E, r, K) * T * r * sizeof(float); }
+size_t lora_ws(int T, int E, int r, int N, int K) { return (size_t)lora_splits(T, E, r, N, K) * T * r * sizeof(float); }
 
 }  // namespace
 
@@ -134,9 +134,9 @@ int ft_moe_swiglu_grad(const uint16_t* gu, const uint16_t* dh, int rows, int I, 
   }
 }
 
-size_t ft_moe_lora_workspace(int T, int E, int r, int K) {
-  if (T <= 0 || E < 1 || E > 1024 || r <= 0 || r > 256 || K <= 0) return 0;
-  return lora_ws(T, E, r, K);
+size_t ft_moe_lora_workspace(int T, int E, int r, int N, int K) {
+  if (T <= 0 || T >= (1 << 24) || E < 1 || E > 1024 || r <= 0 || r > 256 || N <= 0 || N > kMaxCols || K <= 0 || K > kMaxCols) return 0;
+  return lora_ws(T, E, r, N, K);
 }
 
 int ft_moe_lora(const void* base, const uint16_t* x, int T, const uint16_t* a, const uint16_t* b, const float* scale,
@@ -158,7 +158,7 @@ int ft_moe_lora(const void* base, const uint16_t* x, int T, const uint16_t* a, c
     CHECK_PTR(offsets, "offsets");
     CHECK_PTR(gather, "gather");
     CHECK_PTR(out, "out");
-    const size_t need = lora_ws(T, E, r, K);
+    const size_t need = lora_ws(T, E, r, N, K);
     if (need) CHECK_PTR(ws, "ws");
     REQUIRE(ws_bytes >= need, FT_E_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
     const LoraArgs args{{offsets, slot_of_adapter, E, T, (uint32_t)n_slots}, gather, x, a, b, scale, base, out, r, N, K,

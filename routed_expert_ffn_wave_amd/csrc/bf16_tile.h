@@ -323,8 +323,8 @@ __device__ __forceinline__ void swap_quads(V (&v)[4], int lane) {
   }
 }
 
-// A wave's results of 64 columns in whole pieces of rows.  put(row, column, piece): row of the wave's part, column of
-// the 64; a piece is 4 values in fp32, or 8 in bf16 (two fragment rows at a time; MF odd: one, in halves of 4).
+// A wave's results of 64 columns in whole pieces of rows.  put(i, row, column, piece): the i-th piece, row of the wave's part,
+// column of the 64; a piece is 4 values in fp32, or 8 in bf16 (two fragment rows at a time; MF odd: one, in halves of 4).
 template <int MF, bool BF16, class Put>
 __device__ __forceinline__ void each_piece(const f32x4 (&acc)[MF][4], int lane, Put put) {
   const int up = lane >> 4, mid = (lane >> 2) & 3, low = lane & 3;
@@ -337,7 +337,7 @@ __device__ __forceinline__ void each_piece(const f32x4 (&acc)[MF][4], int lane, 
       swap_fours(v);
       swap_quads(v, lane);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) put(16 * m + 4 * mid + j, 16 * up + 4 * low, v[j]);
+      for (int j = 0; j < 4; ++j) put(4 * m + j, 16 * m + 4 * mid + j, 16 * up + 4 * low, v[j]);
     }
   } else {
 #pragma unroll
@@ -368,7 +368,7 @@ __device__ __forceinline__ void each_piece(const f32x4 (&acc)[MF][4], int lane, 
       swap_quads(v, lane);  // lane bits 1, 0: f % 2 and g / 2; the registers' are the row's
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (m + (up & 1) < MF) put(16 * (m + (up & 1)) + 4 * mid + j, 32 * (up >> 1) + 8 * low, v[j]);
+        if (m + (up & 1) < MF) put(2 * m + j, 16 * (m + (up & 1)) + 4 * mid + j, 32 * (up >> 1) + 8 * low, v[j]);
     }
   }
 }
@@ -380,7 +380,7 @@ __device__ __forceinline__ void store_rows(const f32x4 (&acc)[MF][NF], void* out
   static_assert(NF == 4, "64 columns");
   // laundered, so that the addresses are formed here and not kept in registers through the pipeline
   asm volatile("" : "+v"(lane));
-  each_piece<MF, BF16>(acc, lane, [&](int row, int col, auto piece) {
+  each_piece<MF, BF16>(acc, lane, [&](int, int row, int col, auto piece) {
     row += m0, col += n0;
     if (row >= rows || col >= cols) return;
     if constexpr (BF16) {

@@ -48,7 +48,7 @@ struct LoraArgs {
   bool bf16;  // base and out
   float* ws;  // [splits][T][r]
 };
-int lora_splits(int T, int E, int r, int K);
+int lora_splits(int T, int E, int r, int N, int K);  // 0: the call needs no ws
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 
 }  // namespace ftk

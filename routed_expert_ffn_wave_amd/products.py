@@ -23,7 +23,7 @@ _SIG = {
     "ft_moe_grouped_matmul_wgrad": [_P, _P, _i, _i, _i, _P, _P, _i, _P, _i, _P],
     "ft_moe_swiglu": [_P, _i, _i, _P, _P],
     "ft_moe_swiglu_grad": [_P, _P, _i, _i, _P, _P],
-    "ft_moe_lora_workspace": [_i, _i, _i, _i],
+    "ft_moe_lora_workspace": [_i, _i, _i, _i, _i],
     "ft_moe_lora": [_P, _P, _i, _P, _P, _P, _i, _i, _i, _i, _P, _P, _P, _i, _P, _P, ctypes.c_size_t, _i, _P],
 }
 for _name, _args in _SIG.items():
@@ -116,15 +116,15 @@ def ft_moe_swiglu_grad(gu, dh, dgu=None, stream=None):
     return dgu
 
 
-def ft_moe_lora_workspace(T: int, E: int, r: int, K: int) -> int:
-    return lib.ft_moe_lora_workspace(T, E, r, K)
+def ft_moe_lora_workspace(T: int, E: int, r: int, N: int, K: int) -> int:
+    return lib.ft_moe_lora_workspace(T, E, r, N, K)
 
 
 def ft_moe_lora(base, x, a, b, offsets, gather, slot_of_adapter=None, scale=None, out=None, ws=None, stream=None):
     """base [T][N] (bf16 or fp32) plus every row's adapter: scale (x a^T) b^T with x bf16 [T][K], a bf16 [n_slots][r][K],
     b bf16 [n_slots][N][r] and scale fp32 [n_slots] (None: 1).  offsets [E + 1] and gather [T] list the rows of the E
     adapters (ft_moe_permute of the rows' adapters, k = 1); rows without an adapter stand behind them or with one that
-    has no slot, and get base.  out may be base itself.  `ws`: ft_moe_lora_workspace(T, E, r, K) bytes."""
+    has no slot, and get base.  out may be base itself.  `ws`: ft_moe_lora_workspace(T, E, r, N, K) bytes."""
     dev, (T, N) = _first(base, "base", 2, _FLOATS, stream)
     K = x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
     px = _take(x, "x", (_BF,), (T, K), dev)
@@ -138,7 +138,7 @@ def ft_moe_lora(base, x, a, b, offsets, gather, slot_of_adapter=None, scale=None
         out = _new((T, N), base.dtype, dev, stream)
     po = _take(out, "out", (base.dtype,), (T, N), dev)
     if ws is None:
-        need = lib.ft_moe_lora_workspace(T, E, r, K)
+        need = lib.ft_moe_lora_workspace(T, E, r, N, K)
         if need:
             ws = _new((need,), torch.uint8, dev, stream)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():

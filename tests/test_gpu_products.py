@@ -280,7 +280,7 @@ def test_adapters(T, E, held, r, N, K, dtype):
     assert (err <= bound).all(), (err - bound).max()
     bare = (bound == 0).all(1)
     assert same_bits(out[bare.cuda()], base[bare])
-    ws = torch.full((max(ft.ft_moe_lora_workspace(T, E, r, K), 16),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(ft.ft_moe_lora_workspace(T, E, r, N, K), 16),), 255, dtype=torch.uint8, device="cuda")
     again = ft.ft_moe_lora(*args, slot_of_adapter=dev(slot), scale=dev(scale), out=args[0], ws=ws)
     assert again is args[0] and same_bits(again, out)
 

@@ -91,12 +91,13 @@ def test_lora_refusals():
                              (dict(off=None), "offsets is null"), (dict(ga=None), "gather is null"), (dict(slot=MIS), "slot_of_adapter is not"),
                              (dict(out=None), "out is null"), (dict(T=300, r=72, ws=None), "ws is null"), (dict(f=0x40), "unknown flags 0x40")]:
         err(lora(**kw), ft.FT_E_INVAL, text)
-    need = ft.ft_moe_lora_workspace(300, 8, 72, 64)
+    need = ft.ft_moe_lora_workspace(300, 8, 72, 64, 64)
     assert need >= 300 * 72 * 4
     err(lora(T=300, r=72, nb=need - 1), ft.FT_E_WORKSPACE, "workspace of")
     err(lora(T=1 << 24), ft.FT_E_UNSUPPORTED, "T too large")
     assert lora(T=0, base=None, x=None, a=None, b=None, off=None, ga=None, out=None, ws=None, nb=0) == ft.FT_OK
-    for bad in ((0, 8, 16, 64), (4, 0, 16, 64), (4, 1025, 16, 64), (4, 8, 0, 64), (4, 8, 264, 64), (4, 8, 16, 0)):
+    for bad in ((0, 8, 72, 64, 64), (300, 0, 72, 64, 64), (300, 1025, 72, 64, 64), (300, 8, 0, 64, 64), (300, 8, 264, 64, 64),
+                (300, 8, 72, 0, 64), (300, 8, 72, 64, 0), (1 << 24, 8, 72, 64, 64)):
         assert ft.ft_moe_lora_workspace(*bad) == 0
 
 
