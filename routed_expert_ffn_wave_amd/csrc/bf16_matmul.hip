@@ -5,6 +5,9 @@
 //   rows           da[p][k]    = sum_n dout[p][n] w[e][n][k]
 //   matrices       dw[e][n][k] = sum_{p of e} dout[p][n] a[p][k]
 // bf16 products are exact in fp32 and added there by the matrix instructions; results are rounded once.
+#include <algorithm>
+#include <cmath>
+
 #include "bf16_tile.h"
 #include "ft_groups.h"
 #include "ft_kernels.h"
@@ -75,6 +78,73 @@ __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   }
 }
 
+// Few rows an expert: BM rows by 64 columns a block, whose four waves have a share of the reduction each, with stages of
+// their own and no barriers; their sums meet in LDS in a fixed order.
+template <int BM, bool GRAD, bool BF16, int NS>
+__device__ __forceinline__ void few_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
+  using C = Bf16Cfg<BM, 64, 1, 1, NS, 4>;
+  constexpr int PITCH = 68;  // floats of a row of results in LDS, over the stages
+  static_assert(BM * PITCH * 4 <= C::RING, "a wave's results lie over its stages");
+  const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K, stages = (red + 63) / 64;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const int k0 = stages * wv / 4 * 64, k1 = min(stages * (wv + 1) / 4 * 64, red);
+  const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
+  f32x4 acc[C::MF][C::NF];
+  const Operand ro{a.a + (size_t)row0 * red + k0, red, rows, nullptr, 0};
+  const Operand co{GRAD ? w + (size_t)k0 * a.K + n0 : w + (size_t)n0 * a.K + k0, a.K, min(64, cols - n0), nullptr, 0};
+  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, k1 - k0, lds + wv * C::RING, acc);
+  float* mine = (float*)(lds + wv * C::RING);
+#pragma unroll
+  for (int m = 0; m < C::MF; ++m)
+#pragma unroll
+    for (int f = 0; f < C::NF; ++f) *(f32x4*)(mine + (16 * m + r) * PITCH + 16 * f + 4 * g) = acc[m][f];
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * 16; i += 256) {
+    const int row = i / 16, c = i % 16 * 4;
+    const float* p = (const float*)lds + row * PITCH + c;
+    f32x4 v = *(const f32x4*)p;
+#pragma unroll
+    for (int q = 1; q < 4; ++q) v += *(const f32x4*)(p + q * (C::RING / 4));
+    if (n0 + c >= cols) continue;
+    const size_t at = (size_t)(row0 + row) * cols + n0 + c;
+    if constexpr (BF16)
+      *(u32x2*)((uint16_t*)a.out + at) = u32x2{(uint32_t)f32_to_bf16_bits(v[0]) | ((uint32_t)f32_to_bf16_bits(v[1]) << 16),
+                                               (uint32_t)f32_to_bf16_bits(v[2]) | ((uint32_t)f32_to_bf16_bits(v[3]) << 16)};
+    else
+      *(f32x4*)((float*)a.out + at) = v;
+  }
+  __syncthreads();  // the stages are free for the next tile
+}
+
+// ROWS 16: 16 rows a tile, two blocks a compute unit; 64: the least of 16, 32 and 64 that holds a tile's rows.
+template <int ROWS>
+constexpr int kFewLds = ROWS == 16 ? 4 * 2 * (16 + 64) * 128 : 4 * 2 * (64 + 64) * 128;
+
+template <int ROWS, bool GRAD, bool BF16>
+__global__ __launch_bounds__(256) void grouped_few_kernel(GroupedArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int cols = GRAD ? a.K : a.N;
+  const int ntn = (cols + 63) / 64;
+  const int E2 = a.g.E + 2;
+  int* li = (int*)(lds + kFewLds<ROWS>);
+  GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
+  list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + ROWS - 1) / ROWS * ntn; });
+  const int nitems = gl.item0[gl.n];
+  for (int it = blockIdx.x; it < nitems; it += gridDim.x) {
+    const int gi = find_group(gl.item0, gl.n, it);
+    const int local = __builtin_amdgcn_readfirstlane(it - gl.item0[gi]);
+    const int slot = __builtin_amdgcn_readfirstlane(gl.slot[gi]);
+    const int row0 = __builtin_amdgcn_readfirstlane(gl.row0[gi]), cnt = __builtin_amdgcn_readfirstlane(gl.cnt[gi]);
+    const int m0 = local / ntn * ROWS, n0 = local % ntn * 64, rows = min(ROWS, cnt - m0);
+    if (ROWS > 16 && rows > 32)
+      few_tile<64, GRAD, BF16, 2>(a, slot, row0 + m0, rows, n0, lds);
+    else if (ROWS > 16 && rows > 16)
+      few_tile<32, GRAD, BF16, 2>(a, slot, row0 + m0, rows, n0, lds);
+    else
+      few_tile<16, GRAD, BF16, 2>(a, slot, row0 + m0, rows, n0, lds);
+  }
+}
+
 template <class C, bool BF16, bool ADD>
 __global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -92,6 +162,20 @@ __global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
   bf16_tile<C, ACROSS, ACROSS>(ro, co, cnt, lds, acc);
   uint8_t* out = (uint8_t*)a.dw + ((size_t)e * a.N + m0) * a.K * (BF16 ? 2 : 4);
   store_rows<C::MF, C::NF, BF16, ADD>(acc, out, a.K, wv / C::WN * 16 * C::MF, ro.rows, n0 + wv % C::WN * 16 * C::NF, a.K, lane);
+}
+
+template <int ROWS, bool GRAD, bool BF16>
+hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
+  static LaunchCache cache;
+  LaunchFacts f;
+  const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
+  const long long ntn = (cols + 63) / 64, ntm = (P + ROWS - 1) / ROWS;
+  const size_t lds = kFewLds<ROWS> + group_lds_bytes(E);
+  hipError_t e = cache.get((const void*)grouped_few_kernel<ROWS, GRAD, BF16>, 256, lds, &f);
+  if (e != hipSuccess) return e;
+  const long long upper = std::min<long long>(P, ntm + E) * ntn, most = (long long)f.per_cu * f.cus;
+  hipLaunchKernelGGL((grouped_few_kernel<ROWS, GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(256), lds, s, a);
+  return hipGetLastError();
 }
 
 template <bool GRAD, bool BF16>
@@ -125,9 +209,43 @@ using T256 = Bf16Cfg<256, 256, 2, 4, 2>;
 
 }  // namespace
 
+// Which kernel, by times modelled for the rounds that the 256 compute units take, in us (a tile's start and end, and its
+// stages of 64): 256-column tiles, or blocks of 64 columns whose waves share the reduction.  How the rows lie is known on
+// the device only: as if experts were drawn evenly.  Measured, us, 256-column tiles / 64-column blocks, bf16 results:
+//   forward, 128 experts of 1536 x 2048, top 8 of   1 token  18.9 / 11.8    4  34.4 / 29.9    8  70.7 / 60.6    64  143.6 / 137.7
+//                                                  256  148.8 / 147.3    512  154.1 / 160.8    4096 (Zipf)  325 / 533
+//   rows' gradient, the same                         1  17.3 / 11.9    4  32.5 / 33.2    16  99.3 / 110.5    256  147.4 / 178.8
+//   one matrix of 4096 x 4096, rows                 64  31.2 / 16.0    300  73.8 / 29.8
+// With few rows the forward product is bound by the matrices' bytes, which the smaller blocks read at 5.7 - 6.1 TB/s, the larger
+// ones at 5.3 - 5.6; in the rows' gradient, whose 64 columns are 128 bytes of a memory row, it is the other way round.
+// 16 rows a block, two blocks a unit, where 64 would leave most units without one (64 rows, 4096 x 4096: 16.0 -> 12.2).
+template <bool GRAD>
+int choose(const GroupedArgs& a) {
+  const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
+  const double held = a.g.slot_of ? std::min(1.0, (double)a.g.n_slots / a.g.E) : 1.0;
+  const double rows = std::max(1.0, held * a.g.P), groups = std::max(1.0, held * a.g.E * (1.0 - std::exp(-(double)a.g.P / a.g.E)));
+  const double each = rows / groups, stages = (red + 63) / 64;
+  auto blocks = [&](int h, int w) { return std::max(groups, rows / h + (each > h ? 0.5 : 0.0) * groups) * ((cols + w - 1) / w); };
+  const double few = std::ceil(blocks(64, 64) / 256) * (3.5 + stages / 4 * 0.8);
+  const double tiles = std::ceil(blocks(256, 256) / 256) * (3.5 + stages * (0.3 + 0.8 * std::min(each, 256.0) / 256));
+  if (few < tiles || (!GRAD && each <= 16)) return blocks(64, 64) < 100 ? 16 : 64;
+  return 256;
+}
+
+template <bool GRAD, bool BF16>
+hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
+  // tiles of all groups in an int whatever the table holds: one that does not ascend can give all rows to every second expert
+  if ((a.g.P / 16 + 2LL) * (a.g.E / 2 + 1) * (((GRAD ? a.K : a.N) + 63) / 64) >= 1LL << 31) return launch_tiles<GRAD, BF16>(a, s);
+  switch (choose<GRAD>(a)) {
+    case 16: return launch_few<16, GRAD, BF16>(a, s);
+    case 64: return launch_few<64, GRAD, BF16>(a, s);
+    default: return launch_tiles<GRAD, BF16>(a, s);
+  }
+}
+
 hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s) {
-  if (kind == 0) return a.out_bf16 ? launch_tiles<false, true>(a, s) : launch_tiles<false, false>(a, s);
-  return a.out_bf16 ? launch_tiles<true, true>(a, s) : launch_tiles<true, false>(a, s);
+  if (kind == 0) return a.out_bf16 ? launch_grouped_as<false, true>(a, s) : launch_grouped_as<false, false>(a, s);
+  return a.out_bf16 ? launch_grouped_as<true, true>(a, s) : launch_grouped_as<true, false>(a, s);
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {

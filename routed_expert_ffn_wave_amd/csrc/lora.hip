@@ -365,7 +365,7 @@ bool lora_small(int T, int E, int r, int N, int K) {
 // 16 shares: 64.5 / 48.7 / 44.9 / 48.0 / 59.0).  0: no hidden rows in memory.
 int lora_splits(int T, int E, int r, int N, int K) {
   if (lora_small(T, E, r, N, K)) return 0;
-  const long long c = chunks(T, E, 64), s = std::min<long long>({(288 + c - 1) / c, K / 512, 16});
+  const long long c = chunks(T, E, 64), s = std::min<long long>({(256 + c / 2) / c, K / 512, 16});
   return s < 1 ? 1 : (int)s;
 }
 
