@@ -9,8 +9,9 @@
  *
  * Every convention of ft_moe.h holds here: device pointers, 16-byte aligned, dense row-major arrays,
  * caller-owned buffers, enqueue-only on `stream`, FT_OK or a status with ft_moe_last_error(), calls
- * reentrant and capturable into a graph.  Only ft_moe_lora needs a workspace; no call keeps any state, and no
- * result depends on the order in which blocks run: the same inputs give the same bits.  Outputs must not
+ * reentrant and capturable into a graph.  No call keeps any state, and no result depends on the order in which
+ * blocks run: the same inputs give the same bits.  Workspaces' contents do not matter; calls that may overlap, and graphs
+ * that may, need their own.  Outputs must not
  * overlap inputs or each other, except where said.  Sizes of 0 rows are no-ops, except where said.
  *
  * Rows of an expert.  offsets int32 [E+1] as from ft_moe_permute: expert e has rows offsets[e] .. offsets[e+1]-1
@@ -33,6 +34,9 @@ extern "C" {
 /* Flag of ft_moe_grouped_matmul_wgrad: dw += the gradient (fp32 dw). */
 #define FT_ADD_TO_OUT 0x40
 
+/* Bytes of workspace for the three products below of these sizes, each; 0 where none is needed (ws may be NULL). */
+size_t ft_moe_grouped_matmul_workspace(int P, int N, int K, int E);
+
 /*
  * out[p][n] = sum_k a[p][k] * w[slot][n][k] for the rows p of every expert.
  * a bf16 [P][K], w bf16 [n_slots][N][K], out fp32 [P][N], or bf16 with FT_OUT_BF16.  N % 8 == 0, K % 8 == 0, both at
@@ -40,15 +44,16 @@ extern "C" {
  * does not ascend gives to several experts is the result of one or another of them.
  */
 int ft_moe_grouped_matmul(const uint16_t* a, int P, const uint16_t* w, int n_slots, int N, int K, const int32_t* offsets,
-                          const int32_t* slot_of_expert, int E, void* out, int flags, hipStream_t stream);
+                          const int32_t* slot_of_expert, int E, void* out, void* ws, size_t ws_bytes, int flags,
+                          hipStream_t stream);
 
 /*
  * The gradient of its rows: da[p][k] = sum_n dout[p][n] * w[slot][n][k].  dout bf16 [P][N], da fp32 [P][K], or
  * bf16 with FT_OUT_BF16; everything else as above.
  */
 int ft_moe_grouped_matmul_grad(const uint16_t* dout, int P, const uint16_t* w, int n_slots, int N, int K,
-                               const int32_t* offsets, const int32_t* slot_of_expert, int E, void* da, int flags,
-                               hipStream_t stream);
+                               const int32_t* offsets, const int32_t* slot_of_expert, int E, void* da, void* ws,
+                               size_t ws_bytes, int flags, hipStream_t stream);
 
 /*
  * The gradient of its matrices, by expert: dw[e][n][k] = sum over the expert's rows p of dout[p][n] * a[p][k].
@@ -59,7 +64,8 @@ int ft_moe_grouped_matmul_grad(const uint16_t* dout, int P, const uint16_t* w, i
  * parts as its gradient; the caller adds them.)
  */
 int ft_moe_grouped_matmul_wgrad(const uint16_t* dout, const uint16_t* a, int P, int N, int K, const int32_t* offsets,
-                                const int32_t* slot_of_expert, int E, void* dw, int flags, hipStream_t stream);
+                                const int32_t* slot_of_expert, int E, void* dw, void* ws, size_t ws_bytes, int flags,
+                                hipStream_t stream);
 
 /*
  * h = SiLU(g) * u, SiLU(g) = g / (1 + e^-g), formed in fp32 and rounded once.  gu bf16 [rows][2 I]: gate columns
@@ -88,8 +94,7 @@ int ft_moe_swiglu_grad(const uint16_t* gu, const uint16_t* dh, int rows, int I, 
  * does not name is left as it was, one that it names twice is formed twice (with out == base: added twice or once).
  * r % 8 == 0, r <= 256 (adapters of smaller rank: zeros behind), N % 8 == 0, K % 8 == 0, both at most 2^20.
  * The inner sums are held in fp32 and enter the outer ones as two bf16 terms, within 2^-16 of themselves.
- * ws: ft_moe_lora_workspace(T, E, r, N, K) bytes of device memory (0 for few rows: then ws may be NULL); contents do not matter.  Calls that may
- * overlap, and graphs that may, need their own.
+ * ws: ft_moe_lora_workspace(T, E, r, N, K) bytes of device memory (0 for few rows: then ws may be NULL).
  */
 size_t ft_moe_lora_workspace(int T, int E, int r, int N, int K);
 int ft_moe_lora(const void* base, const uint16_t* x, int T, const uint16_t* a, const uint16_t* b, const float* scale,

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "bf16_plan.h"
 #include "bf16_tile.h"
 #include "ft_groups.h"
 #include "ft_kernels.h"
@@ -16,13 +17,6 @@
 namespace ftk {
 namespace {
 
-__device__ __forceinline__ bool group_of(const RowGroups& s, int e, int& slot, int& row0, int& cnt) {
-  slot = s.slot_of ? s.slot_of[e] : e;
-  row0 = min(max(s.offsets[e], 0), s.P);
-  cnt = max(min(max(s.offsets[e + 1], 0), s.P) - row0, 0);
-  return (uint32_t)slot < s.n_slots;
-}
-
 template <class ItemsOf>
 __device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, int* tmp, ItemsOf items_of) {
   build_group_list(
@@ -30,9 +24,9 @@ __device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, in
 }
 
 // A tile of up to BM rows takes the least of these heights that holds its rows.
-template <int BM, bool GRAD, bool BF16>
-__device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
-  using C = Bf16Cfg<BM, 256, 2, 4, BM == 64 ? 3 : 2>;
+template <int BM, bool GRAD, bool BF16, class Next>
+__device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds, Next next) {
+  using C = Bf16Cfg<BM, 256, 2, 4, BM <= 128 ? 3 : 2>;
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
@@ -40,19 +34,36 @@ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int
   const Operand ro{a.a + (size_t)row0 * red, red, rows, nullptr, 0};
   const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0), nullptr, 0};
   bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, red, lds, acc);
+  next();
   uint8_t* out = (uint8_t*)a.out + (size_t)row0 * cols * (BF16 ? 2 : 4);
   store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, lane);
 }
 
-constexpr int kTileLds = 2 * (256 + 256) * 128;
+constexpr int kTileLds = 3 * (128 + 256) * 128;
 
-// Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the tile list, so that tiles that run
-// together share rows and matrices through its L2: bands of 4 row tiles, column tiles within a band in turn.
+// Tile `local` of `rows` rows: bands of 4 row tiles, column tiles within a band in turn.
+template <bool GRAD, bool BF16, class Next>
+__device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int row0, int cnt, int local, uint8_t* lds, Next next) {
+  constexpr int BAND = 4;
+  const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
+  const int band = local / (BAND * ntn), h = min(BAND, (cnt + 255) / 256 - band * BAND), in = local - band * BAND * ntn;
+  const int m0 = (band * BAND + in % h) * 256, n0 = in / h * 256, rows = min(256, cnt - m0);
+  if (rows > 192)
+    grouped_tile<256, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
+  else if (rows > 128)
+    grouped_tile<192, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
+  else if (rows > 64)
+    grouped_tile<128, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
+  else
+    grouped_tile<64, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
+}
+
+// Up to two tiles a block: fixed shares.  Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of
+// the tile list, so that tiles that run together share rows and matrices through its L2.
 template <bool GRAD, bool BF16>
 __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  const int cols = GRAD ? a.K : a.N;
-  const int ntn = (cols + 255) / 256;
+  const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
   const int E2 = a.g.E + 2;
   int* li = (int*)(lds + kTileLds);
   GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
@@ -61,21 +72,27 @@ __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   const int per = gridDim.x / 8, lb = (blockIdx.x % 8) * per + blockIdx.x / 8;  // gridDim.x % 8 == 0
   for (int it = lb; it < nitems; it += gridDim.x) {
     const int gi = find_group(gl.item0, gl.n, it);
-    const int local = __builtin_amdgcn_readfirstlane(it - gl.item0[gi]);
-    const int slot = __builtin_amdgcn_readfirstlane(gl.slot[gi]);
-    const int row0 = __builtin_amdgcn_readfirstlane(gl.row0[gi]), cnt = __builtin_amdgcn_readfirstlane(gl.cnt[gi]);
-    constexpr int BAND = 4;
-    const int band = local / (BAND * ntn), h = min(BAND, (cnt + 255) / 256 - band * BAND), in = local - band * BAND * ntn;
-    const int m0 = (band * BAND + in % h) * 256, n0 = in / h * 256, rows = min(256, cnt - m0);
-    if (rows > 192)
-      grouped_tile<256, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
-    else if (rows > 128)
-      grouped_tile<192, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
-    else if (rows > 64)
-      grouped_tile<128, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
-    else
-      grouped_tile<64, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+    grouped_item<GRAD, BF16>(a, __builtin_amdgcn_readfirstlane(gl.slot[gi]), __builtin_amdgcn_readfirstlane(gl.row0[gi]),
+                             __builtin_amdgcn_readfirstlane(gl.cnt[gi]), __builtin_amdgcn_readfirstlane(it - gl.item0[gi]), lds, [] {});
   }
+}
+
+// More: planned, by classes of experts with more than 192, 128, 64 rows, and the rest.  (A lower last tile stays beside the
+// whole ones of its expert, whose matrix it shares.)
+__global__ __launch_bounds__(kPlanThreads) void grouped_plan_kernel(RowGroups g, int ntn, Plan* plan) {
+  make_plan(g, plan, [&](int slot, int, int row0, int cnt, int (&cls)[2], int (&tiles)[2], PlanPart (&part)[2]) {
+    if (cnt == 0) return;
+    cls[0] = 0, tiles[0] = (cnt + 255) / 256 * ntn;
+    part[0] = PlanPart{slot, row0, cnt, 0};
+  });
+}
+
+template <bool GRAD, bool BF16>
+__global__ __launch_bounds__(512, 2) void grouped_planned_kernel(GroupedArgs a, Plan* plan) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  run_plan(plan, (int*)(lds + kTileLds), [&](const PlanPart& part, int local, auto next) {
+    grouped_item<GRAD, BF16>(a, part.slot, part.row0, part.rows, local, lds, next);
+  });
 }
 
 // Few rows an expert: BM rows by 64 columns a block, whose four waves have a share of the reduction each, with stages of
@@ -145,23 +162,46 @@ __global__ __launch_bounds__(256) void grouped_few_kernel(GroupedArgs a) {
   }
 }
 
-template <class C, bool BF16, bool ADD>
-__global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  const int ntm = (a.N + C::BM - 1) / C::BM, ntn = (a.K + C::BN - 1) / C::BN, tiles = ntm * ntn;
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e = blockIdx.x / tiles, t = blockIdx.x % tiles;
-  int slot, row0, cnt;
-  if (!group_of(a.g, e, slot, row0, cnt)) return;
-  row0 = __builtin_amdgcn_readfirstlane(row0), cnt = __builtin_amdgcn_readfirstlane(cnt);
-  if (ADD && cnt == 0) return;
+template <class C, bool BF16, bool ADD, class Next>
+__device__ __forceinline__ void wgrad_item(const WgradArgs& a, int e, int row0, int cnt, int t, uint8_t* lds, Next next) {
+  const int ntn = (a.K + C::BN - 1) / C::BN, lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (ADD && cnt == 0) return next();
   const int m0 = t / ntn * C::BM, n0 = t % ntn * C::BN;
   f32x4 acc[C::MF][C::NF];
   const Operand ro{a.dout + (size_t)row0 * a.N + m0, a.N, min(C::BM, a.N - m0), nullptr, 0};
   const Operand co{a.a + (size_t)row0 * a.K + n0, a.K, min(C::BN, a.K - n0), nullptr, 0};
   bf16_tile<C, ACROSS, ACROSS>(ro, co, cnt, lds, acc);
+  next();
   uint8_t* out = (uint8_t*)a.dw + ((size_t)e * a.N + m0) * a.K * (BF16 ? 2 : 4);
   store_rows<C::MF, C::NF, BF16, ADD>(acc, out, a.K, wv / C::WN * 16 * C::MF, ro.rows, n0 + wv % C::WN * 16 * C::NF, a.K, lane);
+}
+
+template <class C, bool BF16, bool ADD>
+__global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int tiles = (a.N + C::BM - 1) / C::BM * ((a.K + C::BN - 1) / C::BN);
+  const int e = blockIdx.x / tiles;
+  int slot, row0, cnt;
+  if (!group_of(a.g, e, slot, row0, cnt)) return;
+  wgrad_item<C, BF16, ADD>(a, e, __builtin_amdgcn_readfirstlane(row0), __builtin_amdgcn_readfirstlane(cnt), blockIdx.x % tiles, lds, [] {});
+}
+
+// Classes of experts by their rows: above 2048, 1024, ... 64, and the rest.
+__global__ __launch_bounds__(kPlanThreads) void wgrad_plan_kernel(RowGroups g, int ntiles, Plan* plan) {
+  make_plan(g, plan, [&](int, int e, int row0, int cnt, int (&cls)[2], int (&tiles)[2], PlanPart (&part)[2]) {
+    cls[0] = 0;
+    for (int c = 2048; c >= 64 && cnt <= c; c >>= 1) ++cls[0];
+    tiles[0] = ntiles;
+    part[0] = PlanPart{e, row0, cnt, 0};
+  });
+}
+
+template <class C, bool BF16, bool ADD>
+__global__ __launch_bounds__(C::NT, 2) void wgrad_planned_kernel(WgradArgs a, Plan* plan) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  run_plan(plan, (int*)(lds + C::LDS), [&](const PlanPart& part, int local, auto next) {
+    wgrad_item<C, BF16, ADD>(a, part.slot, part.row0, part.rows, local, lds, next);
+  });
 }
 
 template <int ROWS, bool GRAD, bool BF16>
@@ -178,27 +218,50 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Tiles of a product, at most: more than two a compute unit are planned.
+long long most_tiles(const RowGroups& g, int cols) { return ((g.P + 255) / 256 + (long long)std::min(g.E, g.P)) * ((cols + 255) / 256); }
+long long most_tiles_w(const RowGroups& g, int N, int K) { return (long long)((N + 255) / 256) * ((K + 255) / 256) * g.E; }
+constexpr int kPlanFrom = 512;
+
 template <bool GRAD, bool BF16>
 hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
-  static LaunchCache cache;
+  static LaunchCache cache, planned;
   LaunchFacts f;
   const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
-  const long long ntn = (cols + 255) / 256, ntm = (P + 255) / 256;
+  const long long ntn = (cols + 255) / 256, tiles = most_tiles(a.g, cols);
   if ((P / 256 + 2LL) * (E / 2 + 1) * ntn >= 1LL << 31) return hipErrorNotSupported;
+  if (tiles > kPlanFrom) {
+    const size_t lds = kTileLds + (size_t)2 * E * sizeof(int);
+    hipError_t e = planned.get((const void*)grouped_planned_kernel<GRAD, BF16>, 512, lds, &f);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(grouped_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a.g, (int)ntn, (Plan*)a.ws);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((grouped_planned_kernel<GRAD, BF16>), dim3(f.per_cu * f.cus), dim3(512), lds, s, a, (Plan*)a.ws);
+    return hipGetLastError();
+  }
   const size_t lds = kTileLds + group_lds_bytes(E);
   hipError_t e = cache.get((const void*)grouped_tile_kernel<GRAD, BF16>, 512, lds, &f);
   if (e != hipSuccess) return e;
-  const long long upper = ((ntm + (E < P ? E : P)) * ntn + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
+  const long long upper = (tiles + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
   hipLaunchKernelGGL((grouped_tile_kernel<GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(512), lds, s, a);
   return hipGetLastError();
 }
 
 template <class C, bool BF16, bool ADD>
 hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
-  static LaunchCache cache;
+  static LaunchCache cache, planned;
   LaunchFacts f;
-  const long long blocks = (long long)((a.N + C::BM - 1) / C::BM) * ((a.K + C::BN - 1) / C::BN) * a.g.E;
-  if (blocks * C::NT >= 1LL << 32) return hipErrorNotSupported;
+  const long long blocks = most_tiles_w(a.g, a.N, a.K);
+  if (blocks >= 1LL << 31) return hipErrorNotSupported;
+  if (blocks > kPlanFrom) {
+    const size_t lds = C::LDS + (size_t)2 * a.g.E * sizeof(int);
+    hipError_t e = planned.get((const void*)wgrad_planned_kernel<C, BF16, ADD>, C::NT, lds, &f);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(wgrad_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a.g, (int)(blocks / a.g.E), (Plan*)a.ws);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((wgrad_planned_kernel<C, BF16, ADD>), dim3(f.per_cu * f.cus), dim3(C::NT), lds, s, a, (Plan*)a.ws);
+    return hipGetLastError();
+  }
   hipError_t e = cache.get((const void*)wgrad_tile_kernel<C, BF16, ADD>, C::NT, C::LDS, &f);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((wgrad_tile_kernel<C, BF16, ADD>), dim3((uint32_t)blocks), dim3(C::NT), C::LDS, s, a);
@@ -206,8 +269,6 @@ hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
 }
 
 using T256 = Bf16Cfg<256, 256, 2, 4, 2>;
-
-}  // namespace
 
 // Which kernel, by times modelled for the rounds that the 256 compute units take, in us (a tile's start and end, and its
 // stages of 64): 256-column tiles, or blocks of 64 columns whose waves share the reduction.  How the rows lie is known on
@@ -241,6 +302,13 @@ hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
     case 64: return launch_few<64, GRAD, BF16>(a, s);
     default: return launch_tiles<GRAD, BF16>(a, s);
   }
+}
+
+}  // namespace
+
+size_t grouped_workspace(int P, int N, int K, int E) {
+  const RowGroups g{nullptr, nullptr, E, P, 0};
+  return std::max({most_tiles(g, N), most_tiles(g, K), most_tiles_w(g, N, K)}) > kPlanFrom ? plan_bytes(E) : 0;
 }
 
 hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s) {

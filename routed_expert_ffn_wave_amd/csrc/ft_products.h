@@ -20,7 +20,10 @@ struct GroupedArgs {
   int N, K;
   void* out;
   bool out_bf16;
+  void* ws;
 };
+// Bytes of ws that each of the products of these sizes is content with (0: none needs any).
+size_t grouped_workspace(int P, int N, int K, int E);
 hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s);
 
 // dw[E][N][K] = dout[P][N]^T a[P][K] by expert, or += with add (fp32)
@@ -30,6 +33,7 @@ struct WgradArgs {
   int N, K;
   void* dw;
   bool out_bf16, add;
+  void* ws;
 };
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s);
 

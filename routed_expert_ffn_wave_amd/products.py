@@ -16,20 +16,21 @@ from .rows import _BF, _F32, _FLOATS, _I32, _first, _new, _product_out, _refuse,
 
 FT_ADD_TO_OUT = 0x40
 
-_P, _i = ctypes.c_void_p, ctypes.c_int
+_P, _i, _z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _SIG = {
-    "ft_moe_grouped_matmul": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _i, _P],
-    "ft_moe_grouped_matmul_grad": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _i, _P],
-    "ft_moe_grouped_matmul_wgrad": [_P, _P, _i, _i, _i, _P, _P, _i, _P, _i, _P],
+    "ft_moe_grouped_matmul_workspace": [_i, _i, _i, _i],
+    "ft_moe_grouped_matmul": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _P, _z, _i, _P],
+    "ft_moe_grouped_matmul_grad": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _P, _z, _i, _P],
+    "ft_moe_grouped_matmul_wgrad": [_P, _P, _i, _i, _i, _P, _P, _i, _P, _P, _z, _i, _P],
     "ft_moe_swiglu": [_P, _i, _i, _P, _P],
     "ft_moe_swiglu_grad": [_P, _P, _i, _i, _P, _P],
     "ft_moe_lora_workspace": [_i, _i, _i, _i, _i],
-    "ft_moe_lora": [_P, _P, _i, _P, _P, _P, _i, _i, _i, _i, _P, _P, _P, _i, _P, _P, ctypes.c_size_t, _i, _P],
+    "ft_moe_lora": [_P, _P, _i, _P, _P, _P, _i, _i, _i, _i, _P, _P, _P, _i, _P, _P, _z, _i, _P],
 }
 for _name, _args in _SIG.items():
     _f = getattr(lib, _name)
     _f.argtypes, _f.restype = _args, _i
-lib.ft_moe_lora_workspace.restype = ctypes.c_size_t
+lib.ft_moe_lora_workspace.restype = lib.ft_moe_grouped_matmul_workspace.restype = _z
 
 EXPORTED_PRODUCTS = tuple(_SIG)
 
@@ -49,20 +50,38 @@ def _matrices(w, name: str):
     return w.shape
 
 
-def ft_moe_grouped_matmul(a, w, offsets, slot_of_expert=None, out=None, out_dtype=torch.bfloat16, stream=None):
+def _workspace(ws, need, dev: int, stream, *args):
+    """(the workspace tensor, its address, its bytes): `ws`, or where the call needs one, a new one of need(*args) bytes."""
+    if ws is None:
+        n = need(*args)
+        if n == 0:
+            return None, None, 0
+        ws = _new((n,), torch.uint8, dev, stream)
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(f"ws must be a contiguous tensor on cuda:{dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def ft_moe_grouped_matmul_workspace(P: int, N: int, K: int, E: int) -> int:
+    return lib.ft_moe_grouped_matmul_workspace(P, N, K, E)
+
+
+def ft_moe_grouped_matmul(a, w, offsets, slot_of_expert=None, out=None, out_dtype=torch.bfloat16, stream=None, ws=None):
     """bf16 rows a [P][K] in expert order, each expert's rows times its matrix of w [n_slots][N][K] transposed: [P][N]
     in bf16, or in fp32 with out_dtype=torch.float32 (or an fp32 `out`).  Rows of experts without a slot are left as they
-    were (with out=None: unset).  slot_of_expert None: expert e has matrix e."""
+    were (with out=None: unset).  slot_of_expert None: expert e has matrix e.  `ws`, here and in the two calls below:
+    ft_moe_grouped_matmul_workspace(P, N, K, E) bytes (made for the call when not given)."""
     dev, (P, K) = _first(a, "a", 2, (_BF,), stream)
     n_slots, N, _ = _matrices(w, "w")
     pw = _take(w, "w", (_BF,), (n_slots, N, K), dev)
     pf, pt, E = _groups(offsets, slot_of_expert, "slot_of_expert", dev)
     out, po, flags = _product_out(out, out_dtype, (P, N), dev, stream)
-    _run(lib.ft_moe_grouped_matmul, dev, stream, a.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, flags)
+    ws, pws, nw = _workspace(ws, lib.ft_moe_grouped_matmul_workspace, dev, stream, P, N, K, E)
+    _run(lib.ft_moe_grouped_matmul, dev, stream, a.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, pws, nw, flags)
     return out
 
 
-def ft_moe_grouped_matmul_grad(dout, w, offsets, slot_of_expert=None, da=None, out_dtype=torch.bfloat16, stream=None):
+def ft_moe_grouped_matmul_grad(dout, w, offsets, slot_of_expert=None, da=None, out_dtype=torch.bfloat16, stream=None, ws=None):
     """Gradient of ft_moe_grouped_matmul's rows: dout [P][N] in expert order times the experts' matrices of
     w [n_slots][N][K]: [P][K] in bf16 or fp32."""
     dev, (P, N) = _first(dout, "dout", 2, (_BF,), stream)
@@ -70,12 +89,13 @@ def ft_moe_grouped_matmul_grad(dout, w, offsets, slot_of_expert=None, da=None, o
     pw = _take(w, "w", (_BF,), (n_slots, N, K), dev)
     pf, pt, E = _groups(offsets, slot_of_expert, "slot_of_expert", dev)
     da, po, flags = _product_out(da, out_dtype, (P, K), dev, stream)
-    _run(lib.ft_moe_grouped_matmul_grad, dev, stream, dout.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, flags)
+    ws, pws, nw = _workspace(ws, lib.ft_moe_grouped_matmul_workspace, dev, stream, P, N, K, E)
+    _run(lib.ft_moe_grouped_matmul_grad, dev, stream, dout.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, pws, nw, flags)
     return da
 
 
 def ft_moe_grouped_matmul_wgrad(dout, a, offsets, slot_of_expert=None, dw=None, out_dtype=torch.float32, add=False, stream=None,
-                                n_slots=None):
+                                n_slots=None, ws=None):
     """Gradient of ft_moe_grouped_matmul's matrices, by expert: dw[e] = dout_e^T a_e [E][N][K] of the rows dout [P][N] and
     a [P][K] of every expert, in fp32 (add: dw += it) or bf16; zeros for an expert without rows.  Experts that
     slot_of_expert gives no slot (in [0, n_slots), where n_slots is given) are left as they were."""
@@ -89,7 +109,8 @@ def ft_moe_grouped_matmul_wgrad(dout, a, offsets, slot_of_expert=None, dw=None, 
         _refuse("n_slots is given without slot_of_expert")
     fl = (0 if n_slots is None else FT_N_SLOTS(n_slots)) | (FT_ADD_TO_OUT if add else 0)
     dw, po, flags = _product_out(dw, out_dtype, (E, N, K), dev, stream)
-    _run(lib.ft_moe_grouped_matmul_wgrad, dev, stream, dout.data_ptr(), pa, P, N, K, pf, pt, E, po, flags | fl)
+    ws, pws, nw = _workspace(ws, lib.ft_moe_grouped_matmul_workspace, dev, stream, P, N, K, E)
+    _run(lib.ft_moe_grouped_matmul_wgrad, dev, stream, dout.data_ptr(), pa, P, N, K, pf, pt, E, po, pws, nw, flags | fl)
     return dw
 
 
@@ -137,13 +158,7 @@ def ft_moe_lora(base, x, a, b, offsets, gather, slot_of_adapter=None, scale=None
     if out is None:
         out = _new((T, N), base.dtype, dev, stream)
     po = _take(out, "out", (base.dtype,), (T, N), dev)
-    if ws is None:
-        need = lib.ft_moe_lora_workspace(T, E, r, N, K)
-        if need:
-            ws = _new((need,), torch.uint8, dev, stream)
-    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
-        _refuse(f"ws must be a contiguous tensor on cuda:{dev}")
-    pw, nw = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    ws, pw, nw = _workspace(ws, lib.ft_moe_lora_workspace, dev, stream, T, E, r, N, K)
     _run(lib.ft_moe_lora, dev, stream, base.data_ptr(), px, T, pa, pb, ps, n_slots, r, N, K, pf, pg, pt, E, po, pw, nw,
          FT_OUT_BF16 if base.dtype is _BF else 0)
     return out

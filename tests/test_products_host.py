@@ -32,12 +32,12 @@ def test_every_declared_symbol_is_exported():
     assert int(re.search(r"#define FT_ADD_TO_OUT (0x\w+)", open(HEADER).read()).group(1), 16) == ft.FT_ADD_TO_OUT
 
 
-def grouped(name, a=A, P=4, w=A, n=8, N=64, K=64, off=A, slot=None, E=8, out=B, f=0):
-    return getattr(L, "ft_moe_grouped_matmul" + name)(a, P, w, n, N, K, off, slot, E, out, f, None)
+def grouped(name, a=A, P=4, w=A, n=8, N=64, K=64, off=A, slot=None, E=8, out=B, ws=B, nb=1 << 20, f=0):
+    return getattr(L, "ft_moe_grouped_matmul" + name)(a, P, w, n, N, K, off, slot, E, out, ws, nb, f, None)
 
 
-def wgrad(d=A, a=A, P=4, N=64, K=64, off=A, slot=None, E=8, dw=B, f=0):
-    return L.ft_moe_grouped_matmul_wgrad(d, a, P, N, K, off, slot, E, dw, f, None)
+def wgrad(d=A, a=A, P=4, N=64, K=64, off=A, slot=None, E=8, dw=B, ws=B, nb=1 << 20, f=0):
+    return L.ft_moe_grouped_matmul_wgrad(d, a, P, N, K, off, slot, E, dw, ws, nb, f, None)
 
 
 def lora(base=A, x=A, T=4, a=A, b=A, s=None, n=8, r=16, N=64, K=64, off=A, ga=A, slot=None, E=8, out=B, ws=B, nb=1 << 20, f=0):
@@ -70,6 +70,20 @@ def test_wgrad_refusals():
     assert wgrad(P=0, d=None, a=None, off=None, dw=None, f=ft.FT_ADD_TO_OUT) == ft.FT_OK
     err(wgrad(P=0, d=None, a=None, dw=None), ft.FT_E_INVAL, "dw is null")  # without rows dw is zeroed
     err(wgrad(N=1 << 20, K=1 << 20, E=1024), ft.FT_E_UNSUPPORTED, "gradient too large")
+
+
+def test_grouped_workspace():
+    need = ft.ft_moe_grouped_matmul_workspace
+    assert need(8, 1536, 2048, 8) == 0
+    big = need(32768, 1536, 2048, 128)
+    assert 128 * 2 * 16 <= big <= 1 << 16
+    for bad in ((-1, 64, 64, 8), (1 << 30, 64, 64, 0), (4096, 0, 64, 8), (4096, 64, 0, 8), (4096, 64, 64, 1025)):
+        assert need(*bad) == 0
+    for call in (lambda **kw: grouped("", P=32768, N=1536, K=2048, E=128, n=128, **kw), lambda **kw: grouped("_grad", P=32768, N=1536, K=2048, E=128, n=128, **kw),
+                 lambda **kw: wgrad(P=32768, N=1536, K=2048, E=128, **kw)):
+        err(call(ws=None), ft.FT_E_INVAL, "ws is null")
+        err(call(ws=MIS), ft.FT_E_INVAL, "ws is not 16")
+        err(call(nb=big - 1), ft.FT_E_WORKSPACE, "workspace of")
 
 
 def test_swiglu_refusals():
