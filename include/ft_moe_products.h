@@ -34,9 +34,6 @@ extern "C" {
 /* Flag of ft_moe_grouped_matmul_wgrad: dw += the gradient (fp32 dw). */
 #define FT_ADD_TO_OUT 0x40
 
-/* Bytes of workspace for the three products below of these sizes, each; 0 where none is needed (ws may be NULL). */
-size_t ft_moe_grouped_matmul_workspace(int P, int N, int K, int E);
-
 /*
  * out[p][n] = sum_k a[p][k] * w[slot][n][k] for the rows p of every expert.
  * a bf16 [P][K], w bf16 [n_slots][N][K], out fp32 [P][N], or bf16 with FT_OUT_BF16.  N % 8 == 0, K % 8 == 0, both at
@@ -44,16 +41,15 @@ size_t ft_moe_grouped_matmul_workspace(int P, int N, int K, int E);
  * does not ascend gives to several experts is the result of one or another of them.
  */
 int ft_moe_grouped_matmul(const uint16_t* a, int P, const uint16_t* w, int n_slots, int N, int K, const int32_t* offsets,
-                          const int32_t* slot_of_expert, int E, void* out, void* ws, size_t ws_bytes, int flags,
-                          hipStream_t stream);
+                          const int32_t* slot_of_expert, int E, void* out, int flags, hipStream_t stream);
 
 /*
  * The gradient of its rows: da[p][k] = sum_n dout[p][n] * w[slot][n][k].  dout bf16 [P][N], da fp32 [P][K], or
  * bf16 with FT_OUT_BF16; everything else as above.
  */
 int ft_moe_grouped_matmul_grad(const uint16_t* dout, int P, const uint16_t* w, int n_slots, int N, int K,
-                               const int32_t* offsets, const int32_t* slot_of_expert, int E, void* da, void* ws,
-                               size_t ws_bytes, int flags, hipStream_t stream);
+                               const int32_t* offsets, const int32_t* slot_of_expert, int E, void* da, int flags,
+                               hipStream_t stream);
 
 /*
  * The gradient of its matrices, by expert: dw[e][n][k] = sum over the expert's rows p of dout[p][n] * a[p][k].
@@ -62,7 +58,9 @@ int ft_moe_grouped_matmul_grad(const uint16_t* dout, int P, const uint16_t* w, i
  * slot_of_expert here only says which experts count (NULL: all): where an entry is negative, or not below n with
  * FT_N_SLOTS(n), the expert's part of dw is left as it was.  (A matrix that several experts name has the sum of their
  * parts as its gradient; the caller adds them.)
+ * ws: ft_moe_grouped_matmul_wgrad_workspace(N, K, E) bytes of device memory (0 for few tiles: then ws may be NULL).
  */
+size_t ft_moe_grouped_matmul_wgrad_workspace(int N, int K, int E);
 int ft_moe_grouped_matmul_wgrad(const uint16_t* dout, const uint16_t* a, int P, int N, int K, const int32_t* offsets,
                                 const int32_t* slot_of_expert, int E, void* dw, void* ws, size_t ws_bytes, int flags,
                                 hipStream_t stream);

@@ -28,16 +28,8 @@ int check_slots(int n_slots, const int32_t* slot_of, const char* name, int E) {
   return FT_OK;
 }
 
-int check_grouped_ws(int P, int N, int K, int E, const void* ws, size_t ws_bytes) {
-  const size_t need = grouped_workspace(P, N, K, E);
-  if (need == 0) return FT_OK;
-  CHECK_PTR(ws, "ws");
-  REQUIRE(ws_bytes >= need, FT_E_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
-  return FT_OK;
-}
-
 int run_grouped(int kind, const char* what, const char* in_name, const char* out_name, const uint16_t* in, int P, const uint16_t* w,
-                int n_slots, int N, int K, const int32_t* offsets, const int32_t* slot_of, int E, void* out, void* ws, size_t ws_bytes, int flags,
+                int n_slots, int N, int K, const int32_t* offsets, const int32_t* slot_of, int E, void* out, int flags,
                 hipStream_t stream) {
   int rc = check_groups(P, "P", E, N, K, flags, FT_OUT_BF16);
   if (rc) return rc;
@@ -48,8 +40,7 @@ int run_grouped(int kind, const char* what, const char* in_name, const char* out
   CHECK_PTR(w, "w");
   CHECK_PTR(offsets, "offsets");
   CHECK_PTR(out, out_name);
-  if ((rc = check_grouped_ws(P, N, K, E, ws, ws_bytes))) return rc;
-  const GroupedArgs a{{offsets, slot_of, E, P, (uint32_t)n_slots}, in, w, N, K, out, (flags & FT_OUT_BF16) != 0, ws};
+  const GroupedArgs a{{offsets, slot_of, E, P, (uint32_t)n_slots}, in, w, N, K, out, (flags & FT_OUT_BF16) != 0};
   const hipError_t e = launch_grouped(kind, a, stream);
   REQUIRE(e != hipErrorNotSupported, FT_E_UNSUPPORTED, "product too large (%d rows, N=%d, K=%d, E=%d)", P, N, K, E);
   return hip_status(e, what);
@@ -69,27 +60,26 @@ size_t lora_ws(int T, int E, int r, int N, int K) { return (size_t)lora_splits(T
 
 extern "C" {
 
-size_t ft_moe_grouped_matmul_workspace(int P, int N, int K, int E) {
-  if (P < 0 || P > (1 << 30) || N <= 0 || N > kMaxCols || K <= 0 || K > kMaxCols || E < 1 || E > 1024) return 0;
-  return grouped_workspace(P, N, K, E);
+size_t ft_moe_grouped_matmul_wgrad_workspace(int N, int K, int E) {
+  return N <= 0 || N > kMaxCols || K <= 0 || K > kMaxCols || E < 1 || E > 1024 ? 0 : wgrad_workspace(N, K, E);
 }
 
 int ft_moe_grouped_matmul(const uint16_t* a, int P, const uint16_t* w, int n_slots, int N, int K, const int32_t* offsets,
-                          const int32_t* slot_of_expert, int E, void* out, void* ws, size_t ws_bytes, int flags, hipStream_t stream) {
+                          const int32_t* slot_of_expert, int E, void* out, int flags, hipStream_t stream) {
   try {
-    return run_grouped(0, "ft_moe_grouped_matmul launch", "a", "out", a, P, w, n_slots, N, K, offsets, slot_of_expert, E, out, ws,
-                       ws_bytes, flags, stream);
+    return run_grouped(0, "ft_moe_grouped_matmul launch", "a", "out", a, P, w, n_slots, N, K, offsets, slot_of_expert, E, out, flags,
+                       stream);
   } catch (...) {
     return fail(FT_E_INTERNAL, "ft_moe_grouped_matmul: unexpected exception");
   }
 }
 
 int ft_moe_grouped_matmul_grad(const uint16_t* dout, int P, const uint16_t* w, int n_slots, int N, int K,
-                               const int32_t* offsets, const int32_t* slot_of_expert, int E, void* da, void* ws,
-                               size_t ws_bytes, int flags, hipStream_t stream) {
+                               const int32_t* offsets, const int32_t* slot_of_expert, int E, void* da, int flags,
+                               hipStream_t stream) {
   try {
     return run_grouped(1, "ft_moe_grouped_matmul_grad launch", "dout", "da", dout, P, w, n_slots, N, K, offsets, slot_of_expert, E, da,
-                       ws, ws_bytes, flags, stream);
+                       flags, stream);
   } catch (...) {
     return fail(FT_E_INTERNAL, "ft_moe_grouped_matmul_grad: unexpected exception");
   }
@@ -113,7 +103,9 @@ int ft_moe_grouped_matmul_wgrad(const uint16_t* dout, const uint16_t* a, int P, 
     CHECK_PTR(offsets, "offsets");
     if (slot_of_expert) CHECK_PTR(slot_of_expert, "slot_of_expert");
     CHECK_PTR(dw, "dw");
-    if ((rc = check_grouped_ws(P, N, K, E, ws, ws_bytes))) return rc;
+    const size_t need = wgrad_workspace(N, K, E);
+    if (need) CHECK_PTR(ws, "ws");
+    REQUIRE(ws_bytes >= need, FT_E_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
     const WgradArgs args{{offsets, slot_of_expert, E, P, n ? (uint32_t)n : 0x80000000u}, dout, a, N, K, dw, bf16, add, ws};
     const hipError_t e = launch_wgrad(args, stream);
     REQUIRE(e != hipErrorNotSupported, FT_E_UNSUPPORTED, "gradient too large (N=%d, K=%d, E=%d)", N, K, E);

@@ -24,8 +24,8 @@ __device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, in
 }
 
 // A tile of up to BM rows takes the least of these heights that holds its rows.
-template <int BM, bool GRAD, bool BF16, class Next>
-__device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds, Next next) {
+template <int BM, bool GRAD, bool BF16>
+__device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
   using C = Bf16Cfg<BM, 256, 2, 4, BM <= 128 ? 3 : 2>;
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -33,66 +33,55 @@ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int
   f32x4 acc[C::MF][C::NF];
   const Operand ro{a.a + (size_t)row0 * red, red, rows, nullptr, 0};
   const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0), nullptr, 0};
-  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, red, lds, acc);
-  next();
+  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, red, lds, acc, GRAD ? 0 : slot * 7);
   uint8_t* out = (uint8_t*)a.out + (size_t)row0 * cols * (BF16 ? 2 : 4);
   store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, lane);
 }
 
-constexpr int kTileLds = 3 * (128 + 256) * 128;
+// LDS of the tiles: 128 rows have three stages where the table of experts leaves room for them (7 % faster there: 128 experts of
+// 1536 x 2048 with 128 rows each, 188 -> 177 us).
+constexpr int kThreeStages = 1000;  // experts, at most
+__host__ __device__ constexpr int tile_lds(int E) { return E <= kThreeStages ? 3 * (128 + 256) * 128 : 2 * (256 + 256) * 128; }
+static_assert(tile_lds(kThreeStages) + group_lds_bytes(kThreeStages) <= 160 * 1024 && tile_lds(1024) + group_lds_bytes(1024) <= 160 * 1024, "LDS");
 
 // Tile `local` of `rows` rows: bands of 4 row tiles, column tiles within a band in turn.
-template <bool GRAD, bool BF16, class Next>
-__device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int row0, int cnt, int local, uint8_t* lds, Next next) {
+template <bool GRAD, bool BF16>
+__device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int row0, int cnt, int local, uint8_t* lds) {
   constexpr int BAND = 4;
   const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
   const int band = local / (BAND * ntn), h = min(BAND, (cnt + 255) / 256 - band * BAND), in = local - band * BAND * ntn;
   const int m0 = (band * BAND + in % h) * 256, n0 = in / h * 256, rows = min(256, cnt - m0);
   if (rows > 192)
-    grouped_tile<256, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
-  else if (rows > 128)
-    grouped_tile<192, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
+    grouped_tile<256, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+  else if (rows > 128 || (rows > 64 && a.g.E > kThreeStages))
+    grouped_tile<192, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
   else if (rows > 64)
-    grouped_tile<128, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
+    grouped_tile<128, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
   else
-    grouped_tile<64, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds, next);
+    grouped_tile<64, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
 }
 
-// Up to two tiles a block: fixed shares.  Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of
-// the tile list, so that tiles that run together share rows and matrices through its L2.
+// Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the tile list, so that tiles that run
+// together share rows and matrices through its L2.  (Queues with the tallest tiles first, as the matrix gradient has them,
+// were 5 % slower: one after the other, tiles bound by the matrix cores and tiles bound by memory do not fill each
+// other's gaps, and the list takes a launch of its own.)
 template <bool GRAD, bool BF16>
 __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
   const int E2 = a.g.E + 2;
-  int* li = (int*)(lds + kTileLds);
+  int* li = (int*)(lds + tile_lds(a.g.E));
   GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
   list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + 255) / 256 * ntn; });
   const int nitems = gl.item0[gl.n];
-  const int per = gridDim.x / 8, lb = (blockIdx.x % 8) * per + blockIdx.x / 8;  // gridDim.x % 8 == 0
-  for (int it = lb; it < nitems; it += gridDim.x) {
+  const int per = gridDim.x / 8, x = blockIdx.x % 8, j = blockIdx.x / 8;  // gridDim.x % 8 == 0
+  // (Rounds are turned against each other: heights repeat along the list, and a block must not meet the same one always.)
+  for (int round = 0, it; (it = round * (int)gridDim.x + x * per + (j + 7 * round) % per) < nitems || round * (int)gridDim.x < nitems; ++round) {
+    if (it >= nitems) continue;
     const int gi = find_group(gl.item0, gl.n, it);
     grouped_item<GRAD, BF16>(a, __builtin_amdgcn_readfirstlane(gl.slot[gi]), __builtin_amdgcn_readfirstlane(gl.row0[gi]),
-                             __builtin_amdgcn_readfirstlane(gl.cnt[gi]), __builtin_amdgcn_readfirstlane(it - gl.item0[gi]), lds, [] {});
+                             __builtin_amdgcn_readfirstlane(gl.cnt[gi]), __builtin_amdgcn_readfirstlane(it - gl.item0[gi]), lds);
   }
-}
-
-// More: planned, by classes of experts with more than 192, 128, 64 rows, and the rest.  (A lower last tile stays beside the
-// whole ones of its expert, whose matrix it shares.)
-__global__ __launch_bounds__(kPlanThreads) void grouped_plan_kernel(RowGroups g, int ntn, Plan* plan) {
-  make_plan(g, plan, [&](int slot, int, int row0, int cnt, int (&cls)[2], int (&tiles)[2], PlanPart (&part)[2]) {
-    if (cnt == 0) return;
-    cls[0] = 0, tiles[0] = (cnt + 255) / 256 * ntn;
-    part[0] = PlanPart{slot, row0, cnt, 0};
-  });
-}
-
-template <bool GRAD, bool BF16>
-__global__ __launch_bounds__(512, 2) void grouped_planned_kernel(GroupedArgs a, Plan* plan) {
-  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  run_plan(plan, (int*)(lds + kTileLds), [&](const PlanPart& part, int local, auto next) {
-    grouped_item<GRAD, BF16>(a, part.slot, part.row0, part.rows, local, lds, next);
-  });
 }
 
 // Few rows an expert: BM rows by 64 columns a block, whose four waves have a share of the reduction each, with stages of
@@ -186,21 +175,11 @@ __global__ __launch_bounds__(C::NT, 2) void wgrad_tile_kernel(WgradArgs a) {
   wgrad_item<C, BF16, ADD>(a, e, __builtin_amdgcn_readfirstlane(row0), __builtin_amdgcn_readfirstlane(cnt), blockIdx.x % tiles, lds, [] {});
 }
 
-// Classes of experts by their rows: above 2048, 1024, ... 64, and the rest.
-__global__ __launch_bounds__(kPlanThreads) void wgrad_plan_kernel(RowGroups g, int ntiles, Plan* plan) {
-  make_plan(g, plan, [&](int, int e, int row0, int cnt, int (&cls)[2], int (&tiles)[2], PlanPart (&part)[2]) {
-    cls[0] = 0;
-    for (int c = 2048; c >= 64 && cnt <= c; c >>= 1) ++cls[0];
-    tiles[0] = ntiles;
-    part[0] = PlanPart{e, row0, cnt, 0};
-  });
-}
-
 template <class C, bool BF16, bool ADD>
-__global__ __launch_bounds__(C::NT, 2) void wgrad_planned_kernel(WgradArgs a, Plan* plan) {
+__global__ __launch_bounds__(C::NT, 2) void wgrad_planned_kernel(WgradArgs a, int tiles, Plan* plan) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  run_plan(plan, (int*)(lds + C::LDS), [&](const PlanPart& part, int local, auto next) {
-    wgrad_item<C, BF16, ADD>(a, part.slot, part.row0, part.rows, local, lds, next);
+  run_plan(plan, tiles, [&](const PlanPart& part, int t, auto next) {
+    wgrad_item<C, BF16, ADD>(a, part.expert, part.row0, part.rows, t, lds, next);
   });
 }
 
@@ -218,28 +197,14 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tiles of a product, at most: more than two a compute unit are planned.
-long long most_tiles(const RowGroups& g, int cols) { return ((g.P + 255) / 256 + (long long)std::min(g.E, g.P)) * ((cols + 255) / 256); }
-long long most_tiles_w(const RowGroups& g, int N, int K) { return (long long)((N + 255) / 256) * ((K + 255) / 256) * g.E; }
-constexpr int kPlanFrom = 512;
-
 template <bool GRAD, bool BF16>
 hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
-  static LaunchCache cache, planned;
+  static LaunchCache cache;
   LaunchFacts f;
   const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
-  const long long ntn = (cols + 255) / 256, tiles = most_tiles(a.g, cols);
+  const long long ntn = (cols + 255) / 256, tiles = std::min<long long>(P, (P + 255) / 256 + E) * ntn;
   if ((P / 256 + 2LL) * (E / 2 + 1) * ntn >= 1LL << 31) return hipErrorNotSupported;
-  if (tiles > kPlanFrom) {
-    const size_t lds = kTileLds + (size_t)2 * E * sizeof(int);
-    hipError_t e = planned.get((const void*)grouped_planned_kernel<GRAD, BF16>, 512, lds, &f);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grouped_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a.g, (int)ntn, (Plan*)a.ws);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((grouped_planned_kernel<GRAD, BF16>), dim3(f.per_cu * f.cus), dim3(512), lds, s, a, (Plan*)a.ws);
-    return hipGetLastError();
-  }
-  const size_t lds = kTileLds + group_lds_bytes(E);
+  const size_t lds = tile_lds(E) + group_lds_bytes(E);
   hipError_t e = cache.get((const void*)grouped_tile_kernel<GRAD, BF16>, 512, lds, &f);
   if (e != hipSuccess) return e;
   const long long upper = (tiles + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
@@ -247,19 +212,23 @@ hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Matrix gradients of more tiles than two a compute unit are planned.
+long long wgrad_tiles(int N, int K, int E) { return (long long)((N + 255) / 256) * ((K + 255) / 256) * E; }
+constexpr int kPlanFrom = 512;
+
 template <class C, bool BF16, bool ADD>
 hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
   static LaunchCache cache, planned;
   LaunchFacts f;
-  const long long blocks = most_tiles_w(a.g, a.N, a.K);
+  const long long blocks = wgrad_tiles(a.N, a.K, a.g.E);
   if (blocks >= 1LL << 31) return hipErrorNotSupported;
   if (blocks > kPlanFrom) {
-    const size_t lds = C::LDS + (size_t)2 * a.g.E * sizeof(int);
-    hipError_t e = planned.get((const void*)wgrad_planned_kernel<C, BF16, ADD>, C::NT, lds, &f);
+    const int tiles = (int)(blocks / a.g.E);
+    hipError_t e = planned.get((const void*)wgrad_planned_kernel<C, BF16, ADD>, C::NT, C::LDS, &f);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(wgrad_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a.g, (int)(blocks / a.g.E), (Plan*)a.ws);
+    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a.g, tiles, (Plan*)a.ws);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((wgrad_planned_kernel<C, BF16, ADD>), dim3(f.per_cu * f.cus), dim3(C::NT), lds, s, a, (Plan*)a.ws);
+    hipLaunchKernelGGL((wgrad_planned_kernel<C, BF16, ADD>), dim3(f.per_cu * f.cus), dim3(C::NT), C::LDS, s, a, tiles, (Plan*)a.ws);
     return hipGetLastError();
   }
   hipError_t e = cache.get((const void*)wgrad_tile_kernel<C, BF16, ADD>, C::NT, C::LDS, &f);
@@ -306,10 +275,7 @@ hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t grouped_workspace(int P, int N, int K, int E) {
-  const RowGroups g{nullptr, nullptr, E, P, 0};
-  return std::max({most_tiles(g, N), most_tiles(g, K), most_tiles_w(g, N, K)}) > kPlanFrom ? plan_bytes(E) : 0;
-}
+size_t wgrad_workspace(int N, int K, int E) { return wgrad_tiles(N, K, E) > kPlanFrom ? plan_bytes(E) : 0; }
 
 hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s) {
   if (kind == 0) return a.out_bf16 ? launch_grouped_as<false, true>(a, s) : launch_grouped_as<false, false>(a, s);

@@ -104,6 +104,13 @@ struct Loader {
     else
       p += step;
   }
+  __device__ __forceinline__ void skip(int stages) {
+    if constexpr (MODE == GATHERED)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) at[q] += stages * 128;
+    else
+      p += (long long)stages * (long long)step;
+  }
   // What a short stage holds past its end becomes 0.
   static __device__ __forceinline__ void clear(uint8_t* part, int tid, int left) {
 #pragma unroll
@@ -150,7 +157,8 @@ struct Reader {
 // half's fragments are read from LDS into other registers.  The turn to the next stage comes before the second half, whose
 // fragments have been read by then: from there on the buffer of this stage takes the loads of the stage NS ahead.
 template <class C, int RMODE, int CMODE>
-__device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, int red, uint8_t* lds, f32x4 (&acc)[C::MF][C::NF]) {
+__device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, int red, uint8_t* lds, f32x4 (&acc)[C::MF][C::NF],
+                                          int turn = 0) {
   constexpr int MF = C::MF, NF = C::NF, NS = C::NS, U = C::QM + C::QN;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % C::GW, tid = wv * 64 + lane;
   const int wm = wv / C::WN, wn = wv % C::WN;
@@ -169,7 +177,13 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
   rr.open(wm * 16 * MF, lane);
   rc.open(wn * 16 * NF, lane);
   const uint32_t lds0 = lds_addr(lds) + wv * 1024;
-  int fill = 0;
+  int fill = 0, wrap = 0;  // stages loaded; the one after which the first follows (0: none)
+  if (turn > 0 && left == 0) {
+    const int first = turn % nb;
+    wrap = first ? nb - first : 0;
+    lr.skip(first);
+    lc.skip(first);
+  }
   uint32_t fill_lds = lds0;
   auto open = [&] {
     if (fill == nb - 1 && left && fill > 0) {
@@ -188,6 +202,7 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
     ++fill;
     lr.advance();
     lc.advance();
+    if (fill == wrap) lr.skip(-nb), lc.skip(-nb);
     fill_lds = fill_lds + C::STAGE >= lds0 + C::RING ? lds0 : fill_lds + C::STAGE;
   };
   auto meet = [] {
@@ -208,22 +223,19 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
   using Half0 = std::integral_constant<int, 0>;
   using Half1 = std::integral_constant<int, 1>;
   // Slots between a half's MM matrix instructions: fragment reads in the first three quarters, loads in the first half.
-  constexpr int MM = MF * NF;
+  constexpr int MM = MF * NF, RD = MF + NF, RS = MM - MM / 4, US = MM / 2 > 0 ? MM / 2 : 1;
   auto half = [&](bf16x8(&now)[NF + MF], bf16x8(&next)[NF + MF], const uint8_t* from, auto h, auto loads) {
-#pragma unroll
-    for (int i = 0; i < MM; ++i) {
-      const int m = i / NF, f = i % NF;
+    unrolled<0, MM>([&](auto slot) {
+      constexpr int i = decltype(slot)::value, m = i / NF, f = i % NF;
       acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now[f], now[NF + m], acc[m][f], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int n = 0; n < NF + MF; ++n)
-        if (n * (MM - MM / 4) / (NF + MF) == i) next[n] = frag(from, h, n);
-      if constexpr (decltype(loads)::value)
-        unrolled<0, U>([&](auto u) {
-          if (decltype(u)::value * (MM / 2) / U == i) issue_unit(u);
-        });
+      // reads n with n RS / RD == i, loads u with u US / U == i
+      unrolled<(i * RD + RS - 1) / RS, (i + 1) * RD <= RS * RD ? ((i + 1) * RD + RS - 1) / RS : (i * RD + RS - 1) / RS>([&](auto n) {
+        if constexpr (decltype(n)::value < RD) next[decltype(n)::value] = frag(from, h, decltype(n)::value);
+      });
+      if constexpr (decltype(loads)::value && i < US) unrolled<(i * U + US - 1) / US, ((i + 1) * U + US - 1) / US>(issue_unit);
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
   };
   auto after = [&](uint8_t* s) { return s + C::STAGE >= lds + C::RING ? lds : s + C::STAGE; };
 

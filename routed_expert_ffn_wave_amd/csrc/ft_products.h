@@ -20,10 +20,7 @@ struct GroupedArgs {
   int N, K;
   void* out;
   bool out_bf16;
-  void* ws;
 };
-// Bytes of ws that each of the products of these sizes is content with (0: none needs any).
-size_t grouped_workspace(int P, int N, int K, int E);
 hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s);
 
 // dw[E][N][K] = dout[P][N]^T a[P][K] by expert, or += with add (fp32)
@@ -35,6 +32,7 @@ struct WgradArgs {
   bool out_bf16, add;
   void* ws;
 };
+size_t wgrad_workspace(int N, int K, int E);  // bytes of ws (0: none is needed)
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s);
 
 // h[rows][I] = SiLU(g) u of gu[rows][2 I]; with dh: out[rows][2 I] = its gradient

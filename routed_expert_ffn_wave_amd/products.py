@@ -18,9 +18,9 @@ FT_ADD_TO_OUT = 0x40
 
 _P, _i, _z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _SIG = {
-    "ft_moe_grouped_matmul_workspace": [_i, _i, _i, _i],
-    "ft_moe_grouped_matmul": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _P, _z, _i, _P],
-    "ft_moe_grouped_matmul_grad": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _P, _z, _i, _P],
+    "ft_moe_grouped_matmul_wgrad_workspace": [_i, _i, _i],
+    "ft_moe_grouped_matmul": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _i, _P],
+    "ft_moe_grouped_matmul_grad": [_P, _i, _P, _i, _i, _i, _P, _P, _i, _P, _i, _P],
     "ft_moe_grouped_matmul_wgrad": [_P, _P, _i, _i, _i, _P, _P, _i, _P, _P, _z, _i, _P],
     "ft_moe_swiglu": [_P, _i, _i, _P, _P],
     "ft_moe_swiglu_grad": [_P, _P, _i, _i, _P, _P],
@@ -30,7 +30,7 @@ _SIG = {
 for _name, _args in _SIG.items():
     _f = getattr(lib, _name)
     _f.argtypes, _f.restype = _args, _i
-lib.ft_moe_lora_workspace.restype = lib.ft_moe_grouped_matmul_workspace.restype = _z
+lib.ft_moe_lora_workspace.restype = lib.ft_moe_grouped_matmul_wgrad_workspace.restype = _z
 
 EXPORTED_PRODUCTS = tuple(_SIG)
 
@@ -62,26 +62,24 @@ def _workspace(ws, need, dev: int, stream, *args):
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def ft_moe_grouped_matmul_workspace(P: int, N: int, K: int, E: int) -> int:
-    return lib.ft_moe_grouped_matmul_workspace(P, N, K, E)
+def ft_moe_grouped_matmul_wgrad_workspace(N: int, K: int, E: int) -> int:
+    return lib.ft_moe_grouped_matmul_wgrad_workspace(N, K, E)
 
 
-def ft_moe_grouped_matmul(a, w, offsets, slot_of_expert=None, out=None, out_dtype=torch.bfloat16, stream=None, ws=None):
+def ft_moe_grouped_matmul(a, w, offsets, slot_of_expert=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """bf16 rows a [P][K] in expert order, each expert's rows times its matrix of w [n_slots][N][K] transposed: [P][N]
     in bf16, or in fp32 with out_dtype=torch.float32 (or an fp32 `out`).  Rows of experts without a slot are left as they
-    were (with out=None: unset).  slot_of_expert None: expert e has matrix e.  `ws`, here and in the two calls below:
-    ft_moe_grouped_matmul_workspace(P, N, K, E) bytes (made for the call when not given)."""
+    were (with out=None: unset).  slot_of_expert None: expert e has matrix e."""
     dev, (P, K) = _first(a, "a", 2, (_BF,), stream)
     n_slots, N, _ = _matrices(w, "w")
     pw = _take(w, "w", (_BF,), (n_slots, N, K), dev)
     pf, pt, E = _groups(offsets, slot_of_expert, "slot_of_expert", dev)
     out, po, flags = _product_out(out, out_dtype, (P, N), dev, stream)
-    ws, pws, nw = _workspace(ws, lib.ft_moe_grouped_matmul_workspace, dev, stream, P, N, K, E)
-    _run(lib.ft_moe_grouped_matmul, dev, stream, a.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, pws, nw, flags)
+    _run(lib.ft_moe_grouped_matmul, dev, stream, a.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, flags)
     return out
 
 
-def ft_moe_grouped_matmul_grad(dout, w, offsets, slot_of_expert=None, da=None, out_dtype=torch.bfloat16, stream=None, ws=None):
+def ft_moe_grouped_matmul_grad(dout, w, offsets, slot_of_expert=None, da=None, out_dtype=torch.bfloat16, stream=None):
     """Gradient of ft_moe_grouped_matmul's rows: dout [P][N] in expert order times the experts' matrices of
     w [n_slots][N][K]: [P][K] in bf16 or fp32."""
     dev, (P, N) = _first(dout, "dout", 2, (_BF,), stream)
@@ -89,8 +87,7 @@ def ft_moe_grouped_matmul_grad(dout, w, offsets, slot_of_expert=None, da=None, o
     pw = _take(w, "w", (_BF,), (n_slots, N, K), dev)
     pf, pt, E = _groups(offsets, slot_of_expert, "slot_of_expert", dev)
     da, po, flags = _product_out(da, out_dtype, (P, K), dev, stream)
-    ws, pws, nw = _workspace(ws, lib.ft_moe_grouped_matmul_workspace, dev, stream, P, N, K, E)
-    _run(lib.ft_moe_grouped_matmul_grad, dev, stream, dout.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, pws, nw, flags)
+    _run(lib.ft_moe_grouped_matmul_grad, dev, stream, dout.data_ptr(), P, pw, n_slots, N, K, pf, pt, E, po, flags)
     return da
 
 
@@ -98,7 +95,8 @@ def ft_moe_grouped_matmul_wgrad(dout, a, offsets, slot_of_expert=None, dw=None, 
                                 n_slots=None, ws=None):
     """Gradient of ft_moe_grouped_matmul's matrices, by expert: dw[e] = dout_e^T a_e [E][N][K] of the rows dout [P][N] and
     a [P][K] of every expert, in fp32 (add: dw += it) or bf16; zeros for an expert without rows.  Experts that
-    slot_of_expert gives no slot (in [0, n_slots), where n_slots is given) are left as they were."""
+    slot_of_expert gives no slot (in [0, n_slots), where n_slots is given) are left as they were.  `ws`:
+    ft_moe_grouped_matmul_wgrad_workspace(N, K, E) bytes (made for the call when not given)."""
     dev, (P, N) = _first(dout, "dout", 2, (_BF,), stream)
     K = a.shape[1] if isinstance(a, torch.Tensor) and a.dim() == 2 else 0
     pa = _take(a, "a", (_BF,), (P, K), dev)
@@ -109,7 +107,7 @@ def ft_moe_grouped_matmul_wgrad(dout, a, offsets, slot_of_expert=None, dw=None, 
         _refuse("n_slots is given without slot_of_expert")
     fl = (0 if n_slots is None else FT_N_SLOTS(n_slots)) | (FT_ADD_TO_OUT if add else 0)
     dw, po, flags = _product_out(dw, out_dtype, (E, N, K), dev, stream)
-    ws, pws, nw = _workspace(ws, lib.ft_moe_grouped_matmul_workspace, dev, stream, P, N, K, E)
+    ws, pws, nw = _workspace(ws, lib.ft_moe_grouped_matmul_wgrad_workspace, dev, stream, N, K, E)
     _run(lib.ft_moe_grouped_matmul_wgrad, dev, stream, dout.data_ptr(), pa, P, N, K, pf, pt, E, po, pws, nw, flags | fl)
     return dw
 

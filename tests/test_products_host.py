@@ -32,8 +32,8 @@ def test_every_declared_symbol_is_exported():
     assert int(re.search(r"#define FT_ADD_TO_OUT (0x\w+)", open(HEADER).read()).group(1), 16) == ft.FT_ADD_TO_OUT
 
 
-def grouped(name, a=A, P=4, w=A, n=8, N=64, K=64, off=A, slot=None, E=8, out=B, ws=B, nb=1 << 20, f=0):
-    return getattr(L, "ft_moe_grouped_matmul" + name)(a, P, w, n, N, K, off, slot, E, out, ws, nb, f, None)
+def grouped(name, a=A, P=4, w=A, n=8, N=64, K=64, off=A, slot=None, E=8, out=B, f=0):
+    return getattr(L, "ft_moe_grouped_matmul" + name)(a, P, w, n, N, K, off, slot, E, out, f, None)
 
 
 def wgrad(d=A, a=A, P=4, N=64, K=64, off=A, slot=None, E=8, dw=B, ws=B, nb=1 << 20, f=0):
@@ -72,18 +72,17 @@ def test_wgrad_refusals():
     err(wgrad(N=1 << 20, K=1 << 20, E=1024), ft.FT_E_UNSUPPORTED, "gradient too large")
 
 
-def test_grouped_workspace():
-    need = ft.ft_moe_grouped_matmul_workspace
-    assert need(8, 1536, 2048, 8) == 0
-    big = need(32768, 1536, 2048, 128)
-    assert 128 * 2 * 16 <= big <= 1 << 16
-    for bad in ((-1, 64, 64, 8), (1 << 30, 64, 64, 0), (4096, 0, 64, 8), (4096, 64, 0, 8), (4096, 64, 64, 1025)):
+def test_wgrad_workspace():
+    need = ft.ft_moe_grouped_matmul_wgrad_workspace
+    assert need(1536, 2048, 8) == 0
+    big = need(1536, 2048, 128)
+    assert 128 * 16 <= big <= 1 << 16
+    for bad in ((0, 2048, 128), (1536, 0, 128), (1536, 2048, 1025), (1536, 2048, 0), ((1 << 20) + 8, 2048, 128)):
         assert need(*bad) == 0
-    for call in (lambda **kw: grouped("", P=32768, N=1536, K=2048, E=128, n=128, **kw), lambda **kw: grouped("_grad", P=32768, N=1536, K=2048, E=128, n=128, **kw),
-                 lambda **kw: wgrad(P=32768, N=1536, K=2048, E=128, **kw)):
-        err(call(ws=None), ft.FT_E_INVAL, "ws is null")
-        err(call(ws=MIS), ft.FT_E_INVAL, "ws is not 16")
-        err(call(nb=big - 1), ft.FT_E_WORKSPACE, "workspace of")
+    call = lambda **kw: wgrad(P=32768, N=1536, K=2048, E=128, **kw)  # noqa: E731
+    err(call(ws=None), ft.FT_E_INVAL, "ws is null")
+    err(call(ws=MIS), ft.FT_E_INVAL, "ws is not 16")
+    err(call(nb=big - 1), ft.FT_E_WORKSPACE, "workspace of")
 
 
 def test_swiglu_refusals():
