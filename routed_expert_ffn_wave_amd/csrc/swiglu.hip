@@ -18,11 +18,10 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 template <bool GRAD>
-__global__ __launch_bounds__(ST) void swiglu_kernel(const uint16_t* __restrict__ gu, const uint16_t* __restrict__ dh, long long chunks,
-                                                    int per_row, uint16_t* __restrict__ out) {
-  const long long i = (long long)blockIdx.x * ST + threadIdx.x;  // chunk of 8 columns
+__global__ __launch_bounds__(ST) void swiglu_kernel(const uint16_t* gu, const uint16_t* dh, uint32_t chunks, uint32_t per_row, uint16_t* out) {
+  const uint32_t i = blockIdx.x * ST + threadIdx.x;  // chunk of 8 columns
   if (i >= chunks) return;
-  const long long row = i / per_row, c = i - row * per_row;
+  const uint32_t row = i / per_row, c = i - row * per_row;
   const size_t at = ((size_t)row * 2 * per_row + c) * 8, up = at + (size_t)per_row * 8;
   const u32x4 g = *(const u32x4*)(gu + at), u = *(const u32x4*)(gu + up);
   if constexpr (!GRAD) {
@@ -32,7 +31,7 @@ __global__ __launch_bounds__(ST) void swiglu_kernel(const uint16_t* __restrict__
       const float g0 = lo(g[q]), g1 = hi(g[q]);
       h[q] = pack(g0 * sigmoid(g0) * lo(u[q]), g1 * sigmoid(g1) * hi(u[q]));
     }
-    *(u32x4*)(out + (size_t)i * 8) = h;
+    __builtin_nontemporal_store(h, (u32x4*)(out + (size_t)i * 8));
   } else {
     const u32x4 d = *(const u32x4*)(dh + (size_t)i * 8);
     u32x4 dg, du;
@@ -49,8 +48,8 @@ __global__ __launch_bounds__(ST) void swiglu_kernel(const uint16_t* __restrict__
       dg[q] = pack(a0, a1);
       du[q] = pack(b0, b1);
     }
-    *(u32x4*)(out + at) = dg;
-    *(u32x4*)(out + up) = du;
+    __builtin_nontemporal_store(dg, (u32x4*)(out + at));
+    __builtin_nontemporal_store(du, (u32x4*)(out + up));
   }
 }
 
@@ -60,9 +59,9 @@ hipError_t launch_swiglu(const uint16_t* gu, const uint16_t* dh, long long rows,
   const long long chunks = rows * (I / 8);
   const dim3 grid((uint32_t)((chunks + ST - 1) / ST));
   if (dh)
-    hipLaunchKernelGGL(swiglu_kernel<true>, grid, dim3(ST), 0, s, gu, dh, chunks, I / 8, out);
+    hipLaunchKernelGGL(swiglu_kernel<true>, grid, dim3(ST), 0, s, gu, dh, (uint32_t)chunks, (uint32_t)(I / 8), out);
   else
-    hipLaunchKernelGGL(swiglu_kernel<false>, grid, dim3(ST), 0, s, gu, dh, chunks, I / 8, out);
+    hipLaunchKernelGGL(swiglu_kernel<false>, grid, dim3(ST), 0, s, gu, dh, (uint32_t)chunks, (uint32_t)(I / 8), out);
   return hipGetLastError();
 }
 
