@@ -457,6 +457,6 @@ class MoELayer:
 from .rows import (EXPORTED_ROWS, FT_ROWS_F32, Fp8MoELayer, ft_moe_combine_grad, ft_moe_dispatch, ft_moe_dispatch_fp8,  # noqa: E402,F401
                    ft_moe_dispatch_grad, ft_moe_fp8_grouped_matmul, ft_moe_fp8_matmul, ft_moe_fp8_scale_cols,
                    ft_moe_quant_fp8, ft_moe_swiglu_fp8)
-from .products import (EXPORTED_PRODUCTS, FT_ADD_TO_OUT, ft_moe_grouped_matmul,  # noqa: E402,F401
+from .products import (EXPORTED_PRODUCTS, FT_ADD_TO_OUT, Bf16MoELayer, ft_moe_grouped_matmul,  # noqa: E402,F401
                        ft_moe_grouped_matmul_grad, ft_moe_grouped_matmul_wgrad, ft_moe_grouped_matmul_wgrad_workspace, ft_moe_lora, ft_moe_lora_workspace, ft_moe_swiglu,
                        ft_moe_swiglu_grad)

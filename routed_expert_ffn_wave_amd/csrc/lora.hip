@@ -167,7 +167,7 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
 
 // h[split][p][j] = sum over the split's k of x[gather[p]][k] A[j][k] for 64 positions p and BN columns j
 template <int BN>
-using ShrinkCfg = Bf16Cfg<64, BN, 2, 1, 3>;
+using ShrinkCfg = Bf16Cfg<64, BN, 2, 1, 4>;
 
 template <int BN>
 __global__ __launch_bounds__(128) void lora_shrink_kernel(LoraArgs a, int splits) {
@@ -202,9 +202,8 @@ using ExpandB = Loader<DIRECT, 256, 4>;
 constexpr int ER = 32, kHidden = ER * 128, kExpandLds = 2 * kHidden + 256 * 128;  // both terms, B
 
 template <bool BF16>
-__global__ __launch_bounds__(256, 4) void lora_expand_kernel(LoraArgs a, int splits, bool copy) {
+__global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int splits, bool copy) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  __shared__ int s_t[ER];
   GroupList gl;
   const int chunks = list_chunks<ER>(a.g, copy, gl, (int*)(smem + kExpandLds));
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ntn = (a.N + 255) / 256;
@@ -224,9 +223,25 @@ __global__ __launch_bounds__(256, 4) void lora_expand_kernel(LoraArgs a, int spl
     for (int m = 0; m < ER / 16; ++m)
 #pragma unroll
       for (int f = 0; f < 4; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
-    if (tid < ER) s_t[tid] = tid < c.rows ? a.gather[c.p0 + tid] : -1;
+    // this lane's pieces of 4 columns of out (each_piece): rows 16 m + 4 mid + j; base is on its way while the sums are formed
+    const int col = n0 + wv * 64 + 16 * (lane >> 4) + 4 * (lane & 3);
+    using Piece = std::conditional_t<BF16, u32x2, f32x4>;
+    int t[ER / 4];
+    Piece base[ER / 4];
+#pragma unroll
+    for (int i = 0; i < ER / 4; ++i) {
+      const int row = 16 * (i / 4) + 4 * ((lane >> 2) & 3) + i % 4;
+      t[i] = row < c.rows && col < a.N ? a.gather[c.p0 + row] : -1;
+    }
+    auto load_base = [&] {
+#pragma unroll
+      for (int i = 0; i < ER / 4; ++i) {
+        base[i] = Piece{};
+        if ((uint32_t)t[i] < (uint32_t)a.g.P) base[i] = *(const Piece*)((const uint8_t*)a.base + ((size_t)t[i] * a.N + col) * (BF16 ? 2 : 4));
+      }
+    };
     if (c.slot < 0) {
-      __syncthreads();
+      load_base();
     } else {
       for (int j0 = 0; j0 < a.r; j0 += 64) {
         const int red = min(64, a.r - j0);
@@ -234,6 +249,7 @@ __global__ __launch_bounds__(256, 4) void lora_expand_kernel(LoraArgs a, int spl
         ExpandB lb;
         lb.open(bo, tid, red);
         unrolled<0, ExpandB::Q>([&](auto q) { lb.template issue<decltype(q)::value, 2 * kHidden>(lds_addr(smem) + wv * 1024); });
+        if (j0 == 0) load_base();
         // pieces of 4 hidden values, ER / 16 a thread, splits four at a time so that their loads are under way together
         f32x4 v[ER / 16];
 #pragma unroll
@@ -292,22 +308,16 @@ __global__ __launch_bounds__(256, 4) void lora_expand_kernel(LoraArgs a, int spl
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // LDS is free for what comes next
       }
     }
-    each_piece<ER / 16, false>(acc, lane, [&](int, int row, int col, f32x4 v) {
-      const int t = s_t[row];
-      col += n0 + wv * 64;
-      if ((uint32_t)t >= (uint32_t)a.g.P || col >= a.N) return;
-      const size_t at = (size_t)t * a.N + col;
-      if constexpr (BF16) {
-        u32x2 o = *(const u32x2*)((const uint16_t*)a.base + at);
-        if (c.slot >= 0) o = pack_sum(o, v);
-        *(u32x2*)((uint16_t*)a.out + at) = o;
-      } else {
-        f32x4 o = *(const f32x4*)((const float*)a.base + at);
-        if (c.slot >= 0) o += v;
-        *(f32x4*)((float*)a.out + at) = o;
+    each_piece<ER / 16, false>(acc, lane, [&](int i, int, int, f32x4 v) {
+      Piece o = base[i];
+      if (c.slot >= 0) {
+        if constexpr (BF16)
+          o = pack_sum(o, v);
+        else
+          o += v;
       }
+      if ((uint32_t)t[i] < (uint32_t)a.g.P) *(Piece*)((uint8_t*)a.out + ((size_t)t[i] * a.N + col) * (BF16 ? 2 : 4)) = o;
     });
-    __syncthreads();  // s_t
   }
 }
 
@@ -361,11 +371,12 @@ bool lora_small(int T, int E, int r, int N, int K) {
 
 }  // namespace
 
-// Shares of K: about one block a compute unit, at least 512 values each (4096 rows, 7168 -> 4096, r = 64, us, 1 / 2 / 4 / 8 /
-// 16 shares: 64.5 / 48.7 / 44.9 / 48.0 / 59.0).  0: no hidden rows in memory.
+// Shares of K: 1.5 blocks a compute unit, at least 512 values each (both kernels, us, 2 / 4 / 6 / 8 shares: 4096 rows of 5 adapters,
+// 7168 -> 4096, r = 64: 51.0 / 54.5 / 51.1 / 54.4; 1024 rows of 16, 4096 -> 4096, r = 16: 19.6 / 17.3 / 17.1 / 17.0; 131 rows of 40,
+// 7168 -> 2048, r = 8: 20.5 / 16.3 / 15.4 / 14.6).  0: no hidden rows in memory.
 int lora_splits(int T, int E, int r, int N, int K) {
   if (lora_small(T, E, r, N, K)) return 0;
-  const long long c = chunks(T, E, 64), s = std::min<long long>({(256 + c / 2) / c, K / 512, 16});
+  const long long c = chunks(T, E, 64), s = std::min<long long>({(384 + c / 2) / c, K / 512, 16});
   return s < 1 ? 1 : (int)s;
 }
 

@@ -12,7 +12,8 @@ import ctypes
 import torch
 
 from . import FT_N_SLOTS, FT_OUT_BF16, lib
-from .rows import _BF, _F32, _FLOATS, _I32, _first, _new, _product_out, _refuse, _run, _take
+from .rows import (_BF, _F32, _FLOATS, _I32, _first, _new, _product_out, _raw_stream, _refuse, _run, _take, ft_moe_combine_grad,
+                   ft_moe_dispatch, ft_moe_dispatch_grad)
 
 FT_ADD_TO_OUT = 0x40
 
@@ -160,3 +161,112 @@ def ft_moe_lora(base, x, a, b, offsets, gather, slot_of_adapter=None, scale=None
     _run(lib.ft_moe_lora, dev, stream, base.data_ptr(), px, T, pa, pb, ps, n_slots, r, N, K, pf, pg, pt, E, po, pw, nw,
          FT_OUT_BF16 if base.dtype is _BF else 0)
     return out
+
+
+# ------------------------------------------------------------------------------------- one layer with its gradient
+
+class Bf16MoELayer:
+    """One MoE layer in bf16 with its gradient, for training steps: route, permute, token rows in expert order, gate/up
+    product, SwiGLU, down product, weighted combine; and back.  w13 bf16 [n_slots][2I][d] ([gate ; up] rows) and
+    w2 bf16 [n_slots][d][I] as they are stored; slot_of_expert int32 [E], -1 for experts that are not resident (left to
+    the residual mask; entries outside [0, n_slots) count as -1); None: expert e has matrix e.  Every buffer is allocated
+    here for a fixed (T, k): forward() and backward() allocate nothing and can be captured into a graph.  backward()
+    returns the gradients of x, of the logits and, by expert, of w13 and w2 (fp32; zeros for an expert without rows,
+    nothing for one without a slot); add=True adds the latter two to what the buffers hold.  It takes what the last
+    forward() left in the buffers, and x, which the caller keeps unchanged until then.  One step at a time; streams as
+    in Fp8MoELayer."""
+
+    def __init__(self, w13, w2, slot_of_expert=None, k: int = 1, T: int = 1, out_bf16: bool = False):
+        dev, (self.n_slots, I2, self.d) = _first(w13, "w13", 3, (_BF,))
+        self.I = I2 // 2
+        _take(w2, "w2", (_BF,), (self.n_slots, self.d, self.I), dev)
+        if slot_of_expert is None:
+            E = self.n_slots
+        else:
+            _first(slot_of_expert, "slot_of_expert", 1, (_I32,))
+            _take(slot_of_expert, "slot_of_expert", (_I32,), slot_of_expert.shape, dev)
+            E = slot_of_expert.shape[0]
+        if T < 0 or T * k > 1 << 30 or I2 % 16 or self.d % 8 or self.d * self.I == 0 or not 1 <= self.n_slots < 1 << 23 or E > 1024 or not 1 <= k <= min(E, 32):
+            _refuse(f"invalid layer shape T={T}, k={k}, E={E}, d={self.d}, w13 rows={I2}, slots={self.n_slots}")
+        if slot_of_expert is None:
+            slot_of_expert = torch.arange(E, dtype=torch.int32, device=f"cuda:{dev}")
+        self.dev, self.w13, self.w2, self.slot_of = dev, w13, w2, slot_of_expert
+        self.E, self.k, self.T, self.out_bf16 = E, k, T, out_bf16
+        new = lambda *shape, dtype: _new(shape, dtype, dev)  # noqa: E731
+        P, f32, bf, i32 = T * k, _F32, _BF, _I32
+        out = bf if out_bf16 else f32
+        self.ids, self.w, self.inv = new(T, k, dtype=i32), new(T, k, dtype=f32), new(max(P, 1), dtype=i32)
+        self.counts, self.offsets, self.gather = new(E, dtype=i32), new(E + 1, dtype=i32), new(max(P, 1), dtype=i32)
+        self.perm_ws = new(max(lib.ft_moe_permute_workspace(T, E, k), 16), dtype=torch.uint8)
+        self.xs, self.gu, self.h, self.y_sorted = new(P, self.d, dtype=bf), new(P, I2, dtype=bf), new(P, self.I, dtype=bf), new(P, self.d, dtype=bf)
+        self.out, self.mask = new(T, self.d, dtype=out), new(max(T, 1), dtype=i32)
+        self.dy, self.dh, self.dgu, self.dxs = new(P, self.d, dtype=bf), new(P, self.I, dtype=bf), new(P, I2, dtype=bf), new(P, self.d, dtype=bf)
+        self.dx = new(T, self.d, dtype=bf)
+        self.dw, self.dlogits = new(T, k, dtype=f32), new(T, E, dtype=f32)
+        self.dw13, self.dw2 = new(E, I2, self.d, dtype=f32), new(E, self.d, self.I, dtype=f32)
+        need = max(ft_moe_grouped_matmul_wgrad_workspace(I2, self.d, E), ft_moe_grouped_matmul_wgrad_workspace(self.d, self.I, E))
+        self.grad_ws = new(max(need, 16), dtype=torch.uint8)
+        self._buffers = (self.ids, self.w, self.inv, self.counts, self.offsets, self.gather, self.perm_ws, self.xs, self.gu, self.h,
+                         self.y_sorted, self.out, self.mask, self.dy, self.dh, self.dgu, self.dxs, self.dx, self.dw, self.dlogits, self.dw13,
+                         self.dw2, self.grad_ws)
+        if P == 0:
+            self.offsets.zero_()  # no forward() does
+        # The buffers are memory of the stream that is current here, whose work on tensors freed before may still run.
+        self._streams = {_raw_stream(dev)}
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+
+    def _on(self, stream):
+        """Keeps the buffers' memory, once they are freed, until the work on `stream` is done."""
+        if stream is not None and stream.device_index != self.dev:
+            _refuse(f"the stream is of cuda:{stream.device_index}, the layer is on cuda:{self.dev}")
+        if (_raw_stream(self.dev) if stream is None else stream.cuda_stream) not in self._streams:
+            s = torch.cuda.current_stream(self.dev) if stream is None else stream
+            for b in self._buffers:
+                b.record_stream(s)
+            self._streams.add(s.cuda_stream)
+
+    def forward(self, logits, x, stream=None):
+        """logits fp32 [T][E], x bf16 [T][d] -> (out [T][d], residual mask [T])."""
+        dev, T, E, k, slot, off = self.dev, self.T, self.E, self.k, self.slot_of, self.offsets
+        self._on(stream)
+        _take(x, "x", (_BF,), (T, self.d), dev)
+        pl = _take(logits, "logits", (_F32,), (T, E), dev)
+        if T == 0:
+            return self.out, self.mask[:0]
+        inv = self.inv[: T * k].view(T, k)
+        pi, pw, pv, pt = self.ids.data_ptr(), self.w.data_ptr(), inv.data_ptr(), slot.data_ptr()
+        _run(lib.ft_moe_route, dev, stream, pl, T, E, k, pi, pw)
+        _run(lib.ft_moe_permute, dev, stream, pi, T, E, k, self.counts.data_ptr(), off.data_ptr(), self.gather.data_ptr(), pv,
+             self.perm_ws.data_ptr(), self.perm_ws.numel())
+        ft_moe_dispatch(x, self.ids, inv, slot_of_expert=slot, x_sorted=self.xs, stream=stream, n_slots=self.n_slots)
+        ft_moe_grouped_matmul(self.xs, self.w13, off, slot_of_expert=slot, out=self.gu, stream=stream)
+        ft_moe_swiglu(self.gu, h=self.h, stream=stream)
+        ft_moe_grouped_matmul(self.h, self.w2, off, slot_of_expert=slot, out=self.y_sorted, stream=stream)
+        _run(lib.ft_moe_combine, dev, stream, self.y_sorted.data_ptr(), None, pi, pw, pv, pt, T, E, k, self.d,
+             self.out.data_ptr(), self.mask.data_ptr(), FT_N_SLOTS(self.n_slots) | (FT_OUT_BF16 if self.out_bf16 else 0))
+        return self.out, self.mask[:T]
+
+    def backward(self, dout, add: bool = False, stream=None):
+        """dout [T][d] (bf16 or fp32) of the last forward() -> (dx bf16 [T][d], dlogits fp32 [T][E], dw13 fp32 [E][2I][d],
+        dw2 fp32 [E][d][I])."""
+        T, slot, off, n = self.T, self.slot_of, self.offsets, self.n_slots
+        self._on(stream)
+        _take(dout, "dout", _FLOATS, (T, self.d), self.dev)
+        if T == 0:
+            inv = None
+        else:
+            inv = self.inv[: T * self.k].view(T, self.k)
+            ft_moe_combine_grad(dout, self.y_sorted, self.ids, self.w, inv, slot_of_expert=slot, dy_sorted=self.dy, dw=self.dw,
+                                dlogits=self.dlogits, stream=stream, n_slots=n)
+            ft_moe_grouped_matmul_grad(self.dy, self.w2, off, slot_of_expert=slot, da=self.dh, stream=stream)
+        grads = dict(slot_of_expert=slot, add=add, stream=stream, n_slots=n, ws=self.grad_ws)
+        ft_moe_grouped_matmul_wgrad(self.dy, self.h, off, dw=self.dw2, **grads)
+        if T > 0:
+            ft_moe_swiglu_grad(self.gu, self.dh, dgu=self.dgu, stream=stream)
+        ft_moe_grouped_matmul_wgrad(self.dgu, self.xs, off, dw=self.dw13, **grads)
+        if T > 0:
+            ft_moe_grouped_matmul_grad(self.dgu, self.w13, off, slot_of_expert=slot, da=self.dxs, stream=stream)
+            ft_moe_dispatch_grad(self.dxs, self.ids, inv, slot_of_expert=slot, dx=self.dx, stream=stream, n_slots=n)
+        return self.dx, self.dlogits, self.dw13, self.dw2

@@ -317,3 +317,296 @@ def test_adapters_special_values_stay_in_their_rows():
     bad[7] = True
     assert torch.equal(torch.isnan(out), bad)
     assert torch.isinf(out).sum() == 1 and out[9, 5] == float("inf")
+
+
+# ---------------------------------------------------------------------------------------------- together
+
+def layer_case(seed, T, E, k, d, I, held):
+    g = gen(seed)
+    n = E if held is None else held
+    r = rows_ref.routing(g, T, E, k, held)
+    return r, normal(g, T, d), normal(g, n, 2 * I, d, scale=d ** -0.5), normal(g, n, d, I, scale=I ** -0.5), normal(g, T, d)
+
+
+LAYERS = [(1, 8, 2, 64, 40, None, False), (5, 4, 3, 72, 136, 2, True), (65, 16, 4, 264, 96, 11, False), (400, 8, 8, 128, 264, None, True),
+          (900, 40, 5, 520, 328, 33, False)]
+
+
+@pytest.mark.parametrize("T, E, k, d, I, held, out_bf16", LAYERS)
+def test_layer_step_by_step(T, E, k, d, I, held, out_bf16):
+    """Every buffer of forward() and backward() against the definition of its step from the buffers before it."""
+    r, x, w13, w2, dout = layer_case(T + E, T, E, k, d, I, held)
+    slot = None if held is None else r["slot"]
+    n = w13.shape[0]
+    layer = ft.Bf16MoELayer(w13.cuda(), w2.cuda(), dev(slot), k=k, T=T, out_bf16=out_bf16)
+    out, mask = layer.forward(r["logits"].cuda(), x.cuda())
+    dx, dl, dw13, dw2 = layer.backward(dout.cuda())
+    assert out.dtype == (BF if out_bf16 else F32) and dx.dtype == BF and dw13.dtype == dw2.dtype == F32
+    c = {v: getattr(layer, v).cpu() for v in ("ids", "w", "inv", "offsets", "xs", "gu", "h", "y_sorted", "dy", "dh", "dgu", "dxs", "dw")}
+    ids, inv, off = c["ids"], c["inv"].view(T, k), c["offsets"]
+    rows = rows_ref.pair_rows(ids, inv, E, slot)
+    has = rows >= 0
+    live = rows[has]
+    assert torch.equal(ids, r["ids"])
+    assert torch.equal(c["xs"][live], x[:, None, :].expand(T, k, d)[has])
+
+    def close(got, want, bound, at):
+        assert ((got.double() - want).abs()[at] <= bound[at]).all()
+
+    def product(name, a, w, grad):
+        ok, want, mag = ref.forward(torch.nan_to_num(a), w.transpose(1, 2) if grad else w, off, slot, None)
+        assert torch.equal(ok.nonzero()[:, 0], live.sort()[0])
+        close(c[name], want, ref.sum_bound(want, mag, a.shape[1], BF), ok)
+
+    product("gu", c["xs"], w13, False)
+    want, slack = ref.swiglu(c["gu"])
+    close(c["h"], want, slack * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY, live)
+    product("y_sorted", c["h"], w2, False)
+    y = torch.where(has[:, :, None], c["y_sorted"].double()[rows.clamp(min=0)], torch.zeros((), dtype=torch.float64))
+    terms = c["w"].double()[:, :, None] * y
+    want = terms.sum(1)
+    assert ((out.cpu().double() - want).abs() <= 2 * k * ref.U32 * terms.abs().sum(1) + (ref.UBF * want.abs() if out_bf16 else 0) + ref.TINY).all()
+    assert torch.equal(((mask.cpu()[:, None] >> torch.arange(k)) & 1).bool(), ~has)
+    # back: the combine's gradient is checked by its own tests
+    product("dh", c["dy"], w2, True)
+    want, slack = ref.swiglu_gradient(c["gu"], c["dh"])
+    close(c["dgu"], want, slack * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY, live)
+    product("dxs", c["dgu"], w13, True)
+    for got, a, b in ((dw2, "dy", "h"), (dw13, "dgu", "xs")):
+        ok, want, mag, most = ref.matrix_gradient(torch.nan_to_num(c[a]), torch.nan_to_num(c[b]), off, slot, n)
+        close(got.cpu(), want, ref.sum_bound(want, mag, max(most, 1), F32), ok)
+    g = torch.where(has[:, :, None], c["dxs"].double()[rows.clamp(min=0)], torch.zeros((), dtype=torch.float64))
+    assert ((dx.cpu().double() - g.sum(1)).abs() <= k * ref.U32 * g.abs().sum(1) + ref.UBF * g.sum(1).abs()).all()
+
+
+def test_layer_gradients_against_autograd():
+    """The whole step against fp64 autograd without roundings.  On the way to a gradient at most six bf16 roundings come
+    one after another (gu, h, y or dy, dh, dgu, dx), each within 2^-8 of every value: together they leave less than 6 * 2^-8 of
+    a gradient's norm where they do not all point one way; a wrong term leaves a large part of it."""
+    T, E, k, d, I = 200, 6, 3, 256, 192
+    r, x, w13, w2, dout = layer_case(5, T, E, k, d, I, None)
+    layer = ft.Bf16MoELayer(w13.cuda(), w2.cuda(), k=k, T=T)
+    out = layer.forward(r["logits"].cuda(), x.cuda())[0].cpu().double()
+    got = [t.cpu().double() for t in layer.backward(dout.cuda())]
+    leaves = [t.double().requires_grad_() for t in (x, r["logits"], w13, w2)]
+    X, L, W13, W2 = leaves
+    ids = r["ids"].long()
+    w = L.gather(1, ids).softmax(1)
+    ffn = []
+    for e in range(E):
+        gate, up = (X @ W13[e].t()).chunk(2, 1)
+        ffn.append((gate * torch.sigmoid(gate) * up) @ W2[e].t())
+    want = (w[:, :, None] * torch.stack(ffn, 1).gather(1, ids[:, :, None].expand(T, k, d))).sum(1)
+    assert (out - want).norm() <= 3 * ref.UBF * want.norm()
+    for mine, theirs in zip(got, torch.autograd.grad((want * dout.double()).sum(), leaves)):
+        assert (mine - theirs).norm() <= 6 * ref.UBF * theirs.norm()
+
+
+def test_layer_without_tokens_and_adding():
+    r, x, w13, w2, dout = layer_case(1, 30, 4, 2, 64, 48, 3)
+    slot = r["slot"].cuda()
+    none = ft.Bf16MoELayer(w13.cuda(), w2.cuda(), slot, k=2, T=0)
+    out, mask = none.forward(r["logits"][:0].cuda(), x[:0].cuda())
+    assert out.shape == (0, 64) and mask.shape == (0,)
+    none.dw13.fill_(FILL)
+    dx, dl, dw13, _ = none.backward(dout[:0].cuda(), add=True)
+    assert dx.shape == (0, 64) and dl.shape == (0, 4) and (dw13 == FILL).all()
+    dw13 = none.backward(dout[:0].cuda())[2]
+    assert (dw13[slot >= 0] == 0).all() and (dw13[slot < 0] == FILL).all()
+    layer = ft.Bf16MoELayer(w13.cuda(), w2.cuda(), slot, k=2, T=30)
+    layer.forward(r["logits"].cuda(), x.cuda())
+    once = [t.clone() for t in layer.backward(dout.cuda())]
+    again = [t.clone() for t in layer.backward(dout.cuda())]
+    held = slot >= 0
+    assert all(same_bits(a[held], b[held]) if a.dim() == 3 else same_bits(a, b) for a, b in zip(once, again))
+    twice = layer.backward(dout.cuda(), add=True)
+    for a, b in zip(once[2:], twice[2:]):
+        assert torch.equal(b[held], a[held] * 2)
+
+
+def capture(fn):
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fn()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fn()
+    return graph, out
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_graph_replays_match_eager_calls(T):
+    """A captured training step and a captured adapter call, replayed with other inputs and eager work in between."""
+    E, k, d, I, r_, n = 40, 4, 264, 136, 72, 9
+    case, x, w13, w2, dout = layer_case(T, T, E, k, d, I, 30)
+    slot = case["slot"].cuda()
+    layer, eager = (ft.Bf16MoELayer(w13.cuda(), w2.cuda(), slot, k=k, T=T) for _ in range(2))
+    g = gen(T)
+    off, gather = (t.cuda() for t in adapter_rows(g, T, n))
+    a, b = normal(g, n, r_, d, scale=0.1).cuda(), normal(g, n, d, r_).cuda()
+    logits, X, D, base = case["logits"].cuda(), x.cuda(), dout.cuda(), torch.zeros(T, d, device="cuda", dtype=BF)
+    args = [logits.clone(), X.clone(), D.clone(), base.clone()]
+
+    def step(layer, logits, X, D, base):
+        out, mask = layer.forward(logits, X)
+        return (out, mask, *layer.backward(D), ft.ft_moe_lora(base, X, a, b, off, gather))
+
+    for m in (layer, eager):
+        m.dw13.zero_(), m.dw2.zero_()
+    graph, outs = capture(lambda: step(layer, *args))
+    for turn in range(4):
+        fresh = [torch.randn(t.shape, generator=gen(10 * turn + i)).to(t.dtype).cuda() for i, t in enumerate(args)]
+        for t, f in zip(args, fresh):
+            t.copy_(f)
+        graph.replay()
+        got = [t.clone() for t in outs]
+        want = step(eager, *fresh)
+        torch.cuda.synchronize()
+        assert all(same_bits(p, q) for p, q in zip(got, want)), turn
+
+
+def test_two_streams_at_once():
+    """Calls of one kind at the same time on two streams, large ones with workspaces of their own, match calls in turn."""
+    g = gen(6)
+    E, P, N, K = 128, 3000, 520, 776
+    off = sizes(g, E, P).cuda()
+    w, a, d = normal(g, E, N, K).cuda(), normal(g, P, K).cuda(), normal(g, P, N).cuda()
+    aoff, gather = (t.cuda() for t in adapter_rows(g, P, 7))
+    la, lb, base = normal(g, 7, 64, K, scale=0.1).cuda(), normal(g, 7, N, 64).cuda(), torch.randn(P, N, generator=g).cuda()
+    assert ft.ft_moe_grouped_matmul_wgrad_workspace(N, K, E) > 0 and ft.ft_moe_lora_workspace(P, 7, 64, N, K) > 0
+
+    def calls():
+        return (ft.ft_moe_grouped_matmul(a, w, off), ft.ft_moe_grouped_matmul_grad(d, w, off), ft.ft_moe_grouped_matmul_wgrad(d, a, off),
+                ft.ft_moe_lora(base, a, la, lb, aoff, gather))
+
+    want = calls()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for turn in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(calls())
+    torch.cuda.synchronize()
+    for outs in got:
+        assert all(same_bits(p, q) for p, q in zip(outs, want))
+
+
+def test_outputs_on_a_given_stream():
+    g = gen(7)
+    a, w, off = normal(g, 50, 72).cuda(), normal(g, 2, 40, 72).cuda(), torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = ft.ft_moe_grouped_matmul(a, w, off, stream=s)
+    s.synchronize()
+    assert same_bits(got, ft.ft_moe_grouped_matmul(a, w, off))
+
+
+def test_refused_tensors():
+    z = lambda *s, dtype=BF: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    off, i32 = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda"), torch.int32
+    a, w, d = z(5, 64), z(2, 32, 64), z(5, 32)
+    bad = [lambda: ft.ft_moe_grouped_matmul(a.float(), w, off), lambda: ft.ft_moe_grouped_matmul(a.t(), w, off),
+           lambda: ft.ft_moe_grouped_matmul(a, w[:, :, :32], off), lambda: ft.ft_moe_grouped_matmul(a, w.float(), off),
+           lambda: ft.ft_moe_grouped_matmul(a, w, off.long()), lambda: ft.ft_moe_grouped_matmul(a, w, off[:1]),
+           lambda: ft.ft_moe_grouped_matmul(a, w[:1].contiguous(), off), lambda: ft.ft_moe_grouped_matmul(a, w, off, out=z(5, 64)),
+           lambda: ft.ft_moe_grouped_matmul(a, w, off, out=z(5, 32, dtype=torch.float16)), lambda: ft.ft_moe_grouped_matmul(a, w, off, out_dtype=torch.float16),
+           lambda: ft.ft_moe_grouped_matmul(a, w, off, slot_of_expert=z(3, dtype=i32)), lambda: ft.ft_moe_grouped_matmul(a[:, :60].contiguous(), w[:, :, :60].contiguous(), off),
+           lambda: ft.ft_moe_grouped_matmul(a.to_sparse(), w, off), lambda: ft.ft_moe_grouped_matmul(z(6 * 64 + 1)[1:].view(6, 64), w, off),
+           lambda: ft.ft_moe_grouped_matmul_grad(a, w, off), lambda: ft.ft_moe_grouped_matmul_wgrad(d, z(4, 64), off),
+           lambda: ft.ft_moe_grouped_matmul_wgrad(d, a, off, add=True), lambda: ft.ft_moe_grouped_matmul_wgrad(d, a, off, dw=z(2, 32, 64), add=True),
+           lambda: ft.ft_moe_grouped_matmul_wgrad(d, a, off, n_slots=3), lambda: ft.ft_moe_grouped_matmul_wgrad(z(5, 2048), z(5, 2048), torch.zeros(100, dtype=i32, device="cuda"), ws=z(64, dtype=torch.uint8)),
+           lambda: ft.ft_moe_swiglu(z(3, 63)), lambda: ft.ft_moe_swiglu(z(3, 24)), lambda: ft.ft_moe_swiglu_grad(z(3, 32), z(3, 32)),
+           lambda: ft.ft_moe_swiglu_grad(z(3, 32), z(3, 16, dtype=F32)),
+           lambda: ft.ft_moe_lora(d, a, z(2, 8, 64), z(2, 32, 16), off, z(5, dtype=i32)), lambda: ft.ft_moe_lora(d, a, z(2, 4, 64), z(2, 32, 4), off, z(5, dtype=i32)),
+           lambda: ft.ft_moe_lora(d, a, z(2, 8, 64), z(2, 32, 8), off, z(4, dtype=i32)), lambda: ft.ft_moe_lora(d, a, z(2, 8, 64), z(2, 32, 8), off, z(5, dtype=i32), scale=z(3, dtype=F32)),
+           lambda: ft.ft_moe_lora(d, a, z(2, 8, 64), z(2, 32, 8), off, z(5, dtype=i32), out=z(5, 32, dtype=F32)),
+           lambda: ft.ft_moe_lora(d, a, z(2, 8, 64), z(2, 32, 8), off, z(5, dtype=i32), ws=torch.zeros(8)),
+           lambda: ft.Bf16MoELayer(z(2, 32, 64), z(2, 64, 8), k=1, T=4), lambda: ft.Bf16MoELayer(z(2, 32, 64), z(2, 64, 16), k=3, T=4)]
+    for i, call in enumerate(bad):
+        with pytest.raises(ft.FtError):
+            call()
+            raise AssertionError(i)
+    assert ft.ft_moe_grouped_matmul(z(0, 64), w, off).shape == (0, 32) and ft.ft_moe_swiglu(z(0, 32)).shape == (0, 16)
+    assert ft.ft_moe_lora(z(0, 32), z(0, 64), z(2, 8, 64), z(2, 32, 8), off, z(0, dtype=i32)).shape == (0, 32)
+
+
+def test_calls_repeat_bit_for_bit():
+    g = gen(12)
+    P, E, N, K = 2500, 30, 264, 520
+    off = sizes(g, E, P).cuda()
+    w, a, d = normal(g, E, N, K).cuda(), normal(g, P, K).cuda(), normal(g, P, N).cuda()
+    calls = (lambda: ft.ft_moe_grouped_matmul(a, w, off), lambda: ft.ft_moe_grouped_matmul_grad(d, w, off), lambda: ft.ft_moe_grouped_matmul_wgrad(d, a, off))
+    for call in calls:
+        first = call()
+        for _ in range(3):
+            assert same_bits(call(), first)
+
+
+def test_adapters_beside_an_8_bit_projection():
+    """A shared projection on 8-bit rows, the rows' adapters permuted by the library, and the adapters added in place."""
+    g = gen(13)
+    T, n, r, N, K = 90, 6, 16, 264, 528
+    ids = torch.randint(0, n + 1, (T, 1), generator=g).int().cuda()  # n: none
+    _, off, gather, _ = ft.ft_moe_permute(ids, n + 1)
+    x, w = normal(g, T, K), normal(g, N, K, scale=0.05)
+    a, b, scale = normal(g, n, r, K, scale=0.05), normal(g, n, N, r, scale=0.2), torch.rand(n, generator=g)
+    codes, scales = ft.ft_moe_quant_fp8(x.cuda())
+    wc, ws = rows_ref.random_weights(g, N, K)
+    out = ft.ft_moe_fp8_matmul(codes, scales, wc.cuda(), ws.cuda())
+    base = out.cpu().clone()
+    ft.ft_moe_lora(out, x.cuda(), a.cuda(), b.cuda(), off[: n + 1].contiguous(), gather, scale=scale.cuda(), out=out)
+    want, bound = ref.adapters(base, x, a, b, off.cpu()[: n + 1], gather.cpu(), None, scale)
+    assert ((out.cpu().double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("E, P, N, K", [(1024, 90000, 264, 72), (1022, 60000, 520, 136), (128, 40000, 1032, 200), (48, 9000, 520, 448)])
+def test_tiles_of_many_experts(E, P, N, K, grad):
+    """Tables of experts that leave less LDS to the tiles; groups of every height."""
+    g = gen(E)
+    check_forward(normal(g, P, N if grad else K), normal(g, E, N, K), sizes(g, E, P), None, BF, grad)
+
+
+@pytest.mark.parametrize("P, N, K", [(300, 264, 520), (5000, 1032, 2056), (70000, 264, 520)])
+def test_planned_matrix_gradient(P, N, K):
+    """More tiles than two a compute unit: from queues, with experts of every class of rows, some without a slot."""
+    g = gen(P)
+    E = 90 if N < 1000 else 20
+    cuts = (torch.rand(E - 1, generator=g) ** 4 * P).long().sort()[0]
+    off = torch.cat([torch.zeros(1), cuts, torch.full((1,), P)]).int()
+    slot = torch.arange(E).int()
+    slot[5], slot[11] = -1, E
+    dout, a = normal(g, P, N), normal(g, P, K)
+    assert ft.ft_moe_grouped_matmul_wgrad_workspace(N, K, E) > 0
+    dw = filled(E, N, K, dtype=F32)
+    ft.ft_moe_grouped_matmul_wgrad(dout.cuda(), a.cuda(), off.cuda(), slot_of_expert=slot.cuda(), dw=dw, n_slots=E)
+    for e in range(E):
+        got = dw[e].cpu().double()
+        if not 0 <= slot[e] < E:
+            assert (got == FILL).all()
+            continue
+        x, y = dout[off[e]:off[e + 1]].double(), a[off[e]:off[e + 1]].double()
+        want, mag = x.t() @ y, x.abs().t() @ y.abs()
+        assert ((got - want).abs() <= ref.sum_bound(want, mag, max(x.shape[0], 1), F32)).all(), e
+
+
+def test_adapters_past_32_bits():
+    """Rows of x whose byte offsets pass 2^32, and positions of gather that name them; checked at the ends."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, r, N, K = (1 << 18) + 77, 8, 16, 8200
+    x = torch.empty(T, K, dtype=BF, device="cuda").normal_(generator=g)
+    a = torch.empty(2, r, K, dtype=BF, device="cuda").normal_(generator=g) * 0.02
+    b = torch.empty(2, N, r, dtype=BF, device="cuda").normal_(generator=g)
+    base = torch.empty(T, N, device="cuda").normal_(generator=g)
+    gather = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 70, T - 5], dtype=torch.int32, device="cuda")  # the last 70 rows, all but the first 5
+    out = ft.ft_moe_lora(base, x, a, b, off, gather)
+    assert same_bits(out[:5], base[:5])
+    for s, rows in ((0, slice(T - 70, T)), (1, slice(5, 12)), (1, slice(T - 80, T - 70))):
+        n = rows.stop - rows.start
+        part = torch.tensor([0, n]).int()
+        want, bound = ref.adapters(base[rows].cpu(), x[rows].cpu(), a[s:s + 1].cpu(), b[s:s + 1].cpu(), part, torch.arange(n).int(), None, None)
+        assert ((out[rows].cpu().double() - want).abs() <= bound).all()

@@ -152,3 +152,52 @@ def test_reference_gradients_against_differences():
         v[1].view(-1)[i] -= h
         diff = sum(sign * (dh * ref.swiglu(u)[0]).sum() for sign, u in ((1, v[0]), (-1, v[1]))) / (2 * h)
         assert abs(diff - dgu.view(-1)[i]) < 1e-7
+
+
+def test_layer_orders_its_buffers_with_the_streams(monkeypatch):
+    """With stand-ins for the GPU: making a layer waits for the current stream, and a step on a stream that did not make it
+    records every buffer for that stream, once."""
+    import contextlib
+    import types
+
+    from routed_expert_ffn_wave_amd import products
+    made, waits, used = [], [], []
+
+    class Buffer(torch.Tensor):
+        def record_stream(self, stream):
+            used.append((id(self), stream.cuda_stream))
+
+    def new(shape, dtype, dev, stream=None):
+        made.append(torch.zeros(shape).to(dtype).as_subclass(Buffer))
+        return made[-1]
+
+    streams = {n: types.SimpleNamespace(cuda_stream=n, device_index=0, synchronize=lambda n=n: waits.append(n)) for n in (1, 2, 3)}
+    current = [1]
+    monkeypatch.setattr(products, "_new", new)
+    monkeypatch.setattr(products, "_first", lambda t, name, dims, dtypes, stream=None: (0, t.shape))
+    monkeypatch.setattr(products, "_take", lambda t, name, dtypes, shape, dev: t.data_ptr())
+    monkeypatch.setattr(products, "_run", lambda *a: None)
+    monkeypatch.setattr(products, "_raw_stream", lambda dev: current[0])
+    for name in ("ft_moe_dispatch", "ft_moe_dispatch_grad", "ft_moe_combine_grad", "ft_moe_grouped_matmul", "ft_moe_grouped_matmul_grad",
+                 "ft_moe_grouped_matmul_wgrad", "ft_moe_swiglu", "ft_moe_swiglu_grad"):
+        monkeypatch.setattr(products, name, lambda *a, **k: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: streams[current[0]])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s).to(dtype)  # noqa: E731
+    layer = products.Bf16MoELayer(z(2, 64, 64), z(2, 64, 32), torch.zeros(4, dtype=torch.int32), k=2, T=4)
+    assert waits == [1] and sorted(id(b) for b in layer._buffers) == sorted(id(b) for b in made)
+    args = (torch.zeros(4, 4), z(4, 64))
+    layer.forward(*args)
+    layer.backward(z(4, 64))
+    assert used == []
+    layer.forward(*args, stream=streams[2])
+    assert sorted(used) == sorted((id(b), 2) for b in made)
+    layer.backward(z(4, 64), stream=streams[2])
+    current[0] = 3
+    layer.backward(z(4, 64))
+    layer.forward(*args)
+    assert sorted(used) == sorted((id(b), n) for b in made for n in (2, 3))
+    assert waits == [1]
+    with pytest.raises(ft.FtError, match="the stream is of cuda:1"):
+        layer.forward(*args, stream=types.SimpleNamespace(cuda_stream=9, device_index=1))
