@@ -19,15 +19,15 @@ __device__ __forceinline__ void dma16_at(const uint8_t* from, uint32_t lds) {
   asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds), "i"(AT) : "memory", "scc");
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1>
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1, int BK_ = 64>
 struct Bf16Cfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;  // NS: stages in LDS
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, BK = BK_;  // NS stages of BK steps in LDS
   // KG > 1: a block is KG groups of waves, each with the whole tile, a share of the reduction and stages of its own.
   static constexpr int KG = KG_, GW = WM * WN, NT = 64 * GW * KG;
   static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;              // fragments of a wave
-  static constexpr int QM = BM / (8 * GW), QN = BN / (8 * GW);            // loads of 16 bytes a lane and stage
-  static constexpr int STAGE = (BM + BN) * 128, RING = NS * STAGE, LDS = KG * RING;  // RING: a group's stages
-  static_assert(BM % (8 * GW) == 0 && BN % (8 * GW) == 0, "load passes");
+  static constexpr int QM = BM * BK / (512 * GW), QN = BN * BK / (512 * GW);         // loads of 16 bytes a lane and stage
+  static constexpr int PM = BM * BK * 2, STAGE = (BM + BN) * BK * 2, RING = NS * STAGE, LDS = KG * RING;  // RING: a group's stages
+  static_assert(BM * BK % (512 * GW) == 0 && BN * BK % (512 * GW) == 0 && (BK == 64 || BK == 32), "load passes");
   static_assert((NS - 1) * (QM + QN) <= 63, "what the load counter holds");
 };
 
@@ -43,10 +43,10 @@ struct Operand {
 };
 
 // An operand's loads into its part of a stage, B rows or columns wide, by GW waves.
-template <int MODE, int B, int GW>
+template <int MODE, int B, int GW, int BK = 64>
 struct Loader {
-  static constexpr int Q = B / (8 * GW);
-  static constexpr int CH = MODE == ACROSS ? B / 8 : 8;  // chunks of a row in LDS
+  static constexpr int Q = B * BK / (512 * GW);
+  static constexpr int CH = MODE == ACROSS ? B / 8 : BK / 8;  // chunks of a row in LDS
   static constexpr int RP = 64 * GW / CH;                // rows of a load pass
   uint32_t off[Q];
   const uint8_t* at[MODE == GATHERED ? Q : 1];
@@ -55,7 +55,7 @@ struct Loader {
 
   // Rows 0 - 3 and 8 - 11 of an ACROSS stage are read together (32 bytes each), as are 16 rows of a DIRECT one (16 bytes).
   static __device__ __forceinline__ int key(int row) {
-    if (MODE != ACROSS) return (row >> 1) & 7;
+    if (MODE != ACROSS) return BK == 64 ? (row >> 1) & 7 : ((row >> 1) ^ (row >> 2)) & 3;
     return B == 64 ? (row & 2) | ((row >> 1) & 4) : 2 * ((row & 3) | ((row >> 1) & 4));
   }
   static __device__ __forceinline__ int row_of(int q, int tid) { return q * RP + tid / CH; }
@@ -64,7 +64,7 @@ struct Loader {
   // red: length of the reduction.  What lies past it, or past `rows`, repeats something inside.
   __device__ __forceinline__ void open(const Operand& o, int tid, int red) {
     p = (const uint8_t*)o.base;
-    step = MODE == ACROSS ? (size_t)o.ld * 128 : 128;
+    step = MODE == ACROSS ? (size_t)o.ld * BK * 2 : BK * 2;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int r = row_of(q, tid), c = chunk_of(q, tid);
@@ -77,7 +77,7 @@ struct Loader {
                       : (uint32_t)min(r, o.rows - 1) * (uint32_t)(o.ld * 2) + (uint32_t)(c * 8 < red ? c : 0) * 16;
     }
   }
-  // The last stage is a short one of `left` < 64 steps.
+  // The last stage is a short one of `left` < BK steps.
   __device__ __forceinline__ void shorten(const Operand& o, int tid, int left) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -100,14 +100,14 @@ struct Loader {
   __device__ __forceinline__ void advance() {
     if constexpr (MODE == GATHERED)
 #pragma unroll
-      for (int q = 0; q < Q; ++q) at[q] += 128;
+      for (int q = 0; q < Q; ++q) at[q] += BK * 2;
     else
       p += step;
   }
   __device__ __forceinline__ void skip(int stages) {
     if constexpr (MODE == GATHERED)
 #pragma unroll
-      for (int q = 0; q < Q; ++q) at[q] += stages * 128;
+      for (int q = 0; q < Q; ++q) at[q] += stages * BK * 2;
     else
       p += (long long)stages * (long long)step;
   }
@@ -120,7 +120,7 @@ struct Loader {
 };
 
 // Reads of an operand's fragments, 16 rows or columns by 32 steps, from its part of a stage.
-template <int MODE, int B, int F>
+template <int MODE, int B, int F, int BK = 64>
 struct Reader {
   uint32_t off[MODE == ACROSS ? F : 1];
   __device__ __forceinline__ void open(int first, int lane) {  // first: the wave's first row or column
@@ -130,10 +130,10 @@ struct Reader {
 #pragma unroll
       for (int f = 0; f < F; ++f) off[f] = row * B * 2 + (((first / 8 + 2 * f) ^ key) << 4) + (r & 3) * 8;
     } else {
-      off[0] = (first + r) * 128 + ((g ^ Loader<DIRECT, B, 1>::key(r)) << 4);
+      off[0] = (first + r) * BK * 2 + ((g ^ Loader<DIRECT, B, 1, BK>::key(r)) << 4);
     }
   }
-  // half 0, 1: steps 0 - 31 and 32 - 63
+  // half 0, 1: steps 0 - 31 and 32 - 63 of the stage
   template <int half>
   __device__ __forceinline__ bf16x8 read(const uint8_t* part, int f) const {
     if constexpr (MODE == ACROSS) {
@@ -144,7 +144,7 @@ struct Reader {
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(at + 4 * B * 2));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      return *(const bf16x8*)(part + (off[0] ^ (half * 64)) + f * 2048);
+      return *(const bf16x8*)(part + (off[0] ^ (half * 64)) + f * 32 * BK);
     }
   }
 };
@@ -158,7 +158,7 @@ struct Reader {
 // fragments have been read by then: from there on the buffer of this stage takes the loads of the stage NS ahead.
 template <class C, int RMODE, int CMODE>
 __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, int red, uint8_t* lds, f32x4 (&acc)[C::MF][C::NF],
-                                          int turn = 0) {
+                                          int rotate = 0) {
   constexpr int MF = C::MF, NF = C::NF, NS = C::NS, U = C::QM + C::QN;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % C::GW, tid = wv * 64 + lane;
   const int wm = wv / C::WN, wn = wv % C::WN;
@@ -167,19 +167,19 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
   if (red <= 0) return;
-  const int nb = (red + 63) / 64, left = red & 63;  // stages; the last has `left` steps if that is not 0
-  Loader<RMODE, C::BM, C::GW> lr;
-  Loader<CMODE, C::BN, C::GW> lc;
+  const int nb = (red + C::BK - 1) / C::BK, left = red % C::BK;  // stages; the last has `left` steps if that is not 0
+  Loader<RMODE, C::BM, C::GW, C::BK> lr;
+  Loader<CMODE, C::BN, C::GW, C::BK> lc;
   lr.open(ro, tid, red);
   lc.open(co, tid, red);
-  Reader<RMODE, C::BM, MF> rr;
-  Reader<CMODE, C::BN, NF> rc;
+  Reader<RMODE, C::BM, MF, C::BK> rr;
+  Reader<CMODE, C::BN, NF, C::BK> rc;
   rr.open(wm * 16 * MF, lane);
   rc.open(wn * 16 * NF, lane);
   const uint32_t lds0 = lds_addr(lds) + wv * 1024;
   int fill = 0, wrap = 0;  // stages loaded; the one after which the first follows (0: none)
-  if (turn > 0 && left == 0) {
-    const int first = turn % nb;
+  if (rotate > 0 && left == 0) {
+    const int first = rotate % nb;
     wrap = first ? nb - first : 0;
     lr.skip(first);
     lc.skip(first);
@@ -196,7 +196,7 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
     if constexpr (u < C::QM)
       lr.template issue<u, 0>(fill_lds);
     else
-      lc.template issue<u - C::QM, C::BM * 128>(fill_lds);
+      lc.template issue<u - C::QM, C::PM>(fill_lds);
   };
   auto advance = [&] {
     ++fill;
@@ -209,8 +209,8 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
     if constexpr (C::GW > 1) asm volatile("s_barrier" ::: "memory");
   };
   auto clear = [&](uint8_t* st) {
-    Loader<RMODE, C::BM, C::GW>::clear(st, tid, left);
-    Loader<CMODE, C::BN, C::GW>::clear(st + C::BM * 128, tid, left);
+    Loader<RMODE, C::BM, C::GW, C::BK>::clear(st, tid, left);
+    Loader<CMODE, C::BN, C::GW, C::BK>::clear(st + C::PM, tid, left);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     meet();
   };
@@ -218,7 +218,7 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
   uint8_t* st = lds;
   auto frag = [&](const uint8_t* from, auto half, int n) {
     constexpr int H = decltype(half)::value;
-    return n < NF ? rc.template read<H>(from + C::BM * 128, n) : rr.template read<H>(from, n - NF);
+    return n < NF ? rc.template read<H>(from + C::PM, n) : rr.template read<H>(from, n - NF);
   };
   using Half0 = std::integral_constant<int, 0>;
   using Half1 = std::integral_constant<int, 1>;
@@ -253,23 +253,57 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
 #pragma unroll
   for (int n = 0; n < NF + MF; ++n) f0[n] = frag(st, Half0{}, n);
   int b = 0;
-  for (; b < nb - NS; ++b) {
-    half(f0, f1, st, Half1{}, std::false_type{});
-    // the next stage has landed for every wave, and every wave has read this one
+  // The next stage has landed for every wave, and every wave has read this one, whose buffer may be loaded again.
+  auto turn = [&] {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * U) : "memory");
     meet();
     open();
     st = after(st);
-    half(f1, f0, st, Half0{}, std::true_type{});
-    advance();
-  }
-  for (; b < nb; ++b) {  // nothing left to load
-    half(f0, f1, st, Half1{}, std::false_type{});
+  };
+  auto last_turn = [&] {  // nothing is left to load
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     meet();
     st = after(st);
     if (b == nb - 2 && left) clear(st);
-    half(f1, f0, st, Half0{}, std::false_type{});  // past the last stage: read but unused
+  };
+  // (Past the last stage fragments are read but unused.)
+  if constexpr (C::BK == 64) {
+    for (; b < nb - NS; ++b) {
+      half(f0, f1, st, Half1{}, std::false_type{});
+      turn();
+      half(f1, f0, st, Half0{}, std::true_type{});
+      advance();
+    }
+    for (; b < nb; ++b) {
+      half(f0, f1, st, Half1{}, std::false_type{});
+      last_turn();
+      half(f1, f0, st, Half0{}, std::false_type{});
+    }
+  } else {
+    for (; b < nb - NS - 1; b += 2) {
+      turn();
+      half(f0, f1, st, Half0{}, std::true_type{});
+      advance();
+      turn();
+      half(f1, f0, st, Half0{}, std::true_type{});
+      advance();
+    }
+    if (b < nb - NS) {  // an odd one: its successor is in f1
+      turn();
+      half(f0, f1, st, Half0{}, std::true_type{});
+      advance();
+      ++b;
+      last_turn();
+      half(f1, f0, st, Half0{}, std::false_type{});
+      ++b;
+    }
+    for (; b < nb; ++b) {
+      last_turn();
+      half(f0, f1, st, Half0{}, std::false_type{});
+      if (++b >= nb) break;
+      last_turn();
+      half(f1, f0, st, Half0{}, std::false_type{});
+    }
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   meet();  // the stages are free for the next tile
