@@ -20,7 +20,8 @@
  * skipped.  Several experts may name one matrix.
  *
  * Sums are fp32 sums of exact products of bf16 values, rounded once to the output's type.  Their order, and with it a
- * result's last bits, depends on the sizes of the call (not on the number of rows its expert has).
+ * result's last bits, depends on the sizes of the call and, for the rows, on the slot of their matrix; for a matrix's
+ * gradient, on the number of rows its expert has.
  */
 #ifndef FT_MOE_PRODUCTS_H
 #define FT_MOE_PRODUCTS_H
@@ -89,8 +90,10 @@ int ft_moe_swiglu_grad(const uint16_t* gu, const uint16_t* dh, int rows, int I, 
  * rows' adapters (k = 1); rows without an adapter are given number E there (and E + 1 experts), or an adapter
  * without a slot in [0, n_slots).  slot_of_adapter NULL: adapter i is in slot i (E <= n_slots).  Positions from
  * offsets[E] on count as rows without an adapter; entries of gather outside [0, T) are skipped; a row that gather
- * does not name is left as it was, one that it names twice is formed twice (with out == base: added twice or once).
- * r % 8 == 0, r <= 256 (adapters of smaller rank: zeros behind), N % 8 == 0, K % 8 == 0, both at most 2^20.
+ * does not name is left as it was, one that it names twice is formed twice (with out == base: added twice or once),
+ * and rows that a table which does not ascend gives to several adapters get values of no use.
+ * r % 8 == 0, r <= 256 (adapters of smaller rank: zeros behind), N % 8 == 0, K % 8 == 0, both at most 2^20, T < 2^24;
+ * sizes whose tiles an int cannot count, whatever offsets holds, are refused with FT_E_UNSUPPORTED.
  * The inner sums are held in fp32 and enter the outer ones as two bf16 terms, within 2^-16 of themselves.
  * ws: ft_moe_lora_workspace(T, E, r, N, K) bytes of device memory (0 for few rows: then ws may be NULL).
  */

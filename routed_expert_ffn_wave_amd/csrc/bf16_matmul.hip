@@ -5,6 +5,12 @@
 //   rows           da[p][k]    = sum_n dout[p][n] w[e][n][k]
 //   matrices       dw[e][n][k] = sum_{p of e} dout[p][n] a[p][k]
 // bf16 products are exact in fp32 and added there by the matrix instructions; results are rounded once.
+//
+// What bounds them.  Compute: 16384 rows of one 4096 x 7168 matrix take 690 - 710 us forward (1.36 - 1.4 PFLOP/s; the library 615) and
+// 670 - 700 back (the library 700), 8 experts with 2048 rows each 808 us for the matrices (1.19 PFLOP/s; the library's dense
+// product of that layout 1.0 - 1.2): without the loads 583 of 740 us, without the matrix instructions 623, so neither alone; the clock
+// falls to 1.4 - 1.7 GHz under them.  Memory: 128 experts of 1536 x 2048 with 64 rows each 147 - 156 us (5.6 TB/s), 16 tokens 92 us (5.4).
+// Between them both share the time: 256 rows each 210 us (bytes alone 166, products alone 132).
 #include <algorithm>
 #include <cmath>
 
@@ -33,7 +39,9 @@ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int
   f32x4 acc[C::MF][C::NF];
   const Operand ro{a.a + (size_t)row0 * red, red, rows, nullptr, 0};
   const Operand co{GRAD ? w + n0 : w + (size_t)n0 * a.K, a.K, min(C::BN, cols - n0), nullptr, 0};
-  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, red, lds, acc, GRAD ? 0 : slot * 7);
+  // Experts begin at different stages of a forward product: rows of K values (4 KiB for K = 2048) that all begin at once meet in the
+  // same memory channels (128 experts of 1536 x 2048 with 64 rows each: 200 -> 161 us; the rows' gradient reads whole memory rows).
+  bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, red, lds, acc, GRAD ? 0 : (slot & 0xffff) * 7);
   uint8_t* out = (uint8_t*)a.out + (size_t)row0 * cols * (BF16 ? 2 : 4);
   store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, lane);
 }
@@ -215,6 +223,8 @@ __global__ __launch_bounds__(256) void wgrad_few_kernel(WgradArgs a) {
   join_waves<C, BF16, ADD>(acc, (uint8_t*)a.dw + ((size_t)e * a.N + m0) * a.K * (BF16 ? 2 : 4), a.K, ro.rows, n0, a.K, lds);
 }
 
+constexpr long long kMostItems = (1LL << 31) - (1 << 16);  // counted in an int, with a launch's blocks added
+
 template <int ROWS, bool GRAD, bool BF16>
 hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   static LaunchCache cache;
@@ -235,7 +245,7 @@ hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
   LaunchFacts f;
   const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
   const long long ntn = (cols + 255) / 256, tiles = std::min<long long>(P, (P + 255) / 256 + E) * ntn;
-  if ((P / 256 + 2LL) * (E / 2 + 1) * ntn >= 1LL << 31) return hipErrorNotSupported;
+  if ((P / 256 + 2LL) * (E / 2 + 1) * ntn >= kMostItems) return hipErrorNotSupported;
   const size_t lds = tile_lds(E) + group_lds_bytes(E);
   hipError_t e = cache.get((const void*)grouped_tile_kernel<GRAD, BF16>, 512, lds, &f);
   if (e != hipSuccess) return e;
@@ -309,7 +319,7 @@ int choose(const GroupedArgs& a) {
 template <bool GRAD, bool BF16>
 hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
   // tiles of all groups in an int whatever the table holds: one that does not ascend can give all rows to every second expert
-  if ((a.g.P / 16 + 2LL) * (a.g.E / 2 + 1) * (((GRAD ? a.K : a.N) + 63) / 64) >= 1LL << 31) return launch_tiles<GRAD, BF16>(a, s);
+  if ((a.g.P / 16 + 2LL) * (a.g.E / 2 + 1) * (((GRAD ? a.K : a.N) + 63) / 64) >= kMostItems) return launch_tiles<GRAD, BF16>(a, s);
   switch (choose<GRAD>(a)) {
     case 16: return launch_few<16, GRAD, BF16>(a, s);
     case 64: return launch_few<64, GRAD, BF16>(a, s);
@@ -323,7 +333,7 @@ hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
 // 16 experts of 1024 x 512 with 512 rows 21.9 / 43.6.
 bool wgrad_few(const WgradArgs& a) {
   const double stages = std::ceil((double)a.g.P / a.g.E / 64), blocks = (double)((a.N + 63) / 64) * ((a.K + 63) / 64) * a.g.E;
-  return std::ceil(blocks / 256) * (5 + stages / 4 * 1.1) < std::ceil(wgrad_tiles(a.N, a.K, a.g.E) / 256.0) * (4 + stages * 1.4);
+  return blocks < 1 << 24 && std::ceil(blocks / 256) * (5 + stages / 4 * 1.1) < std::ceil(wgrad_tiles(a.N, a.K, a.g.E) / 256.0) * (4 + stages * 1.4);
 }
 
 template <bool BF16, bool ADD>
@@ -341,8 +351,7 @@ hipError_t launch_grouped(int kind, const GroupedArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, hipStream_t s) {
-  // a launch counts its threads in 32 bits
-  if (wgrad_tiles(a.N, a.K, a.g.E) >= 1 << 23) return hipErrorNotSupported;
+  if (wgrad_tiles(a.N, a.K, a.g.E) >= kMostItems) return hipErrorNotSupported;
   if (a.out_bf16) return launch_wgrad_as<true, false>(a, s);
   return a.add ? launch_wgrad_as<false, true>(a, s) : launch_wgrad_as<false, false>(a, s);
 }

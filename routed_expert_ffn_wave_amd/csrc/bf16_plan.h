@@ -36,7 +36,7 @@ __device__ __forceinline__ bool group_of(const RowGroups& s, int e, int& slot, i
 }
 
 // Classes of experts with more than 2048, 1024, ... 64 rows, and the rest; `tiles` of each.
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(RowGroups s, int tiles, Plan* plan) {
+static __global__ __launch_bounds__(kPlanThreads) void plan_kernel(RowGroups s, int tiles, Plan* plan) {
   constexpr int W = kPlanThreads / 64;
   __shared__ int s_parts[kClasses][W + 1];
   const int e = threadIdx.x, lane = e & 63, wv = e >> 6;

@@ -1,9 +1,9 @@
 // Tiles of the bf16 products by expert: BM x BN results of out[i][j] = sum over the reduction of R[i][.] C[j][.], in
-// stages of 64 steps.  An operand is DIRECT when its reduction is contiguous in memory (activation rows; the matrix of a
+// stages of BK (64 or 32) steps.  An operand is DIRECT when its reduction is contiguous in memory (activation rows; the matrix of a
 // forward product) and ACROSS when the reduction runs over its memory rows (the matrix of a rows' gradient, both operands of a
 // matrix gradient).
 //
-// Both go through LDS, loaded there directly, 16 bytes a lane.  A DIRECT stage is rows of 128 bytes; an ACROSS stage is 64
+// Both go through LDS, loaded there directly, 16 bytes a lane.  A DIRECT stage is rows of 2 BK bytes; an ACROSS stage is BK
 // memory rows of the tile's columns, read back with the transposing LDS read (four rows by 16 columns per 16 lanes), so that
 // either way a lane gets eight consecutive reduction steps of one row or column.  Chunks are permuted by a key of the row,
 // applied to the global addresses, so that the lanes of a read touch all banks.
@@ -24,8 +24,8 @@ struct Bf16Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, BK = BK_;  // NS stages of BK steps in LDS
   // KG > 1: a block is KG groups of waves, each with the whole tile, a share of the reduction and stages of its own.
   static constexpr int KG = KG_, GW = WM * WN, NT = 64 * GW * KG;
-  static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;              // fragments of a wave
-  static constexpr int QM = BM * BK / (512 * GW), QN = BN * BK / (512 * GW);         // loads of 16 bytes a lane and stage
+  static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;                  // fragments of a wave
+  static constexpr int QM = BM * BK / (512 * GW), QN = BN * BK / (512 * GW);  // loads of 16 bytes a lane and stage
   static constexpr int PM = BM * BK * 2, STAGE = (BM + BN) * BK * 2, RING = NS * STAGE, LDS = KG * RING;  // RING: a group's stages
   static_assert(BM * BK % (512 * GW) == 0 && BN * BK % (512 * GW) == 0 && (BK == 64 || BK == 32), "load passes");
   static_assert((NS - 1) * (QM + QN) <= 63, "what the load counter holds");
@@ -47,7 +47,7 @@ template <int MODE, int B, int GW, int BK = 64>
 struct Loader {
   static constexpr int Q = B * BK / (512 * GW);
   static constexpr int CH = MODE == ACROSS ? B / 8 : BK / 8;  // chunks of a row in LDS
-  static constexpr int RP = 64 * GW / CH;                // rows of a load pass
+  static constexpr int RP = 64 * GW / CH;                     // rows of a load pass
   uint32_t off[Q];
   const uint8_t* at[MODE == GATHERED ? Q : 1];
   const uint8_t* p;
@@ -154,8 +154,14 @@ struct Reader {
 // without barriers, and groups of several have to have the same number of stages.
 //
 // One pipeline over all stages, in halves of 32 steps: while the matrix instructions of a half run from registers, the next
-// half's fragments are read from LDS into other registers.  The turn to the next stage comes before the second half, whose
-// fragments have been read by then: from there on the buffer of this stage takes the loads of the stage NS ahead.
+// half's fragments are read from LDS into other registers.  The turn to the next stage comes before the half (a stage's second, with
+// BK = 64) whose fragments have been read by then: from there on the buffer of this stage takes the loads of the stage NS
+// ahead.  rotate: the stage to begin with, where all are whole ones (modulo their number).
+//
+// A wave's 128 x 64 results read 24 KB of LDS per 64 steps for 64 matrix instructions of 16 cycles; eight waves of a 256 x 256 tile
+// and its loads need 2048 cycles of LDS at 128 bytes a cycle, and its matrix instructions 2048.  Four waves of 128 x 128 read a
+// third less, but took 40 % longer (1026 against 714 us for 16384 rows, 7168 -> 4096: one wave a SIMD waits for every read and
+// barrier, and 512 registers did not hold it).
 template <class C, int RMODE, int CMODE>
 __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, int red, uint8_t* lds, f32x4 (&acc)[C::MF][C::NF],
                                           int rotate = 0) {

@@ -108,6 +108,7 @@ def test_lora_refusals():
     assert need >= 300 * 72 * 4
     err(lora(T=300, r=72, nb=need - 1), ft.FT_E_WORKSPACE, "workspace of")
     err(lora(T=1 << 24), ft.FT_E_UNSUPPORTED, "T too large")
+    err(lora(T=(1 << 24) - 1, N=1 << 20, E=1024, n=1024), ft.FT_E_UNSUPPORTED, "T too large")
     assert lora(T=0, base=None, x=None, a=None, b=None, off=None, ga=None, out=None, ws=None, nb=0) == ft.FT_OK
     for bad in ((0, 8, 72, 64, 64), (300, 0, 72, 64, 64), (300, 1025, 72, 64, 64), (300, 8, 0, 64, 64), (300, 8, 264, 64, 64),
                 (300, 8, 72, 0, 64), (300, 8, 72, 64, 0), (1 << 24, 8, 72, 64, 64)):
