@@ -52,6 +52,10 @@ __device__ __forceinline__ Chunk chunk_of(const GroupList& gl, int ch) {
 __device__ __forceinline__ bf16x8 load8(const uint16_t* p, bool in) {
   return in ? *(const bf16x8*)p : __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
 }
+// The second term of v, whose first is h: nothing beside an infinity (whose own rest would be a NaN) or a NaN.
+__device__ __forceinline__ uint16_t second_term(float v, uint16_t h) {
+  return (h & 0x7f80) == 0x7f80 ? 0 : f32_to_bf16_bits(v - bf16_bits_to_f32(h));
+}
 // four bf16 values plus four fp32, rounded
 __device__ __forceinline__ u32x2 pack_sum(u32x2 base, f32x4 v) {
   u32x2 o;
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
         }
         const uint16_t h = f32_to_bf16_bits(v);
         s_hi[row * C::PITCH + j] = h;
-        s_lo[row * C::PITCH + j] = f32_to_bf16_bits(v - bf16_bits_to_f32(h));
+        s_lo[row * C::PITCH + j] = second_term(v, h);
       }
       __syncthreads();
 #pragma unroll
@@ -279,7 +283,7 @@ __global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int spl
           for (int q = 0; q < 2; ++q) {
             const uint16_t h0 = f32_to_bf16_bits(h[2 * q]), h1 = f32_to_bf16_bits(h[2 * q + 1]);
             hi[q] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-            lo[q] = (uint32_t)f32_to_bf16_bits(h[2 * q] - bf16_bits_to_f32(h0)) | ((uint32_t)f32_to_bf16_bits(h[2 * q + 1] - bf16_bits_to_f32(h1)) << 16);
+            lo[q] = (uint32_t)second_term(h[2 * q], h0) | ((uint32_t)second_term(h[2 * q + 1], h1) << 16);
           }
           uint8_t* to = smem + row * 128 + ((tid % 16 / 2 ^ Loader<DIRECT, ER, 4>::key(row)) << 4) + (tid & 1) * 8;
           *(u32x2*)to = hi;

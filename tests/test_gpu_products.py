@@ -319,6 +319,25 @@ def test_adapters_special_values_stay_in_their_rows():
     assert torch.isinf(out).sum() == 1 and out[9, 5] == float("inf")
 
 
+@pytest.mark.parametrize("T, r, K", [(40, 8, 136), (40, 56, 136), (900, 40, 520)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adapters_of_infinite_rows(T, r, K, dtype):
+    """An infinite hidden sum times positive values is infinite, not a NaN; other rows are what they are without it."""
+    g = gen(T + r)
+    E, N = 3, 72
+    off, gather = adapter_rows(g, T, E, 0.0)
+    base = torch.randn(T, N, generator=g).to(dtype)
+    x, a, b = normal(g, T, K), normal(g, E, r, K, scale=0.1), normal(g, E, N, r)
+    a[:, :, 3], b = a[:, :, 3].abs() + 0.5, b.abs() + 0.5
+    plain = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)]).cpu()
+    x[7, 3], x[9, 3] = float("inf"), -float("inf")
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)]).cpu()
+    assert (out[7] == float("inf")).all() and (out[9] == -float("inf")).all()
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[[7, 9]] = False
+    assert same_bits(out[rest], plain[rest])
+
+
 # ---------------------------------------------------------------------------------------------- together
 
 def layer_case(seed, T, E, k, d, I, held):
