@@ -173,7 +173,7 @@ class Bf16MoELayer:
     here for a fixed (T, k): forward() and backward() allocate nothing and can be captured into a graph.  backward()
     returns the gradients of x, of the logits and, by expert, of w13 and w2 (fp32; zeros for an expert without rows,
     nothing for one without a slot); add=True adds the latter two to what the buffers hold.  It takes what the last
-    forward() left in the buffers, and x, which the caller keeps unchanged until then.  One step at a time; streams as
+    forward() left in the buffers and refuses to run before one.  One step at a time; streams as
     in Fp8MoELayer."""
 
     def __init__(self, w13, w2, slot_of_expert=None, k: int = 1, T: int = 1, out_bf16: bool = False):
@@ -211,6 +211,7 @@ class Bf16MoELayer:
                          self.dw2, self.grad_ws)
         if P == 0:
             self.offsets.zero_()  # no forward() does
+        self._ran = P == 0
         # The buffers are memory of the stream that is current here, whose work on tensors freed before may still run.
         self._streams = {_raw_stream(dev)}
         with torch.cuda.device(dev):
@@ -235,6 +236,7 @@ class Bf16MoELayer:
         pl = _take(logits, "logits", (_F32,), (T, E), dev)
         if T == 0:
             return self.out, self.mask[:0]
+        self._ran = True
         inv = self.inv[: T * k].view(T, k)
         pi, pw, pv, pt = self.ids.data_ptr(), self.w.data_ptr(), inv.data_ptr(), slot.data_ptr()
         _run(lib.ft_moe_route, dev, stream, pl, T, E, k, pi, pw)
@@ -254,6 +256,8 @@ class Bf16MoELayer:
         T, slot, off, n = self.T, self.slot_of, self.offsets, self.n_slots
         self._on(stream)
         _take(dout, "dout", _FLOATS, (T, self.d), self.dev)
+        if not self._ran:
+            _refuse("backward() needs a forward() before it")
         if T == 0:
             inv = None
         else:

@@ -455,6 +455,16 @@ def capture(fn):
     return graph, out
 
 
+def test_layer_refuses_backward_before_forward():
+    g = gen(15)
+    layer = ft.Bf16MoELayer(normal(g, 4, 32, 64).cuda(), normal(g, 4, 64, 16).cuda(), k=2, T=9)
+    dout = normal(g, 9, 64).cuda()
+    with pytest.raises(ft.FtError, match="needs a forward"):
+        layer.backward(dout)
+    layer.forward(torch.randn(9, 4, generator=g).cuda(), normal(g, 9, 64).cuda())
+    assert all(torch.isfinite(t).all() for t in layer.backward(dout))
+
+
 @pytest.mark.parametrize("T", [3, 700])
 def test_graph_replays_match_eager_calls(T):
     """A captured training step and a captured adapter call, replayed with other inputs and eager work in between."""
