@@ -72,7 +72,7 @@ __device__ __forceinline__ u32x2 pack_sum(u32x2 base, f32x4 v) {
 template <int RF>
 struct SmallCfg {
   static constexpr int SW = RF == 4 ? 4 : 8, NF = 16 / SW;
-  using Tile = Bf16Cfg<16, 16 * RF, 1, 1, RF == 2 ? 2 : 3, SW>;
+  using Tile = Bf16Cfg<16, 16 * RF, 1, 1, RF == 4 ? 3 : 2, SW>;  // RF 1: two blocks a compute unit
   static constexpr int KS = (RF + 1) / 2, PITCH = KS * 32 + 8;  // the second product's steps of 32
 };
 
@@ -87,7 +87,9 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int ntn = (a.N + 255) / 256, stages = (a.K + 63) / 64;
-  for (int it = blockIdx.x; it < chunks * ntn; it += gridDim.x) {
+  // Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the items, whose columns share x and A.
+  const int xcd = blockIdx.x % 8, end = (int)((long long)chunks * ntn * (xcd + 1) / 8);  // gridDim.x % 8 == 0
+  for (int it = (int)((long long)chunks * ntn * xcd / 8) + blockIdx.x / 8; it < end; it += gridDim.x / 8) {
     const Chunk c = chunk_of<16>(gl, it / ntn);
     const int n0 = it % ntn * 256 + wv * 16 * C::NF;
     const int t = r < c.rows ? a.gather[c.p0 + r] : -1;
@@ -335,7 +337,7 @@ hipError_t launch_small(const LoraArgs& a, hipStream_t s) {
   const size_t lds = SmallCfg<RF>::Tile::LDS + list_lds(a.g.E);
   hipError_t e = cache.get((const void*)lora_small_kernel<RF, BF16>, SmallCfg<RF>::Tile::NT, lds, &f);
   if (e != hipSuccess) return e;
-  const long long items = chunks(a.g.P, a.g.E + 1, 16) * ((a.N + 255) / 256), most = (long long)f.per_cu * f.cus;
+  const long long items = (chunks(a.g.P, a.g.E + 1, 16) * ((a.N + 255) / 256) + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
   hipLaunchKernelGGL((lora_small_kernel<RF, BF16>), dim3((uint32_t)(items < most ? items : most)), dim3(SmallCfg<RF>::Tile::NT), lds, s, a, a.base != a.out);
   return hipGetLastError();
 }
@@ -364,13 +366,16 @@ hipError_t launch_expand(const LoraArgs& a, int splits, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Few rows: every 256 columns' block reads its rows of x and A itself.  Blocks run in rounds of the 256 compute units, each
-// about 4.5 us and 10 us for a megabyte of x and A; two kernels take 11 - 14 us for as many rows.  Measured, us, small /
-// large: 16 rows of 16 adapters, r = 16, 2048 -> 4096: 6.2 / 11.1; 256 rows of 16: 10.0 / 11.8; 512 rows: 15.4 / 13.4; 64 rows of 64,
-// 4096 -> 4096: 17.9 / 17.0; 16 rows of 16, r = 64, 2048 -> 4096: 9.4 / 11.4; 7168 -> 4096: 19.2 / 13.6.
+// One kernel or two, by times modelled in us.  In the one every 256 columns' block reads its rows of x and A itself, which is what it
+// takes past 4.5 us: blocks of an adapter run on one XCD, and share the 256 compute units' loads where there are more blocks than
+// units, and in turn where one unit holds no more (two, with r > 16 one).  Measured, us, one kernel / two: 16 rows of 16 adapters, r = 16, 2048 -> 4096: 5.9 / 10.9; 32 rows of 32: 7.4 / 11.9; 256 rows of
+// 16: 8.4 / 11.5; 512 rows: 11.3 / 13.2; 1024 rows: 17.8 / 15.5; 131 rows of 40, r = 8, 7168 -> 2048: 12.7 / 14.3; 64 rows of 64, r = 16, 4096 -> 4096:
+// 12.5 / 14.7; 512 rows of 16: 15.5 / 13.8; 3000 rows of 7, 776 -> 520, r = 16: 8.8 / 13.5, r = 64: 18.8 / 18.3; 16 rows of 16, r = 64, 2048 -> 4096: 9.0 / 11.2, 7168 -> 4096: 14.7 / 14.4.
 bool lora_small(int T, int E, int r, int N, int K) {
-  const long long rounds = (chunks(T, E + 1, 16) * ((N + 255) / 256) + 255) / 256;
-  return r <= 64 && rounds * (4.5 + 20e-6 * (r + 16) * K) <= 12;
+  const double ntn = (N + 255) / 256, blocks = chunks(T, E + 1, 16) * ntn, rows = std::min(16.0, std::max(1.0, (double)T / E));
+  const double one = 4.5 + std::max(0.6, blocks / 256) * 38e-6 * (std::max(16, r) + rows) * K + std::max(0.0, r <= 16 ? blocks / 512 - 1 : 5 * (blocks / 256 - 1)) * 0.8;
+  const double two = 9 + 0.4e-3 * K + 0.5e-3 * T + 0.0055 * chunks(T, E + 1, 32) * ntn;
+  return r <= 64 && one < two;
 }
 
 }  // namespace
