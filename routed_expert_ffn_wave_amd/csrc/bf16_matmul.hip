@@ -29,10 +29,15 @@ __device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, in
       s.E, g, tmp, [&](int e, int& slot, int& row0, int& cnt) { return e < s.E && group_of(s, e, slot, row0, cnt) && cnt > 0; }, items_of);
 }
 
+constexpr int kTileLds = 160 * 1024;  // all of a compute unit's
+static_assert(group_lds_bytes(1024) <= kTileLds, "LDS");
+
 // A tile of up to BM rows takes the least of these heights that holds its rows.
 template <int BM, bool GRAD, bool BF16>
 __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
-  using C = Bf16Cfg<BM, 256, 2, 4, BM <= 128 ? 3 : 2>;
+  constexpr int NS = BM <= 64 && !GRAD ? 4 : BM <= 128 ? 3 : 2;
+  using C = Bf16Cfg<BM, 256, 2, 4, NS, 1, 64, NS == 2 ? 3 : NS>;
+  static_assert(C::LDS <= kTileLds, "LDS");
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
@@ -46,27 +51,31 @@ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int
   store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, lane);
 }
 
-// LDS of the tiles: 128 rows have three stages where the table of experts leaves room for them (7 % faster there: 128 experts of
-// 1536 x 2048 with 128 rows each, 188 -> 177 us).
-constexpr int kThreeStages = 1000;  // experts, at most
-__host__ __device__ constexpr int tile_lds(int E) { return E <= kThreeStages ? 3 * (128 + 256) * 128 : 2 * (256 + 256) * 128; }
-static_assert(tile_lds(kThreeStages) + group_lds_bytes(kThreeStages) <= 160 * 1024 && tile_lds(1024) + group_lds_bytes(1024) <= 160 * 1024, "LDS");
-
 // Tile `local` of `rows` rows: bands of 4 row tiles, column tiles within a band in turn.
 template <bool GRAD, bool BF16>
 __device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int row0, int cnt, int local, uint8_t* lds) {
   constexpr int BAND = 4;
   const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
-  const int band = local / (BAND * ntn), h = min(BAND, (cnt + 255) / 256 - band * BAND), in = local - band * BAND * ntn;
-  const int m0 = (band * BAND + in % h) * 256, n0 = in / h * 256, rows = min(256, cnt - m0);
-  if (rows > 192)
-    grouped_tile<256, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
-  else if (rows > 128 || (rows > 64 && a.g.E > kThreeStages))
-    grouped_tile<192, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+  const int ntm = (cnt + 255) / 256, each = ((cnt + ntm - 1) / ntm + 31) / 32 * 32;
+  const int band = local / (BAND * ntn), h = min(BAND, ntm - band * BAND), in = local - band * BAND * ntn;
+  const int m0 = (band * BAND + in % h) * each, n0 = in / h * 256, rows = min(each, cnt - m0);
+  auto tile = [&](auto height) { grouped_tile<decltype(height)::value, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds); };
+  if (rows > 224)
+    tile(std::integral_constant<int, 256>{});
+  else if (rows > 192)
+    tile(std::integral_constant<int, 224>{});
+  else if (rows > 160)
+    tile(std::integral_constant<int, 192>{});
+  else if (rows > 128)
+    tile(std::integral_constant<int, 160>{});
+  else if (rows > 96)
+    tile(std::integral_constant<int, 128>{});
   else if (rows > 64)
-    grouped_tile<128, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+    tile(std::integral_constant<int, 96>{});
+  else if (rows > 32)
+    tile(std::integral_constant<int, 64>{});
   else
-    grouped_tile<64, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
+    tile(std::integral_constant<int, 32>{});
 }
 
 // Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the tile list, so that tiles that run
@@ -77,18 +86,29 @@ template <bool GRAD, bool BF16>
 __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
-  const int E2 = a.g.E + 2;
-  int* li = (int*)(lds + tile_lds(a.g.E));
-  GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
-  list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + 255) / 256 * ntn; });
-  const int nitems = gl.item0[gl.n];
-  const int per = gridDim.x / 8, x = blockIdx.x % 8, j = blockIdx.x / 8;  // gridDim.x % 8 == 0
-  // (Rounds are turned against each other: heights repeat along the list, and a block must not meet the same one always.)
-  for (int round = 0, it; (it = round * (int)gridDim.x + x * per + (j + 7 * round) % per) < nitems || round * (int)gridDim.x < nitems; ++round) {
-    if (it >= nitems) continue;
-    const int gi = find_group(gl.item0, gl.n, it);
-    grouped_item<GRAD, BF16>(a, __builtin_amdgcn_readfirstlane(gl.slot[gi]), __builtin_amdgcn_readfirstlane(gl.row0[gi]),
-                             __builtin_amdgcn_readfirstlane(gl.cnt[gi]), __builtin_amdgcn_readfirstlane(it - gl.item0[gi]), lds);
+  const int per = gridDim.x / 8, x = blockIdx.x % 8, j = blockIdx.x / 8, lane = threadIdx.x & 63;  // gridDim.x % 8 == 0
+  // The list lies where the stages will: every wave keeps what it says of this block's next 16 tiles, lanes 4 i .. 4 i + 3 tile i.
+  for (int first = 0;; first += 16) {
+    const int E2 = a.g.E + 2;
+    int* li = (int*)lds;
+    GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
+    list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + 255) / 256 * ntn; });
+    const int nitems = gl.item0[gl.n], rounds = (nitems + (int)gridDim.x - 1) / (int)gridDim.x;
+    // (Rounds are turned against each other: heights repeat along the list, and a block must not meet the same one always.)
+    const int mine = first + lane / 4, it = mine * (int)gridDim.x + x * per + (j + 7 * mine) % per;
+    int word = 0;  // its slot, first row, rows, and number in the group
+    if (it < nitems) {
+      const int gi = find_group(gl.item0, gl.n, it);
+      word = lane % 4 == 3 ? it - gl.item0[gi] : (lane % 4 == 0 ? gl.slot : lane % 4 == 1 ? gl.row0 : gl.cnt)[gi];
+    }
+    __syncthreads();
+    for (int r = 0; r < 16; ++r) {
+      if (first + r >= rounds) return;
+      const int rows = __builtin_amdgcn_readlane(word, 4 * r + 2);
+      if (rows > 0)
+        grouped_item<GRAD, BF16>(a, __builtin_amdgcn_readlane(word, 4 * r), __builtin_amdgcn_readlane(word, 4 * r + 1), rows,
+                                 __builtin_amdgcn_readlane(word, 4 * r + 3), lds);
+    }
   }
 }
 
@@ -246,7 +266,7 @@ hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
   const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
   const long long ntn = (cols + 255) / 256, tiles = std::min<long long>(P, (P + 255) / 256 + E) * ntn;
   if ((P / 256 + 2LL) * (E / 2 + 1) * ntn >= kMostItems) return hipErrorNotSupported;
-  const size_t lds = tile_lds(E) + group_lds_bytes(E);
+  const size_t lds = kTileLds;
   hipError_t e = cache.get((const void*)grouped_tile_kernel<GRAD, BF16>, 512, lds, &f);
   if (e != hipSuccess) return e;
   const long long upper = (tiles + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;

@@ -19,16 +19,19 @@ __device__ __forceinline__ void dma16_at(const uint8_t* from, uint32_t lds) {
   asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds), "i"(AT) : "memory", "scc");
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1, int BK_ = 64>
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1, int BK_ = 64, int NSC_ = NS_>
 struct Bf16Cfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, BK = BK_;  // NS stages of BK steps in LDS
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_;
+  static constexpr int NS = NS_, NSC = NSC_;  // stages of BK steps in LDS, of the rows and of the columns
   // KG > 1: a block is KG groups of waves, each with the whole tile, a share of the reduction and stages of its own.
   static constexpr int KG = KG_, GW = WM * WN, NT = 64 * GW * KG;
-  static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;                  // fragments of a wave
-  static constexpr int QM = BM * BK / (512 * GW), QN = BN * BK / (512 * GW);  // loads of 16 bytes a lane and stage
-  static constexpr int PM = BM * BK * 2, STAGE = (BM + BN) * BK * 2, RING = NS * STAGE, LDS = KG * RING;  // RING: a group's stages
-  static_assert(BM * BK % (512 * GW) == 0 && BN * BK % (512 * GW) == 0 && (BK == 64 || BK == 32), "load passes");
-  static_assert((NS - 1) * (QM + QN) <= 63, "what the load counter holds");
+  static constexpr int MF = BM / WM / 16, NF = BN / WN / 16;  // fragments of a wave
+  // Loads of 16 bytes a lane and stage, whole passes of all lanes: rows past BM are loaded but not read.
+  static constexpr int QM = (BM * BK + 512 * GW - 1) / (512 * GW), QN = BN * BK / (512 * GW), LM = QM * 512 * GW / BK;
+  static constexpr int PM = LM * BK * 2, PN = BN * BK * 2, RING = NS * PM + NSC * PN, LDS = KG * RING;  // RING: a group's stages
+  static_assert(BM % (16 * WM) == 0 && BN * BK % (512 * GW) == 0 && (BK == 64 || BK == 32), "fragments, load passes");
+  static_assert(NSC == NS || (NSC == NS + 1 && BK == 64), "what the waits count");
+  static_assert((NS - 1) * QM + (NSC - 1) * QN <= 63, "what the load counter holds");
 };
 
 enum { DIRECT = 0, ACROSS = 1, GATHERED = 2 };  // GATHERED: DIRECT rows named by a table
@@ -155,8 +158,13 @@ struct Reader {
 //
 // One pipeline over all stages, in halves of 32 steps: while the matrix instructions of a half run from registers, the next
 // half's fragments are read from LDS into other registers.  The turn to the next stage comes before the half (a stage's second, with
-// BK = 64) whose fragments have been read by then: from there on the buffer of this stage takes the loads of the stage NS
-// ahead.  rotate: the stage to begin with, where all are whole ones (modulo their number).
+// BK = 64) whose fragments have been read by then: from there on the buffers of this stage take the rows of the stage NS ahead and
+// the columns of the one NSC ahead.  rotate: the stage to begin with, where all are whole ones (modulo their number).
+//
+// Columns are an expert's matrix, most of which comes from far memory, rows are shared by the tiles beside this one: with 256 rows
+// all of the LDS holds two stages of rows and three of columns.  (Three of columns against two: 128 experts of 1536 x 2112 with 256
+// rows each 231 -> 210 us, 16384 rows, 7168 -> 4096, 698 -> 687 us.  A touch of the lines of later stages instead, to have them in L2 in
+// time, took 15 - 30 % longer: L2 holds little more than the stages that its 32 compute units have under way.)
 //
 // A wave's 128 x 64 results read 24 KB of LDS per 64 steps for 64 matrix instructions of 16 cycles; eight waves of a 256 x 256 tile
 // and its loads need 2048 cycles of LDS at 128 bytes a cycle, and its matrix instructions 2048.  Four waves of 128 x 128 read a
@@ -165,8 +173,10 @@ struct Reader {
 template <class C, int RMODE, int CMODE>
 __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, int red, uint8_t* lds, f32x4 (&acc)[C::MF][C::NF],
                                           int rotate = 0) {
-  constexpr int MF = C::MF, NF = C::NF, NS = C::NS, U = C::QM + C::QN;
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % C::GW, tid = wv * 64 + lane;
+  constexpr int MF = C::MF, NF = C::NF, NS = C::NS, NSC = C::NSC, U = C::QM + C::QN;
+  int thread = threadIdx.x;
+  asm volatile("" : "+v"(thread));  // laundered: addresses are formed here, not kept from one tile of a block to the next
+  const int lane = thread & 63, wv = __builtin_amdgcn_readfirstlane(thread >> 6) % C::GW, tid = wv * 64 + lane;
   const int wm = wv / C::WN, wn = wv % C::WN;
 #pragma unroll
   for (int m = 0; m < MF; ++m)
@@ -174,141 +184,192 @@ __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, 
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
   if (red <= 0) return;
   const int nb = (red + C::BK - 1) / C::BK, left = red % C::BK;  // stages; the last has `left` steps if that is not 0
-  Loader<RMODE, C::BM, C::GW, C::BK> lr;
+  Loader<RMODE, C::LM, C::GW, C::BK> lr;
   Loader<CMODE, C::BN, C::GW, C::BK> lc;
   lr.open(ro, tid, red);
   lc.open(co, tid, red);
-  Reader<RMODE, C::BM, MF, C::BK> rr;
+  Reader<RMODE, C::LM, MF, C::BK> rr;
   Reader<CMODE, C::BN, NF, C::BK> rc;
   rr.open(wm * 16 * MF, lane);
   rc.open(wn * 16 * NF, lane);
   const uint32_t lds0 = lds_addr(lds) + wv * 1024;
-  int fill = 0, wrap = 0;  // stages loaded; the one after which the first follows (0: none)
+  int wrap = 0;  // the number of stages after which the first follows (0: none)
   if (rotate > 0 && left == 0) {
     const int first = rotate % nb;
     wrap = first ? nb - first : 0;
     lr.skip(first);
     lc.skip(first);
   }
-  uint32_t fill_lds = lds0;
-  auto open = [&] {
-    if (fill == nb - 1 && left && fill > 0) {
+  int fill_r = 0, fill_c = 0;  // stages loaded
+  // As many stages of both: rows and columns side by side, one pointer; otherwise all rows, then all columns.
+  constexpr bool SAME = NSC == NS;
+  constexpr int SR = SAME ? C::PM + C::PN : C::PM;
+  uint32_t to_r = lds0, to_c = lds0 + NS * C::PM;
+  // Before the loads of a stage, once each: the last may be a short one.
+  auto open_r = [&] {
+    if (fill_r == nb - 1 && left && fill_r > 0) {
       lr.shorten(ro, tid, left);
-      lc.shorten(co, tid, left);
+      if (SAME) lc.shorten(co, tid, left);
     }
+  };
+  auto open_c = [&] {
+    if (!SAME && fill_c == nb - 1 && left && fill_c > 0) lc.shorten(co, tid, left);
   };
   auto issue_unit = [&](auto u_) {
     constexpr int u = decltype(u_)::value;
     if constexpr (u < C::QM)
-      lr.template issue<u, 0>(fill_lds);
+      lr.template issue<u, 0>(to_r);
     else
-      lc.template issue<u - C::QM, C::PM>(fill_lds);
+      lc.template issue<u - C::QM, SAME ? C::PM : 0>(SAME ? to_r : to_c);
+  };
+  auto advance_r = [&] {
+    lr.advance();
+    if (++fill_r == wrap) lr.skip(-nb);
+    to_r = to_r + SR >= lds0 + NS * SR ? lds0 : to_r + SR;
+  };
+  auto advance_c = [&] {
+    lc.advance();
+    if (++fill_c == wrap) lc.skip(-nb);
+    to_c = to_c + C::PN >= lds0 + C::RING ? lds0 + NS * C::PM : to_c + C::PN;
   };
   auto advance = [&] {
-    ++fill;
-    lr.advance();
-    lc.advance();
-    if (fill == wrap) lr.skip(-nb), lc.skip(-nb);
-    fill_lds = fill_lds + C::STAGE >= lds0 + C::RING ? lds0 : fill_lds + C::STAGE;
+    if constexpr (SAME) {
+      ++fill_r;
+      lr.advance();
+      lc.advance();
+      if (fill_r == wrap) lr.skip(-nb), lc.skip(-nb);
+      to_r = to_r + SR >= lds0 + NS * SR ? lds0 : to_r + SR;
+    } else {
+      advance_r(), advance_c();
+    }
   };
   auto meet = [] {
     if constexpr (C::GW > 1) asm volatile("s_barrier" ::: "memory");
   };
-  auto clear = [&](uint8_t* st) {
-    Loader<RMODE, C::BM, C::GW, C::BK>::clear(st, tid, left);
-    Loader<CMODE, C::BN, C::GW, C::BK>::clear(st + C::PM, tid, left);
+  uint8_t *sr = lds, *sc = lds + NS * C::PM;  // this stage
+  auto cols = [&] { return SAME ? sr + C::PM : sc; };
+  auto next_stage = [&] {
+    sr = sr + SR >= lds + NS * SR ? lds : sr + SR;
+    if (!SAME) sc = sc + C::PN >= lds + C::RING ? lds + NS * C::PM : sc + C::PN;
+  };
+  auto clear = [&] {
+    Loader<RMODE, C::LM, C::GW, C::BK>::clear(sr, tid, left);
+    Loader<CMODE, C::BN, C::GW, C::BK>::clear(cols(), tid, left);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     meet();
   };
   bf16x8 f0[NF + MF], f1[NF + MF];  // the fragments of a half: columns, then rows
-  uint8_t* st = lds;
-  auto frag = [&](const uint8_t* from, auto half, int n) {
+  auto frag = [&](auto half, int n) {
     constexpr int H = decltype(half)::value;
-    return n < NF ? rc.template read<H>(from + C::PM, n) : rr.template read<H>(from, n - NF);
+    return n < NF ? rc.template read<H>(cols(), n) : rr.template read<H>(sr, n - NF);
   };
   using Half0 = std::integral_constant<int, 0>;
   using Half1 = std::integral_constant<int, 1>;
   // Slots between a half's MM matrix instructions: fragment reads in the first three quarters, loads in the first half.
   constexpr int MM = MF * NF, RD = MF + NF, RS = MM - MM / 4, US = MM / 2 > 0 ? MM / 2 : 1;
-  auto half = [&](bf16x8(&now)[NF + MF], bf16x8(&next)[NF + MF], const uint8_t* from, auto h, auto loads) {
+  auto half = [&](bf16x8(&now)[NF + MF], bf16x8(&next)[NF + MF], auto h, auto loads) {
     unrolled<0, MM>([&](auto slot) {
       constexpr int i = decltype(slot)::value, m = i / NF, f = i % NF;
       acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now[f], now[NF + m], acc[m][f], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
-      // reads n with n RS / RD == i, loads u with u US / U == i
+      // reads n with n RS / RD == i, loads u with u US / L == i
       unrolled<(i * RD + RS - 1) / RS, (i + 1) * RD <= RS * RD ? ((i + 1) * RD + RS - 1) / RS : (i * RD + RS - 1) / RS>([&](auto n) {
-        if constexpr (decltype(n)::value < RD) next[decltype(n)::value] = frag(from, h, decltype(n)::value);
+        if constexpr (decltype(n)::value < RD) next[decltype(n)::value] = frag(h, decltype(n)::value);
       });
-      if constexpr (decltype(loads)::value && i < US) unrolled<(i * U + US - 1) / US, ((i + 1) * U + US - 1) / US>(issue_unit);
+      constexpr int L = decltype(loads)::value;
+      if constexpr (L > 0 && i < US) unrolled<(i * L + US - 1) / US, ((i + 1) * L + US - 1) / US>(issue_unit);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  auto after = [&](uint8_t* s) { return s + C::STAGE >= lds + C::RING ? lds : s + C::STAGE; };
+  using None = std::integral_constant<int, 0>;
+  using Rows = std::integral_constant<int, C::QM>;
+  using Both = std::integral_constant<int, U>;
 
-  while (fill < min(NS, nb)) {
-    open();
-    unrolled<0, U>(issue_unit);
-    advance();
+  if constexpr (SAME) {
+    while (fill_r < min(NS, nb)) {
+      open_r();
+      unrolled<0, U>(issue_unit);
+      advance();
+    }
+  } else {
+    while (fill_c < min(NSC, nb)) {
+      const bool rows = fill_c < NS;
+      if (rows) {
+        open_r();
+        unrolled<0, C::QM>(issue_unit);
+      }
+      open_c();
+      unrolled<C::QM, U>(issue_unit);
+      advance_c();
+      if (rows) advance_r();
+    }
   }
-  if (nb >= NS)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 1) * U) : "memory");
+  if (nb >= NSC)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 1) * C::QM + (NSC - 1) * C::QN) : "memory");
   else
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   meet();
-  if (nb == 1 && left) clear(st);
+  if (nb == 1 && left) clear();
 #pragma unroll
-  for (int n = 0; n < NF + MF; ++n) f0[n] = frag(st, Half0{}, n);
+  for (int n = 0; n < NF + MF; ++n) f0[n] = frag(Half0{}, n);
   int b = 0;
-  // The next stage has landed for every wave, and every wave has read this one, whose buffer may be loaded again.
+  // The next stage has landed for every wave, and every wave has read this one, whose buffers may be loaded again.
   auto turn = [&] {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * U) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * C::QM + (NSC - 2) * C::QN) : "memory");
     meet();
-    open();
-    st = after(st);
+    open_r(), open_c();  // (a stage's loads follow at once; the columns have none left where only rows do)
+    next_stage();
   };
   auto last_turn = [&] {  // nothing is left to load
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     meet();
-    st = after(st);
-    if (b == nb - 2 && left) clear(st);
+    next_stage();
+    if (b == nb - 2 && left) clear();
   };
   // (Past the last stage fragments are read but unused.)
   if constexpr (C::BK == 64) {
-    for (; b < nb - NS; ++b) {
-      half(f0, f1, st, Half1{}, std::false_type{});
+    for (; b < nb - NSC; ++b) {
+      half(f0, f1, Half1{}, None{});
       turn();
-      half(f1, f0, st, Half0{}, std::true_type{});
+      half(f1, f0, Half0{}, Both{});
       advance();
     }
+    if (!SAME && b < nb - NS) {
+      half(f0, f1, Half1{}, None{});
+      turn();
+      half(f1, f0, Half0{}, Rows{});
+      advance_r();
+      ++b;
+    }
     for (; b < nb; ++b) {
-      half(f0, f1, st, Half1{}, std::false_type{});
+      half(f0, f1, Half1{}, None{});
       last_turn();
-      half(f1, f0, st, Half0{}, std::false_type{});
+      half(f1, f0, Half0{}, None{});
     }
   } else {
     for (; b < nb - NS - 1; b += 2) {
       turn();
-      half(f0, f1, st, Half0{}, std::true_type{});
+      half(f0, f1, Half0{}, Both{});
       advance();
       turn();
-      half(f1, f0, st, Half0{}, std::true_type{});
+      half(f1, f0, Half0{}, Both{});
       advance();
     }
     if (b < nb - NS) {  // an odd one: its successor is in f1
       turn();
-      half(f0, f1, st, Half0{}, std::true_type{});
+      half(f0, f1, Half0{}, Both{});
       advance();
       ++b;
       last_turn();
-      half(f1, f0, st, Half0{}, std::false_type{});
+      half(f1, f0, Half0{}, None{});
       ++b;
     }
     for (; b < nb; ++b) {
       last_turn();
-      half(f0, f1, st, Half0{}, std::false_type{});
+      half(f0, f1, Half0{}, None{});
       if (++b >= nb) break;
       last_turn();
-      half(f1, f0, st, Half0{}, std::false_type{});
+      half(f1, f0, Half0{}, None{});
     }
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

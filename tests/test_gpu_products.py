@@ -599,6 +599,16 @@ def test_tiles_of_many_experts(E, P, N, K, grad):
     check_forward(normal(g, P, N if grad else K), normal(g, E, N, K), sizes(g, E, P), None, BF, grad)
 
 
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("red", [8, 64, 72, 128, 136, 192, 200, 256, 264, 320, 328])
+def test_tiles_of_every_height_and_few_stages(red, grad):
+    """Groups of every height of a tile, whole ones and pairs, over reductions of one to six stages, whole and short."""
+    counts = torch.tensor([20, 33, 64, 65, 96, 100, 128, 130, 160, 161, 192, 200, 224, 230, 256, 257, 300, 448, 449, 512, 513, 700] * 3)
+    off = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]).int()
+    g, cols = gen(red), 1032
+    check_forward(normal(g, int(off[-1]), red), normal(g, len(counts), *((red, cols) if grad else (cols, red))), off, None, BF, grad)
+
+
 @pytest.mark.parametrize("P, N, K", [(300, 264, 520), (5000, 1032, 2056), (70000, 264, 520)])
 def test_planned_matrix_gradient(P, N, K):
     """More tiles than two a compute unit: from queues, with experts of every class of rows, some without a slot."""
