@@ -32,14 +32,17 @@ __device__ __forceinline__ void list_groups(const RowGroups& s, GroupList& g, in
 constexpr int kTileLds = 160 * 1024;  // all of a compute unit's
 static_assert(group_lds_bytes(1024) <= kTileLds, "LDS");
 
-// A tile of up to BM rows takes the least of these heights that holds its rows.
-template <int BM, bool GRAD, bool BF16>
+// Tiles of W columns: 256 by up to 256 rows, or 128 by up to 128 rows where there are few tiles.
+template <int W>
+constexpr int kTallest = W;
+
+template <int BM, int W, bool GRAD, bool BF16>
 __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
-  constexpr int NS = BM <= 64 && !GRAD ? 4 : BM <= 128 ? 3 : 2;
-  using C = Bf16Cfg<BM, 256, 2, 4, NS, 1, 64, NS == 2 ? 3 : NS>;
+  constexpr int NS = W == 128 ? (BM <= 64 ? 6 : 5) : BM <= 64 && !GRAD ? 4 : BM <= 128 ? 3 : 2;
+  using C = Bf16Cfg<BM, W, W == 128 ? 4 : 2, W == 128 ? 2 : 4, NS, 1, 64, NS == 2 ? 3 : NS>;
   static_assert(C::LDS <= kTileLds, "LDS");
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint16_t* w = a.w + (size_t)slot * a.N * a.K;
   f32x4 acc[C::MF][C::NF];
   const Operand ro{a.a + (size_t)row0 * red, red, rows, nullptr, 0};
@@ -48,19 +51,26 @@ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int
   // same memory channels (128 experts of 1536 x 2048 with 64 rows each: 200 -> 161 us; the rows' gradient reads whole memory rows).
   bf16_tile<C, DIRECT, GRAD ? ACROSS : DIRECT>(ro, co, red, lds, acc, GRAD ? 0 : (slot & 0xffff) * 7);
   uint8_t* out = (uint8_t*)a.out + (size_t)row0 * cols * (BF16 ? 2 : 4);
-  store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, lane);
+  store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, this_lane());
 }
 
-// Tile `local` of `rows` rows: bands of 4 row tiles, column tiles within a band in turn.
-template <bool GRAD, bool BF16>
+// Tile `local` of a group of cnt rows, cut into tiles of the same height: bands of 4 row tiles, column tiles within a band in turn.  A tile
+// takes the least of the heights that holds its rows.
+template <int W, bool GRAD, bool BF16>
 __device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int row0, int cnt, int local, uint8_t* lds) {
   constexpr int BAND = 4;
-  const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
-  const int ntm = (cnt + 255) / 256, each = ((cnt + ntm - 1) / ntm + 31) / 32 * 32;
+  constexpr int STEP = W == 128 ? 64 : 32;
+  const int ntn = ((GRAD ? a.K : a.N) + W - 1) / W;
+  const int ntm = (cnt + kTallest<W> - 1) / kTallest<W>, each = ((cnt + ntm - 1) / ntm + STEP - 1) / STEP * STEP;
   const int band = local / (BAND * ntn), h = min(BAND, ntm - band * BAND), in = local - band * BAND * ntn;
-  const int m0 = (band * BAND + in % h) * each, n0 = in / h * 256, rows = min(each, cnt - m0);
-  auto tile = [&](auto height) { grouped_tile<decltype(height)::value, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds); };
-  if (rows > 224)
+  const int m0 = (band * BAND + in % h) * each, n0 = in / h * W, rows = min(each, cnt - m0);
+  auto tile = [&](auto height) { grouped_tile<decltype(height)::value, W, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds); };
+  if constexpr (W == 128) {
+    if (rows > 64)
+      tile(std::integral_constant<int, 128>{});
+    else
+      tile(std::integral_constant<int, 64>{});
+  } else if (rows > 224)
     tile(std::integral_constant<int, 256>{});
   else if (rows > 192)
     tile(std::integral_constant<int, 224>{});
@@ -82,31 +92,31 @@ __device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int
 // together share rows and matrices through its L2.  (Queues with the tallest tiles first, as the matrix gradient has them,
 // were 5 % slower: one after the other, tiles bound by the matrix cores and tiles bound by memory do not fill each
 // other's gaps, and the list takes a launch of its own.)
-template <bool GRAD, bool BF16>
+template <int W, bool GRAD, bool BF16>
 __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  const int ntn = ((GRAD ? a.K : a.N) + 255) / 256;
+  const int ntn = ((GRAD ? a.K : a.N) + W - 1) / W;
   const int per = gridDim.x / 8, x = blockIdx.x % 8, j = blockIdx.x / 8, lane = threadIdx.x & 63;  // gridDim.x % 8 == 0
   // The list lies where the stages will: every wave keeps what it says of this block's next 16 tiles, lanes 4 i .. 4 i + 3 tile i.
   for (int first = 0;; first += 16) {
     const int E2 = a.g.E + 2;
     int* li = (int*)lds;
     GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
-    list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + 255) / 256 * ntn; });
-    const int nitems = gl.item0[gl.n], rounds = (nitems + (int)gridDim.x - 1) / (int)gridDim.x;
+    list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + kTallest<W> - 1) / kTallest<W> * ntn; });
+    const int nitems = gl.item0[gl.n];
     // (Rounds are turned against each other: heights repeat along the list, and a block must not meet the same one always.)
     const int mine = first + lane / 4, it = mine * (int)gridDim.x + x * per + (j + 7 * mine) % per;
-    int word = 0;  // its slot, first row, rows, and number in the group
+    int word = mine * (int)gridDim.x < nitems ? 0 : -1;  // its slot, first row, rows (0: no tile in this round, -1: nor later), and number in the group
     if (it < nitems) {
       const int gi = find_group(gl.item0, gl.n, it);
       word = lane % 4 == 3 ? it - gl.item0[gi] : (lane % 4 == 0 ? gl.slot : lane % 4 == 1 ? gl.row0 : gl.cnt)[gi];
     }
     __syncthreads();
     for (int r = 0; r < 16; ++r) {
-      if (first + r >= rounds) return;
       const int rows = __builtin_amdgcn_readlane(word, 4 * r + 2);
+      if (rows < 0) return;
       if (rows > 0)
-        grouped_item<GRAD, BF16>(a, __builtin_amdgcn_readlane(word, 4 * r), __builtin_amdgcn_readlane(word, 4 * r + 1), rows,
+        grouped_item<W, GRAD, BF16>(a, __builtin_amdgcn_readlane(word, 4 * r), __builtin_amdgcn_readlane(word, 4 * r + 1), rows,
                                  __builtin_amdgcn_readlane(word, 4 * r + 3), lds);
     }
   }
@@ -259,18 +269,17 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool GRAD, bool BF16>
+template <int W, bool GRAD, bool BF16>
 hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
   static LaunchCache cache;
   LaunchFacts f;
   const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
-  const long long ntn = (cols + 255) / 256, tiles = std::min<long long>(P, (P + 255) / 256 + E) * ntn;
-  if ((P / 256 + 2LL) * (E / 2 + 1) * ntn >= kMostItems) return hipErrorNotSupported;
-  const size_t lds = kTileLds;
-  hipError_t e = cache.get((const void*)grouped_tile_kernel<GRAD, BF16>, 512, lds, &f);
+  const long long ntn = (cols + W - 1) / W, tiles = std::min<long long>(P, (P + kTallest<W> - 1) / kTallest<W> + E) * ntn;
+  if ((P / kTallest<W> + 2LL) * (E / 2 + 1) * ntn >= kMostItems) return hipErrorNotSupported;
+  hipError_t e = cache.get((const void*)grouped_tile_kernel<W, GRAD, BF16>, 512, kTileLds, &f);
   if (e != hipSuccess) return e;
   const long long upper = (tiles + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
-  hipLaunchKernelGGL((grouped_tile_kernel<GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(512), lds, s, a);
+  hipLaunchKernelGGL((grouped_tile_kernel<W, GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(512), kTileLds, s, a);
   return hipGetLastError();
 }
 
@@ -322,6 +331,9 @@ using T256 = Bf16Cfg<256, 256, 2, 4, 4, 1, 32>;
 //   one matrix of 4096 x 4096, rows                 64  31.2 / 16.0    300  73.8 / 29.8
 // With few rows the forward product is bound by the matrices' bytes, which the smaller blocks read at 5.7 - 6.1 TB/s, the larger
 // ones at 5.3 - 5.6; in the rows' gradient, whose 64 columns are 128 bytes of a memory row, it is the other way round.
+// Tiles of 128 columns where 256 leave units without one, or a round nearly empty.  us, 256 (or 64) / 128: 256 tokens, top 2 of 8 experts of
+// 4096 x 4096 73 / 50, back 86 / 53; 300, top 4 of 16 of 2048 x 2048 32 / 25, back 33 / 27; 333, top 8 of 64, 40 here, of 2048 x 1032 56 / 49; but 128 experts
+// with 128 rows each 161 / 168, 512 tokens, top 2 of 8, 81 / 89; back 77 tokens, top 4 of 32 of 2048 x 768 19.8 / 21.0, 64, top 2 of 8, 54.6 / 51.1.
 // 16 rows a block, two blocks a unit, where 64 would leave most units without one (64 rows, 4096 x 4096: 16.0 -> 12.2).
 template <bool GRAD>
 int choose(const GroupedArgs& a) {
@@ -330,20 +342,24 @@ int choose(const GroupedArgs& a) {
   const double rows = std::max(1.0, held * a.g.P), groups = std::max(1.0, held * a.g.E * (1.0 - std::exp(-(double)a.g.P / a.g.E)));
   const double each = rows / groups, stages = (red + 63) / 64;
   auto blocks = [&](int h, int w) { return std::max(groups, rows / h + (each > h ? 0.5 : 0.0) * groups) * ((cols + w - 1) / w); };
-  const double few = std::ceil(blocks(64, 64) / 256) * (3.5 + stages / 4 * 0.8);
-  const double tiles = std::ceil(blocks(256, 256) / 256) * (3.5 + stages * (0.3 + 0.8 * std::min(each, 256.0) / 256));
-  if (few < tiles || (!GRAD && each <= 16)) return blocks(64, 64) < 100 ? 16 : 64;
-  return 256;
+  auto rounds = [&](int h, int w) { return std::ceil(blocks(h, w) / 256); };
+  const double tile = 3.5 + stages * (0.3 + 0.8 * std::min(each, 256.0) / 256);
+  const double few = rounds(64, 64) * (3.5 + stages / 4 * 0.8), wide = rounds(256, 256) * tile;
+  // (Groups of about 128 rows: many in two tiles.  A rows' gradient of few rows wants whole memory rows.)
+  const double narrow = each <= 100 && !(GRAD && each < 12) ? rounds(128, 128) * (GRAD ? 0.68 : 0.58) * tile : wide;
+  if (few < std::min(wide, narrow) || (!GRAD && each <= 16)) return blocks(64, 64) < 100 ? 16 : 64;
+  return narrow < wide ? 128 : 256;
 }
 
 template <bool GRAD, bool BF16>
 hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
   // tiles of all groups in an int whatever the table holds: one that does not ascend can give all rows to every second expert
-  if ((a.g.P / 16 + 2LL) * (a.g.E / 2 + 1) * (((GRAD ? a.K : a.N) + 63) / 64) >= kMostItems) return launch_tiles<GRAD, BF16>(a, s);
+  if ((a.g.P / 16 + 2LL) * (a.g.E / 2 + 1) * (((GRAD ? a.K : a.N) + 63) / 64) >= kMostItems) return launch_tiles<256, GRAD, BF16>(a, s);
   switch (choose<GRAD>(a)) {
     case 16: return launch_few<16, GRAD, BF16>(a, s);
     case 64: return launch_few<64, GRAD, BF16>(a, s);
-    default: return launch_tiles<GRAD, BF16>(a, s);
+    case 128: return launch_tiles<128, GRAD, BF16>(a, s);
+    default: return launch_tiles<256, GRAD, BF16>(a, s);
   }
 }
 

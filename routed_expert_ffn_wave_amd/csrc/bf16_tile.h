@@ -19,6 +19,13 @@ __device__ __forceinline__ void dma16_at(const uint8_t* from, uint32_t lds) {
   asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds), "i"(AT) : "memory", "scc");
 }
 
+// The lane, laundered: addresses are formed from it where they are used, not kept in registers from one tile of a block to the next.
+__device__ __forceinline__ int this_lane() {
+  int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 template <int BM_, int BN_, int WM_, int WN_, int NS_, int KG_ = 1, int BK_ = 64, int NSC_ = NS_>
 struct Bf16Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_;
@@ -174,9 +181,7 @@ template <class C, int RMODE, int CMODE>
 __device__ __forceinline__ void bf16_tile(const Operand& ro, const Operand& co, int red, uint8_t* lds, f32x4 (&acc)[C::MF][C::NF],
                                           int rotate = 0) {
   constexpr int MF = C::MF, NF = C::NF, NS = C::NS, NSC = C::NSC, U = C::QM + C::QN;
-  int thread = threadIdx.x;
-  asm volatile("" : "+v"(thread));  // laundered: addresses are formed here, not kept from one tile of a block to the next
-  const int lane = thread & 63, wv = __builtin_amdgcn_readfirstlane(thread >> 6) % C::GW, tid = wv * 64 + lane;
+  const int lane = this_lane(), wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % C::GW, tid = wv * 64 + lane;
   const int wm = wv / C::WN, wn = wv % C::WN;
 #pragma unroll
   for (int m = 0; m < MF; ++m)

@@ -609,6 +609,16 @@ def test_tiles_of_every_height_and_few_stages(red, grad):
     check_forward(normal(g, int(off[-1]), red), normal(g, len(counts), *((red, cols) if grad else (cols, red))), off, None, BF, grad)
 
 
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("red", [8, 72, 128, 200, 264, 448, 456, 1032])
+def test_narrow_tiles(red, grad):
+    """Some 60 rows an expert in few tiles, and groups that take several."""
+    counts = torch.tensor([17, 64, 65, 0, 100, 128, 129, 200, 257, 1, 30, 64] + [17] * 8)
+    off = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]).int()
+    g, cols = gen(red), 1032
+    check_forward(normal(g, int(off[-1]), red), normal(g, len(counts), *((red, cols) if grad else (cols, red))), off, None, BF, grad)
+
+
 @pytest.mark.parametrize("P, N, K", [(300, 264, 520), (5000, 1032, 2056), (70000, 264, 520)])
 def test_planned_matrix_gradient(P, N, K):
     """More tiles than two a compute unit: from queues, with experts of every class of rows, some without a slot."""
