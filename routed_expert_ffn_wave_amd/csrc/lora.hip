@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out[t] = base[t] + scale_s (x[t] A_s^T) B_s^T,  s the slot of row t's adapter; rows without one: out[t] = base[t].
-// The hidden rows h = x A^T (r values each) are held in fp32; the second product takes them as two bf16 terms (the value
-// and what its rounding left), so that they carry 16 bits or more of it and not 8.
+// The hidden rows h = x A^T (r values each) are held in fp32; the second product takes them as bf16 terms (the value, what its
+// rounding left, and for fp32 results what that one's left), which carry 16 bits or more of it, or all 24, and not 8.
 //
 // lora_small_kernel: few rows.  A block has 16 rows of one adapter and 256 columns and forms their hidden rows by itself, its
 // waves sharing K; one launch, no workspace.  Bound by its chain of dependent loads.
@@ -52,9 +52,13 @@ __device__ __forceinline__ Chunk chunk_of(const GroupList& gl, int ch) {
 __device__ __forceinline__ bf16x8 load8(const uint16_t* p, bool in) {
   return in ? *(const bf16x8*)p : __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
 }
-// The second term of v, whose first is h: nothing beside an infinity (whose own rest would be a NaN) or a NaN.
-__device__ __forceinline__ uint16_t second_term(float v, uint16_t h) {
-  return (h & 0x7f80) == 0x7f80 ? 0 : f32_to_bf16_bits(v - bf16_bits_to_f32(h));
+// Bf16 terms that a hidden value is passed on as: with a bf16 result two hold more than it does, with an fp32 one three hold all of it.
+constexpr int terms(bool bf16) { return bf16 ? 2 : 3; }
+// The next term of v, of which v is left for the one after: nothing beside an infinity (whose own rest would be a NaN) or a NaN.
+__device__ __forceinline__ uint32_t next_term(float& v) {
+  const uint16_t h = f32_to_bf16_bits(v);
+  v = (h & 0x7f80) == 0x7f80 ? 0.0f : v - bf16_bits_to_f32(h);
+  return h;
 }
 // four bf16 values plus four fp32, rounded
 __device__ __forceinline__ u32x2 pack_sum(u32x2 base, f32x4 v) {
@@ -81,7 +85,8 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
   using C = SmallCfg<RF>;
   using T = typename C::Tile;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  __shared__ __attribute__((aligned(16))) uint16_t s_hi[16 * C::PITCH], s_lo[16 * C::PITCH];
+  constexpr int TERMS = terms(BF16);
+  __shared__ __attribute__((aligned(16))) uint16_t s_hidden[TERMS][16 * C::PITCH];
   GroupList gl;
   const int chunks = list_chunks<16>(a.g, copy, gl, (int*)(smem + T::LDS));
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -138,19 +143,19 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
           for (int q = 0; q < C::SW; ++q) v += ((const float*)(smem + q * T::RING))[row * RF * 16 + j];
           v *= scale;
         }
-        const uint16_t h = f32_to_bf16_bits(v);
-        s_hi[row * C::PITCH + j] = h;
-        s_lo[row * C::PITCH + j] = second_term(v, h);
+#pragma unroll
+        for (int q = 0; q < TERMS; ++q) s_hidden[q][row * C::PITCH + j] = (uint16_t)next_term(v);
       }
       __syncthreads();
 #pragma unroll
       for (int q = 0; q < C::KS; ++q) {
-        const bf16x8 hf = *(const bf16x8*)(s_hi + r * C::PITCH + 32 * q + 8 * g), lf = *(const bf16x8*)(s_lo + r * C::PITCH + 32 * q + 8 * g);
+        bf16x8 hf[TERMS];
 #pragma unroll
-        for (int f = 0; f < C::NF; ++f) {
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[q][f], hf, acc[f], 0, 0, 0);
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[q][f], lf, acc[f], 0, 0, 0);
-        }
+        for (int k = 0; k < TERMS; ++k) hf[k] = *(const bf16x8*)(s_hidden[k] + r * C::PITCH + 32 * q + 8 * g);
+#pragma unroll
+        for (int f = 0; f < C::NF; ++f)
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[q][f], hf[k], acc[f], 0, 0, 0);
       }
     }
 #pragma unroll
@@ -205,13 +210,16 @@ __global__ __launch_bounds__(128) void lora_shrink_kernel(LoraArgs a, int splits
 // 32 rows by 256 columns of out, 64 of the r columns at a time: B goes to LDS directly, the hidden rows are added up on
 // the way there.
 using ExpandB = Loader<DIRECT, 256, 4>;
-constexpr int ER = 32, kHidden = ER * 128, kExpandLds = 2 * kHidden + 256 * 128;  // both terms, B
+constexpr int ER = 32, kHidden = ER * 128;  // bytes of a term of 64 columns
+template <bool BF16>
+constexpr int kExpandLds = terms(BF16) * kHidden + 256 * 128;  // the terms, B
 
 template <bool BF16>
 __global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int splits, bool copy) {
+  constexpr int TERMS = terms(BF16), AT_B = TERMS * kHidden;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   GroupList gl;
-  const int chunks = list_chunks<ER>(a.g, copy, gl, (int*)(smem + kExpandLds));
+  const int chunks = list_chunks<ER>(a.g, copy, gl, (int*)(smem + kExpandLds<BF16>));
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ntn = (a.N + 255) / 256;
   for (int it = blockIdx.x; it < chunks * ntn; it += gridDim.x) {
     const Chunk c = chunk_of<ER>(gl, it / ntn);
@@ -254,7 +262,7 @@ __global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int spl
         const Operand bo{a.b + ((size_t)c.slot * a.N + n0) * a.r + j0, a.r, min(256, a.N - n0), nullptr, 0};
         ExpandB lb;
         lb.open(bo, tid, red);
-        unrolled<0, ExpandB::Q>([&](auto q) { lb.template issue<decltype(q)::value, 2 * kHidden>(lds_addr(smem) + wv * 1024); });
+        unrolled<0, ExpandB::Q>([&](auto q) { lb.template issue<decltype(q)::value, AT_B>(lds_addr(smem) + wv * 1024); });
         if (j0 == 0) load_base();
         // pieces of 4 hidden values, ER / 16 a thread, splits four at a time so that their loads are under way together
         f32x4 v[ER / 16];
@@ -279,36 +287,40 @@ __global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int spl
 #pragma unroll
         for (int i = 0; i < ER / 16; ++i) {
           const int row = 16 * i + tid / 16;
-          const f32x4 h = v[i] * scale;
-          u32x2 hi, lo;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint16_t h0 = f32_to_bf16_bits(h[2 * q]), h1 = f32_to_bf16_bits(h[2 * q + 1]);
-            hi[q] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-            lo[q] = (uint32_t)second_term(h[2 * q], h0) | ((uint32_t)second_term(h[2 * q + 1], h1) << 16);
-          }
+          f32x4 h = v[i] * scale;
           uint8_t* to = smem + row * 128 + ((tid % 16 / 2 ^ Loader<DIRECT, ER, 4>::key(row)) << 4) + (tid & 1) * 8;
-          *(u32x2*)to = hi;
-          *(u32x2*)(to + kHidden) = lo;
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            u32x2 pair;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float lo = h[2 * q], hi = h[2 * q + 1];
+              pair[q] = next_term(lo);
+              pair[q] |= next_term(hi) << 16;
+              h[2 * q] = lo, h[2 * q + 1] = hi;
+            }
+            *(u32x2*)(to + k * kHidden) = pair;
+          }
         }
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (red < 64) {
-          ExpandB::clear(smem + 2 * kHidden, tid, red);
+          ExpandB::clear(smem + AT_B, tid, red);
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
         unrolled<0, 2>([&](auto half) {
           constexpr int H = decltype(half)::value;
           bf16x8 bf[4];
 #pragma unroll
-          for (int f = 0; f < 4; ++f) bf[f] = rb.template read<H>(smem + 2 * kHidden, f);
+          for (int f = 0; f < 4; ++f) bf[f] = rb.template read<H>(smem + AT_B, f);
 #pragma unroll
           for (int m = 0; m < ER / 16; ++m) {
-            const bf16x8 hf = rr.template read<H>(smem, m), lf = rr.template read<H>(smem + kHidden, m);
+            bf16x8 hf[TERMS];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[f], hf, acc[m][f], 0, 0, 0);
-              acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[f], lf, acc[m][f], 0, 0, 0);
-            }
+            for (int k = 0; k < TERMS; ++k) hf[k] = rr.template read<H>(smem + k * kHidden, m);
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+              for (int k = 0; k < TERMS; ++k) acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[f], hf[k], acc[m][f], 0, 0, 0);
           }
         });
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // LDS is free for what comes next
@@ -358,7 +370,7 @@ template <bool BF16>
 hipError_t launch_expand(const LoraArgs& a, int splits, hipStream_t s) {
   static LaunchCache cache;
   LaunchFacts f;
-  const size_t lds = kExpandLds + list_lds(a.g.E);
+  const size_t lds = kExpandLds<BF16> + list_lds(a.g.E);
   hipError_t e = cache.get((const void*)lora_expand_kernel<BF16>, 256, lds, &f);
   if (e != hipSuccess) return e;
   const long long items = chunks(a.g.P, a.g.E + 1, ER) * ((a.N + 255) / 256), most = (long long)f.per_cu * f.cus;

@@ -71,9 +71,9 @@ def swiglu_gradient(gu, dh):
     return torch.cat([dg, du], 1), torch.cat([off_g, off_u], 1)
 
 
-def adapters(base, x, a, b, offsets, gather, slot, scale):
+def adapters(base, x, a, b, offsets, gather, slot, scale, left=2.0 ** -16):
     """(fp64 out, bound): rows without an adapter are base; a hidden value is a sum of K products in fp32 (in splits) times the
-    scale (a rounding), in two bf16 terms that leave 2^-16 of it (2^-8 of 2^-8); the outer sum has 2 r terms; base is
+    scale (a rounding), in two bf16 terms that leave 2^-16 of it (2^-8 of 2^-8), or in three that leave 2^-24 (left); the outer sum has 2 r terms; base is
     added and the sum rounded."""
     T, E, n_slots, r, K = base.shape[0], offsets.numel() - 1, a.shape[0], a.shape[1], a.shape[2]
     ref, bound = base.double().clone(), torch.zeros(base.shape, dtype=torch.float64)
@@ -83,7 +83,7 @@ def adapters(base, x, a, b, offsets, gather, slot, scale):
         sc = 1.0 if scale is None else float(scale[s])
         A, B, xr = a[s].double(), b[s].double(), x[rows].double()
         hid, hmag = xr @ A.t(), xr.abs() @ A.abs().t()
-        hoff = 2 * (K + 20) * U32 * hmag + 2.0 ** -16 * hid.abs()
+        hoff = 2 * (K + 20) * U32 * hmag + left * hid.abs()
         delta = sc * (hid @ B.t())
         ref[rows] += delta
         bound[rows] = abs(sc) * ((hoff + 2 * (2 * r + 2) * U32 * hid.abs()) @ B.abs().t()) + 2 * U32 * (delta.abs() + base[rows].double().abs())

@@ -319,6 +319,18 @@ def test_adapters_special_values_stay_in_their_rows():
     assert torch.isinf(out).sum() == 1 and out[9, 5] == float("inf")
 
 
+@pytest.mark.parametrize("T, E, r, N, K", [(7, 3, 8, 72, 8), (50, 4, 40, 264, 64), (300, 2, 72, 264, 64), (3000, 5, 16, 1288, 136), (200, 3, 256, 64, 32)])
+def test_adapters_keep_what_fp32_results_hold(T, E, r, N, K):
+    """Short inner sums, whose own error is small beside 2^-16: fp32 results have them whole."""
+    g = gen(T + r)
+    off, gather = adapter_rows(g, T, E)
+    base = torch.zeros(T, N)
+    x, a, b = normal(g, T, K), normal(g, E, r, K, scale=K ** -0.5), normal(g, E, N, r)
+    want, bound = ref.adapters(base, x, a, b, off, gather, None, None, left=2.0 ** -24)
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)]).cpu()
+    assert ((out.double() - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("T, r, K", [(40, 8, 136), (40, 56, 136), (900, 40, 520)])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_adapters_of_infinite_rows(T, r, K, dtype):
