@@ -54,14 +54,21 @@ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, int slot, int
   store_rows<C::MF, C::NF, BF16, false>(acc, out, cols, wv / C::WN * 16 * C::MF, rows, n0 + wv % C::WN * 16 * C::NF, cols, this_lane());
 }
 
+// The height of the tiles of a group of cnt rows.
+template <int W>
+__device__ __forceinline__ int tile_rows(int cnt) {
+  constexpr int STEP = W == 128 ? 64 : 32;
+  const int ntm = (cnt + kTallest<W> - 1) / kTallest<W>;
+  return ((cnt + ntm - 1) / ntm + STEP - 1) / STEP * STEP;
+}
+
 // Tile `local` of a group of cnt rows, cut into tiles of the same height: bands of 4 row tiles, column tiles within a band in turn.  A tile
 // takes the least of the heights that holds its rows.
 template <int W, bool GRAD, bool BF16>
 __device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int row0, int cnt, int local, uint8_t* lds) {
   constexpr int BAND = 4;
-  constexpr int STEP = W == 128 ? 64 : 32;
   const int ntn = ((GRAD ? a.K : a.N) + W - 1) / W;
-  const int ntm = (cnt + kTallest<W> - 1) / kTallest<W>, each = ((cnt + ntm - 1) / ntm + STEP - 1) / STEP * STEP;
+  const int ntm = (cnt + kTallest<W> - 1) / kTallest<W>, each = tile_rows<W>(cnt);
   const int band = local / (BAND * ntn), h = min(BAND, ntm - band * BAND), in = local - band * BAND * ntn;
   const int m0 = (band * BAND + in % h) * each, n0 = in / h * W, rows = min(each, cnt - m0);
   auto tile = [&](auto height) { grouped_tile<decltype(height)::value, W, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds); };
@@ -89,25 +96,59 @@ __device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int
 }
 
 // Blocks are placed on the 8 XCDs round-robin; each XCD gets a contiguous run of the tile list, so that tiles that run
-// together share rows and matrices through its L2.  (Queues with the tallest tiles first, as the matrix gradient has them,
-// were 5 % slower: one after the other, tiles bound by the matrix cores and tiles bound by memory do not fill each
-// other's gaps, and the list takes a launch of its own.)
-template <int W, bool GRAD, bool BF16>
+// together share rows and matrices through its L2, which holds little more than the stages that they have under way: they share
+// only what they read in step.  So groups are cut into even tiles and long lists go by falling heights, and an XCD's tiles take equally long;
+// XCDs begin at different rounds, or all would be bound by the matrix cores first and by memory later.  us, without order / with it:
+// 4096 tokens, Zipf, top 8 of 128 experts of 1536 x 2048 297 / 279 (read by L2 1.39 -> 1.2 GB, 0.92 needed), 1024 tokens 158 / 145.
+// (Each block a run of tiles of even cost: 343; queues with the tallest tiles first, as the matrix gradient has them, 5 % more than no order.)
+template <int W, bool ORDERED, bool GRAD, bool BF16>
 __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int ntn = ((GRAD ? a.K : a.N) + W - 1) / W;
   const int per = gridDim.x / 8, x = blockIdx.x % 8, j = blockIdx.x / 8, lane = threadIdx.x & 63;  // gridDim.x % 8 == 0
   // The list lies where the stages will: every wave keeps what it says of this block's next 16 tiles, lanes 4 i .. 4 i + 3 tile i.
   for (int first = 0;; first += 16) {
-    const int E2 = a.g.E + 2;
+    const int E = a.g.E, E2 = E + 2;
     int* li = (int*)lds;
     GroupList gl{li, li + E2, li + 2 * E2, li + 3 * E2, 0};
-    list_groups(a.g, gl, li + 4 * E2, [&](int cnt) { return (cnt + kTallest<W> - 1) / kTallest<W> * ntn; });
-    const int nitems = gl.item0[gl.n];
-    // (Rounds are turned against each other: heights repeat along the list, and a block must not meet the same one always.)
-    const int mine = first + lane / 4, it = mine * (int)gridDim.x + x * per + (j + 7 * mine) % per;
-    int word = mine * (int)gridDim.x < nitems ? 0 : -1;  // its slot, first row, rows (0: no tile in this round, -1: nor later), and number in the group
-    if (it < nitems) {
+    auto tiles_of = [&](int cnt) { return (cnt + kTallest<W> - 1) / kTallest<W> * ntn; };
+    int classes = 0;
+    if constexpr (!ORDERED) {
+      list_groups(a.g, gl, li + 4 * E2, tiles_of);
+    } else {
+      // The groups by falling class of their tiles' heights, classes that there are in turn.
+      int* rows_of = li + 5 * E2;  // [E]: slot, first row, rows (0: none)
+      int* present = rows_of + 3 * E;
+      if (threadIdx.x == 0) *present = 0;
+      __syncthreads();
+      auto class_of = [](int cnt) { return 4 - (tile_rows<W>(cnt) + 63) / 64; };
+      for (int e = threadIdx.x; e < E; e += 512) {
+        int slot, row0, cnt;
+        if (!group_of(a.g, e, slot, row0, cnt)) cnt = 0;
+        rows_of[e] = slot, rows_of[E + e] = row0, rows_of[2 * E + e] = cnt;
+        if (cnt > 0) atomicOr(present, 1 << class_of(cnt));
+      }
+      __syncthreads();
+      classes = __builtin_amdgcn_readfirstlane(*present);
+      const int E64 = (E + 63) / 64 * 64;
+      build_group_list(
+          __popc(classes) * E64, gl, li + 4 * E2,
+          [&](int i, int& slot, int& row0, int& cnt) {
+            const int pass = i / E64, e = i - pass * E64;
+            if (e >= E) return false;
+            int left = classes;
+            for (int k = 0; k < pass; ++k) left &= left - 1;
+            slot = rows_of[e], row0 = rows_of[E + e], cnt = rows_of[2 * E + e];
+            return cnt > 0 && (left & -left) == 1 << class_of(cnt);
+          },
+          tiles_of);
+    }
+    const int nitems = gl.item0[gl.n], rounds = (nitems + (int)gridDim.x - 1) / (int)gridDim.x;
+    // Each XCD begins at another round, and rounds are turned against each other: a block must not meet the same height always.
+    const int mine = first + lane / 4, turned = classes & (classes - 1) ? (mine + x * rounds / 8) % max(rounds, 1) : mine;
+    const int it = turned * (int)gridDim.x + x * per + (j + 7 * mine) % per;
+    int word = mine < rounds ? 0 : -1;  // its slot, first row, rows (0: no tile in this round, -1: nor later), and number in the group
+    if (mine < rounds && it < nitems) {
       const int gi = find_group(gl.item0, gl.n, it);
       word = lane % 4 == 3 ? it - gl.item0[gi] : (lane % 4 == 0 ? gl.slot : lane % 4 == 1 ? gl.row0 : gl.cnt)[gi];
     }
@@ -117,7 +158,7 @@ __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {
       if (rows < 0) return;
       if (rows > 0)
         grouped_item<W, GRAD, BF16>(a, __builtin_amdgcn_readlane(word, 4 * r), __builtin_amdgcn_readlane(word, 4 * r + 1), rows,
-                                 __builtin_amdgcn_readlane(word, 4 * r + 3), lds);
+                                    __builtin_amdgcn_readlane(word, 4 * r + 3), lds);
     }
   }
 }
@@ -269,17 +310,17 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int W, bool GRAD, bool BF16>
+template <int W, bool ORDERED, bool GRAD, bool BF16>
 hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
   static LaunchCache cache;
   LaunchFacts f;
   const int cols = GRAD ? a.K : a.N, E = a.g.E, P = a.g.P;
   const long long ntn = (cols + W - 1) / W, tiles = std::min<long long>(P, (P + kTallest<W> - 1) / kTallest<W> + E) * ntn;
   if ((P / kTallest<W> + 2LL) * (E / 2 + 1) * ntn >= kMostItems) return hipErrorNotSupported;
-  hipError_t e = cache.get((const void*)grouped_tile_kernel<W, GRAD, BF16>, 512, kTileLds, &f);
+  hipError_t e = cache.get((const void*)grouped_tile_kernel<W, ORDERED, GRAD, BF16>, 512, kTileLds, &f);
   if (e != hipSuccess) return e;
   const long long upper = (tiles + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
-  hipLaunchKernelGGL((grouped_tile_kernel<W, GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(512), kTileLds, s, a);
+  hipLaunchKernelGGL((grouped_tile_kernel<W, ORDERED, GRAD, BF16>), dim3((uint32_t)(upper < most ? upper : most)), dim3(512), kTileLds, s, a);
   return hipGetLastError();
 }
 
@@ -334,7 +375,9 @@ using T256 = Bf16Cfg<256, 256, 2, 4, 4, 1, 32>;
 // Tiles of 128 columns where 256 leave units without one, or a round nearly empty.  us, 256 (or 64) / 128: 256 tokens, top 2 of 8 experts of
 // 4096 x 4096 73 / 50, back 86 / 53; 300, top 4 of 16 of 2048 x 2048 32 / 25, back 33 / 27; 333, top 8 of 64, 40 here, of 2048 x 1032 56 / 49; but 128 experts
 // with 128 rows each 161 / 168, 512 tokens, top 2 of 8, 81 / 89; back 77 tokens, top 4 of 32 of 2048 x 768 19.8 / 21.0, 64, top 2 of 8, 54.6 / 51.1.
+// The list is put in order of heights where there are more than two rounds and heights to differ: it takes 1 - 2 us.
 // 16 rows a block, two blocks a unit, where 64 would leave most units without one (64 rows, 4096 x 4096: 16.0 -> 12.2).
+constexpr int kOrdered = 257;
 template <bool GRAD>
 int choose(const GroupedArgs& a) {
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;
@@ -348,18 +391,20 @@ int choose(const GroupedArgs& a) {
   // (Groups of about 128 rows: many in two tiles.  A rows' gradient of few rows wants whole memory rows.)
   const double narrow = each <= 100 && !(GRAD && each < 12) ? rounds(128, 128) * (GRAD ? 0.68 : 0.58) * tile : wide;
   if (few < std::min(wide, narrow) || (!GRAD && each <= 16)) return blocks(64, 64) < 100 ? 16 : 64;
-  return narrow < wide ? 128 : 256;
+  if (narrow < wide) return 128;
+  return each >= 48 && blocks(256, 256) > 512 ? kOrdered : 256;
 }
 
 template <bool GRAD, bool BF16>
 hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
   // tiles of all groups in an int whatever the table holds: one that does not ascend can give all rows to every second expert
-  if ((a.g.P / 16 + 2LL) * (a.g.E / 2 + 1) * (((GRAD ? a.K : a.N) + 63) / 64) >= kMostItems) return launch_tiles<256, GRAD, BF16>(a, s);
+  if ((a.g.P / 16 + 2LL) * (a.g.E / 2 + 1) * (((GRAD ? a.K : a.N) + 63) / 64) >= kMostItems) return launch_tiles<256, true, GRAD, BF16>(a, s);
   switch (choose<GRAD>(a)) {
     case 16: return launch_few<16, GRAD, BF16>(a, s);
     case 64: return launch_few<64, GRAD, BF16>(a, s);
-    case 128: return launch_tiles<128, GRAD, BF16>(a, s);
-    default: return launch_tiles<256, GRAD, BF16>(a, s);
+    case 128: return launch_tiles<128, false, GRAD, BF16>(a, s);
+    case kOrdered: return launch_tiles<256, true, GRAD, BF16>(a, s);
+    default: return launch_tiles<256, false, GRAD, BF16>(a, s);
   }
 }
 

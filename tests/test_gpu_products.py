@@ -631,6 +631,17 @@ def test_narrow_tiles(red, grad):
     check_forward(normal(g, int(off[-1]), red), normal(g, len(counts), *((red, cols) if grad else (cols, red))), off, None, BF, grad)
 
 
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("P, low", [(20000, 17), (52000, 1)])
+def test_more_tiles_than_a_block_keeps_at_once(P, low, grad):
+    """Some 5000 tiles of 1024 experts, of one height in the experts' order, and of all heights by height."""
+    g, E, cols, red = gen(P), 1024, 1032, 24
+    spare = torch.rand(E, generator=g).pow(2)
+    counts = low + ((spare * (P - low * E) / spare.sum()) if low == 1 else torch.ones(E)).long()
+    off = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]).int()
+    check_forward(normal(g, int(off[-1]), red), normal(g, E, *((red, cols) if grad else (cols, red))), off, None, BF, grad)
+
+
 @pytest.mark.parametrize("P, N, K", [(300, 264, 520), (5000, 1032, 2056), (70000, 264, 520)])
 def test_planned_matrix_gradient(P, N, K):
     """More tiles than two a compute unit: from queues, with experts of every class of rows, some without a slot."""
