@@ -6,11 +6,12 @@
 //   matrices       dw[e][n][k] = sum_{p of e} dout[p][n] a[p][k]
 // bf16 products are exact in fp32 and added there by the matrix instructions; results are rounded once.
 //
-// What bounds them.  Compute: 16384 rows of one 4096 x 7168 matrix take 690 - 710 us forward (1.36 - 1.4 PFLOP/s; the library 615) and
-// 670 - 700 back (the library 700), 8 experts with 2048 rows each 808 us for the matrices (1.19 PFLOP/s; the library's dense
+// What bounds them.  Compute: 16384 rows of one 4096 x 7168 matrix take 680 - 710 us forward (1.36 - 1.41 PFLOP/s; the library 615) and
+// 690 - 710 back (the library 700), 8 experts with 2048 rows each 790 - 810 us for the matrices (1.2 PFLOP/s; the library's dense
 // product of that layout 1.0 - 1.2): without the loads 583 of 740 us, without the matrix instructions 623, so neither alone; the clock
-// falls to 1.4 - 1.7 GHz under them.  Memory: 128 experts of 1536 x 2048 with 64 rows each 147 - 156 us (5.6 TB/s), 16 tokens 92 us (5.4).
-// Between them both share the time: 256 rows each 210 us (bytes alone 166, products alone 132).
+// falls to 1.4 - 1.7 GHz under them.  Memory: 128 experts of 1536 x 2048 with 64 rows each 150 us (5.5 TB/s), 16 tokens 97 us (5.2); with
+// 256 rows each 210 us, what L2 reads from beyond it at 5 TB/s.  4096 tokens, Zipf, 274 us: both in turn (1.24 GB and 206 GFLOP, 36 % of
+// the matrix cores' cycles).
 #include <algorithm>
 #include <cmath>
 
@@ -99,7 +100,7 @@ __device__ __forceinline__ void grouped_item(const GroupedArgs& a, int slot, int
 // together share rows and matrices through its L2, which holds little more than the stages that they have under way: they share
 // only what they read in step.  So groups are cut into even tiles and long lists go by falling heights, and an XCD's tiles take equally long;
 // XCDs begin at different rounds, or all would be bound by the matrix cores first and by memory later.  us, without order / with it:
-// 4096 tokens, Zipf, top 8 of 128 experts of 1536 x 2048 297 / 279 (read by L2 1.39 -> 1.2 GB, 0.92 needed), 1024 tokens 158 / 145.
+// 4096 tokens, Zipf, top 8 of 128 experts of 1536 x 2048 297 / 279 (read by L2 1.39 -> 1.14 GB, 0.92 needed), 1024 tokens 158 / 145.
 // (Each block a run of tiles of even cost: 343; queues with the tallest tiles first, as the matrix gradient has them, 5 % more than no order.)
 template <int W, bool ORDERED, bool GRAD, bool BF16>
 __global__ __launch_bounds__(512, 2) void grouped_tile_kernel(GroupedArgs a) {

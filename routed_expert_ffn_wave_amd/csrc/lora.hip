@@ -4,9 +4,12 @@
 // rounding left, and for fp32 results what that one's left), which carry 16 bits or more of it, or all 24, and not 8.
 //
 // lora_small_kernel: few rows.  A block has 16 rows of one adapter and 256 columns and forms their hidden rows by itself, its
-// waves sharing K; one launch, no workspace.  Bound by its chain of dependent loads.
+// waves sharing K; one launch, no workspace.  Bound by its chain of dependent loads (16 rows of 16 adapters 5.9 us, of which 3.6 are the
+// launch) and, with more blocks, by the reads of x and A that the blocks of an adapter repeat from L2.
 // lora_shrink_kernel, lora_expand_kernel: many rows.  The first forms hidden rows in tiles of 64 rows by splits of K, so that
-// every compute unit has loads in flight; the second adds the splits up in their order and multiplies with B.
+// every compute unit has loads in flight; the second adds the splits up in their order and multiplies with B.  4096 rows of 5
+// adapters, r = 64, 7168 -> 4096: 17.3 + 27.4 us.  The first streams x at 3.4 TB/s: latency, one or two blocks a unit (other splits, 128
+// rows a block, another place in K to begin with: within 3 %); the second at 2.5 TB/s: its blocks' loads, sums and stores in turn.
 #include <algorithm>
 
 #include "bf16_tile.h"
