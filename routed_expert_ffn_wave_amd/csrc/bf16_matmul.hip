@@ -7,7 +7,7 @@
 // bf16 products are exact in fp32 and added there by the matrix instructions; results are rounded once.
 //
 // What bounds them.  Compute: 16384 rows of one 4096 x 7168 matrix take 680 - 710 us forward (1.36 - 1.41 PFLOP/s; the library 615) and
-// 690 - 710 back (the library 700), 8 experts with 2048 rows each 790 - 810 us for the matrices (1.2 PFLOP/s; the library's dense
+// 690 - 710 back (the library 700), 8 experts with 2048 rows each 780 us for the matrices (1.23 PFLOP/s; the library's dense
 // product of that layout 1.0 - 1.2): without the loads 583 of 740 us, without the matrix instructions 623, so neither alone; the clock
 // falls to 1.4 - 1.7 GHz under them.  Memory: 128 experts of 1536 x 2048 with 64 rows each 150 us (5.5 TB/s), 16 tokens 97 us (5.2); with
 // 256 rows each 210 us, what L2 reads from beyond it at 5 TB/s.  4096 tokens, Zipf, 274 us: both in turn (1.24 GB and 206 GFLOP, 36 % of
@@ -245,7 +245,10 @@ template <class C, bool BF16, bool ADD, class Next>
 __device__ __forceinline__ void wgrad_item(const WgradArgs& a, int e, int row0, int cnt, int t, uint8_t* lds, Next next) {
   const int ntn = (a.K + C::BN - 1) / C::BN, lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (ADD && cnt == 0) return next();
-  const int m0 = t / ntn * C::BM, n0 = t % ntn * C::BN;
+  // bands of 4 tiles along N, in turn along K: 32 that run together read 4 + 8 tiles' operands and not 1 + 28
+  // (8 experts of 4096 x 7168 with 2048 rows each: 3.6 -> 1.5 GB read by L2, 849 -> 822 us)
+  const int ntm = (a.N + C::BM - 1) / C::BM, band = t / (4 * ntn), h = min(4, ntm - band * 4), in = t - band * 4 * ntn;
+  const int m0 = (band * 4 + in % h) * C::BM, n0 = in / h * C::BN;
   f32x4 acc[C::MF][C::NF];
   const Operand ro{a.dout + (size_t)row0 * a.N + m0, a.N, min(C::BM, a.N - m0), nullptr, 0};
   const Operand co{a.a + (size_t)row0 * a.K + n0, a.K, min(C::BN, a.K - n0), nullptr, 0};
