@@ -371,7 +371,7 @@ using T256 = Bf16Cfg<256, 256, 2, 4, 4, 1, 32>;
 // stages of 64): 256-column tiles, or blocks of 64 columns whose waves share the reduction.  How the rows lie is known on
 // the device only: as if experts were drawn evenly.  Measured, us, 256-column tiles / 64-column blocks, bf16 results:
 //   forward, 128 experts of 1536 x 2048, top 8 of   1 token  18.9 / 11.8    4  34.4 / 29.9    8  70.7 / 60.6    64  143.6 / 137.7
-//                                                  256  148.8 / 147.3    512  154.1 / 160.8    4096 (Zipf)  325 / 533
+//                                                  256  148.8 / 147.3    512  154.1 / 160.8    4096 (Zipf)  274 / 533
 //   rows' gradient, the same                         1  17.3 / 11.9    4  32.5 / 33.2    16  99.3 / 110.5    256  147.4 / 178.8
 //   one matrix of 4096 x 4096, rows                 64  31.2 / 16.0    300  73.8 / 29.8
 // With few rows the forward product is bound by the matrices' bytes, which the smaller blocks read at 5.7 - 6.1 TB/s, the larger
@@ -381,7 +381,7 @@ using T256 = Bf16Cfg<256, 256, 2, 4, 4, 1, 32>;
 // with 128 rows each 161 / 168, 512 tokens, top 2 of 8, 81 / 89; back 77 tokens, top 4 of 32 of 2048 x 768 19.8 / 21.0, 64, top 2 of 8, 54.6 / 51.1.
 // The list is put in order of heights where there are more than two rounds and heights to differ: it takes 1 - 2 us.
 // 16 rows a block, two blocks a unit, where 64 would leave most units without one (64 rows, 4096 x 4096: 16.0 -> 12.2).
-constexpr int kOrdered = 257;
+constexpr int kOrdered = 257;  // 256, the list in order
 template <bool GRAD>
 int choose(const GroupedArgs& a) {
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K;

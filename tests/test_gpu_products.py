@@ -331,6 +331,27 @@ def test_adapters_keep_what_fp32_results_hold(T, E, r, N, K):
     assert ((out.double() - want).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("T, E, r, N, K", [(4000, 7, 16, 2056, 1544), (2000, 7, 24, 2056, 1544), (300, 3, 72, 264, 520)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adapters_in_two_kernels(T, E, r, N, K, dtype):
+    """Hidden rows in memory, for every width of their tiles; an infinite row among them."""
+    g = gen(T + r)
+    assert ft.ft_moe_lora_workspace(T, E, r, N, K) > 0
+    off, gather = adapter_rows(g, T, E)
+    base = torch.randn(T, N, generator=g).to(dtype)
+    x, a, b = normal(g, T, K), normal(g, E, r, K, scale=K ** -0.5), normal(g, E, N, r)
+    a[:, :, 3], b = a[:, :, 3].abs() + 0.5, b.abs() + 0.5
+    want, bound = ref.adapters(base, x, a, b, off, gather, None, None, left=2.0 ** (-24 if dtype is F32 else -16))
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)])
+    assert ((out.cpu().double() - want).abs() <= bound).all()
+    row = int(gather[T // 3])
+    x[row, 3] = float("inf")
+    again = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)]).cpu()
+    assert (again[row] == float("inf")).all()
+    rest = torch.arange(T) != row
+    assert same_bits(again[rest], out.cpu()[rest])
+
+
 @pytest.mark.parametrize("T, r, K", [(40, 8, 136), (40, 56, 136), (900, 40, 520)])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_adapters_of_infinite_rows(T, r, K, dtype):
