@@ -103,6 +103,23 @@ def test_grouped_product_of_a_table_that_does_not_ascend(grad):
 
 
 @pytest.mark.parametrize("grad", [False, True])
+def test_many_tiles_of_a_table_that_does_not_ascend(grad):
+    g = gen(9)
+    P, E, cols, red = 3000, 40, 4104, 40
+    off = torch.randint(-100, P + 200, (E + 1,), generator=g).int()
+    off[::2] = off[::2] // 4
+    a, w = normal(g, P, red), normal(g, E, *((red, cols) if grad else (cols, red)))
+    got = (ft.ft_moe_grouped_matmul_grad if grad else ft.ft_moe_grouped_matmul)(a.cuda(), w.cuda(), off.cuda(), out_dtype=F32).cpu()
+    fits, some = torch.zeros(got.shape, dtype=torch.bool), torch.zeros(P, dtype=torch.bool)
+    for e, r0, r1, s in ref.groups(off, None, E, P, E):
+        y = w[s].double() if grad else w[s].double().t()
+        want, mag = a[r0:r1].double() @ y, a[r0:r1].double().abs() @ y.abs()
+        fits[r0:r1] |= (got[r0:r1].double() - want).abs() <= ref.sum_bound(want, mag, red, F32)
+        some[r0:r1] = True
+    assert some.sum() > P // 2 and fits[some].all()
+
+
+@pytest.mark.parametrize("grad", [False, True])
 @pytest.mark.parametrize("P", [6, 200])
 def test_special_values_stay_in_their_rows(P, grad):
     """A NaN or an infinity in a row shows in that row only, one in a matrix in its expert's column only; the reduction's
