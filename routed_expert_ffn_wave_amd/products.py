@@ -188,11 +188,10 @@ class Bf16MoELayer:
             E = slot_of_expert.shape[0]
         if T < 0 or T * k > 1 << 30 or I2 % 16 or self.d % 8 or self.d * self.I == 0 or not 1 <= self.n_slots < 1 << 23 or E > 1024 or not 1 <= k <= min(E, 32):
             _refuse(f"invalid layer shape T={T}, k={k}, E={E}, d={self.d}, w13 rows={I2}, slots={self.n_slots}")
-        if slot_of_expert is None:
-            slot_of_expert = torch.arange(E, dtype=torch.int32, device=f"cuda:{dev}")
-        self.dev, self.w13, self.w2, self.slot_of = dev, w13, w2, slot_of_expert
-        self.E, self.k, self.T, self.out_bf16 = E, k, T, out_bf16
         new = lambda *shape, dtype: _new(shape, dtype, dev)  # noqa: E731
+        own = () if slot_of_expert is not None else (torch.arange(E, dtype=torch.int32, out=new(E, dtype=torch.int32)),)
+        self.dev, self.w13, self.w2, self.slot_of = dev, w13, w2, own[0] if own else slot_of_expert
+        self.E, self.k, self.T, self.out_bf16 = E, k, T, out_bf16
         P, f32, bf, i32 = T * k, _F32, _BF, _I32
         out = bf if out_bf16 else f32
         self.ids, self.w, self.inv = new(T, k, dtype=i32), new(T, k, dtype=f32), new(max(P, 1), dtype=i32)
@@ -208,7 +207,7 @@ class Bf16MoELayer:
         self.grad_ws = new(max(need, 16), dtype=torch.uint8)
         self._buffers = (self.ids, self.w, self.inv, self.counts, self.offsets, self.gather, self.perm_ws, self.xs, self.gu, self.h,
                          self.y_sorted, self.out, self.mask, self.dy, self.dh, self.dgu, self.dxs, self.dx, self.dw, self.dlogits, self.dw13,
-                         self.dw2, self.grad_ws)
+                         self.dw2, self.grad_ws, *own)
         if P == 0:
             self.offsets.zero_()  # no forward() does
         self._ran = P == 0

@@ -202,3 +202,61 @@ def test_layer_orders_its_buffers_with_the_streams(monkeypatch):
     assert waits == [1]
     with pytest.raises(ft.FtError, match="the stream is of cuda:1"):
         layer.forward(*args, stream=types.SimpleNamespace(cuda_stream=9, device_index=1))
+
+
+class StandInGpu:
+    """Stand-ins for the GPU under a Bf16MoELayer: what it allocates (filled with `fill`), which streams it records its buffers for, and
+    the names of its calls; a call named in `fails` raises."""
+
+    def __init__(self, monkeypatch, fill=0.0):
+        import contextlib
+        import types
+
+        from routed_expert_ffn_wave_amd import products
+        self.made, self.used, self.calls, self.fails = [], [], [], ()
+        gpu = self
+
+        class Buffer(torch.Tensor):
+            def record_stream(self, stream):
+                gpu.used.append((id(self), stream.cuda_stream))
+
+        def new(shape, dtype, dev, stream=None):
+            gpu.made.append(torch.full(shape, fill).to(dtype).as_subclass(Buffer))
+            return gpu.made[-1]
+
+        def call(name):
+            def stub(*a, **k):
+                gpu.calls.append(name)
+                if name in gpu.fails:
+                    raise ft.FtError(ft.FT_E_UNSUPPORTED, name)
+            return stub
+
+        self.streams = {n: types.SimpleNamespace(cuda_stream=n, device_index=0, synchronize=lambda: None) for n in (1, 2)}
+        monkeypatch.setattr(products, "_new", new)
+        monkeypatch.setattr(products, "_first", lambda t, name, dims, dtypes, stream=None: (0, t.shape))
+        monkeypatch.setattr(products, "_take", lambda t, name, dtypes, shape, dev: t.data_ptr())
+        monkeypatch.setattr(products, "_run", lambda *a: None)
+        monkeypatch.setattr(products, "_raw_stream", lambda dev: 1)
+        for name in ("ft_moe_dispatch", "ft_moe_dispatch_grad", "ft_moe_combine_grad", "ft_moe_grouped_matmul", "ft_moe_grouped_matmul_grad",
+                     "ft_moe_grouped_matmul_wgrad", "ft_moe_swiglu", "ft_moe_swiglu_grad"):
+            monkeypatch.setattr(products, name, call(name))
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: self.streams[1])
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+
+    def layer(self, slot=None):
+        bf = torch.bfloat16
+        return ft.Bf16MoELayer(torch.zeros(4, 64, 64, dtype=bf), torch.zeros(4, 64, 32, dtype=bf), slot, k=2, T=4)
+
+
+STEP = (torch.zeros(4, 4), torch.zeros(4, 64, dtype=torch.bfloat16))  # logits, x
+
+
+def test_layer_keeps_its_own_table_for_the_streams(monkeypatch):
+    """A layer that makes the slot table itself records that too for the streams it runs on: its kernels read it there."""
+    gpu = StandInGpu(monkeypatch)
+    layer = gpu.layer()
+    assert torch.equal(layer.slot_of, torch.arange(4).int()) and layer.slot_of.dtype == torch.int32
+    layer.forward(*STEP, stream=gpu.streams[2])
+    assert (id(layer.slot_of), 2) in gpu.used
+    assert sorted(gpu.used) == sorted((id(b), 2) for b in gpu.made)
