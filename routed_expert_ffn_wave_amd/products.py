@@ -171,8 +171,8 @@ class Bf16MoELayer:
     w2 bf16 [n_slots][d][I] as they are stored; slot_of_expert int32 [E], -1 for experts that are not resident (left to
     the residual mask; entries outside [0, n_slots) count as -1); None: expert e has matrix e.  Every buffer is allocated
     here for a fixed (T, k): forward() and backward() allocate nothing and can be captured into a graph.  backward()
-    returns the gradients of x, of the logits and, by expert, of w13 and w2 (fp32; zeros for an expert without rows,
-    nothing for one without a slot); add=True adds the latter two to what the buffers hold.  It takes what the last
+    returns the gradients of x, of the logits and, by expert, of w13 and w2 (fp32; zeros for an expert without rows;
+    what the buffers hold for one without a slot); add=True adds the latter two to what the buffers hold: zeros when the layer is made.  It takes what the last
     forward() left in the buffers and refuses to run before one.  One step at a time; streams as
     in Fp8MoELayer."""
 
@@ -202,7 +202,7 @@ class Bf16MoELayer:
         self.dy, self.dh, self.dgu, self.dxs = new(P, self.d, dtype=bf), new(P, self.I, dtype=bf), new(P, I2, dtype=bf), new(P, self.d, dtype=bf)
         self.dx = new(T, self.d, dtype=bf)
         self.dw, self.dlogits = new(T, k, dtype=f32), new(T, E, dtype=f32)
-        self.dw13, self.dw2 = new(E, I2, self.d, dtype=f32), new(E, self.d, self.I, dtype=f32)
+        self.dw13, self.dw2 = new(E, I2, self.d, dtype=f32).zero_(), new(E, self.d, self.I, dtype=f32).zero_()
         need = max(ft_moe_grouped_matmul_wgrad_workspace(I2, self.d, E), ft_moe_grouped_matmul_wgrad_workspace(self.d, self.I, E))
         self.grad_ws = new(max(need, 16), dtype=torch.uint8)
         self._buffers = (self.ids, self.w, self.inv, self.counts, self.offsets, self.gather, self.perm_ws, self.xs, self.gu, self.h,

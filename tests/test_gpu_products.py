@@ -720,3 +720,20 @@ def test_adapters_past_32_bits():
         part = torch.tensor([0, n]).int()
         want, bound = ref.adapters(base[rows].cpu(), x[rows].cpu(), a[s:s + 1].cpu(), b[s:s + 1].cpu(), part, torch.arange(n).int(), None, None)
         assert ((out[rows].cpu().double() - want).abs() <= bound).all()
+
+
+def test_layer_adds_from_the_first_step_on():
+    """backward(add=True) of a layer that has run no other: what backward() gives, and zeros for experts without a slot, in
+    memory that held other values."""
+    r, x, w13, w2, dout = layer_case(4, 60, 6, 2, 136, 72, 4)
+    slot = r["slot"].cuda()
+    torch.cuda.empty_cache()
+    old = [filled(6, n, m, dtype=F32) for n, m in ((144, 136), (136, 72)) for _ in range(3)]
+    del old
+    adding, plain = (ft.Bf16MoELayer(w13.cuda(), w2.cuda(), slot, k=2, T=60) for _ in range(2))
+    outs = []
+    for layer, add in ((adding, True), (plain, False)):
+        layer.forward(r["logits"].cuda(), x.cuda())
+        outs.append(layer.backward(dout.cuda(), add=add)[2:])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and not a[slot < 0].any() and a[slot >= 0].any()

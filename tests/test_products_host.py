@@ -260,3 +260,9 @@ def test_layer_keeps_its_own_table_for_the_streams(monkeypatch):
     layer.forward(*STEP, stream=gpu.streams[2])
     assert (id(layer.slot_of), 2) in gpu.used
     assert sorted(gpu.used) == sorted((id(b), 2) for b in gpu.made)
+
+
+def test_layer_gradients_start_from_zeros(monkeypatch):
+    """A first backward(add=True) adds to zeros, and experts without a slot have zeros as long as nobody writes others."""
+    layer = StandInGpu(monkeypatch, fill=7.0).layer(torch.tensor([0, -1, 1, 2]).int())
+    assert not layer.dw13.any() and not layer.dw2.any()
