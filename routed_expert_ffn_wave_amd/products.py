@@ -172,9 +172,9 @@ class Bf16MoELayer:
     the residual mask; entries outside [0, n_slots) count as -1); None: expert e has matrix e.  Every buffer is allocated
     here for a fixed (T, k): forward() and backward() allocate nothing and can be captured into a graph.  backward()
     returns the gradients of x, of the logits and, by expert, of w13 and w2 (fp32; zeros for an expert without rows;
-    what the buffers hold for one without a slot); add=True adds the latter two to what the buffers hold: zeros when the layer is made.  It takes what the last
-    forward() left in the buffers and refuses to run before one.  One step at a time; streams as
-    in Fp8MoELayer."""
+    what the buffers hold for one without a slot); add=True adds the latter two to what the buffers hold: zeros when the
+    layer is made.  It takes what the last forward() left in the buffers and refuses to run before one, or after one that
+    raised on its way.  One step at a time; streams as in Fp8MoELayer."""
 
     def __init__(self, w13, w2, slot_of_expert=None, k: int = 1, T: int = 1, out_bf16: bool = False):
         dev, (self.n_slots, I2, self.d) = _first(w13, "w13", 3, (_BF,))
@@ -235,7 +235,7 @@ class Bf16MoELayer:
         pl = _take(logits, "logits", (_F32,), (T, E), dev)
         if T == 0:
             return self.out, self.mask[:0]
-        self._ran = True
+        self._ran = False  # until every step of this one is enqueued
         inv = self.inv[: T * k].view(T, k)
         pi, pw, pv, pt = self.ids.data_ptr(), self.w.data_ptr(), inv.data_ptr(), slot.data_ptr()
         _run(lib.ft_moe_route, dev, stream, pl, T, E, k, pi, pw)
@@ -247,6 +247,7 @@ class Bf16MoELayer:
         ft_moe_grouped_matmul(self.h, self.w2, off, slot_of_expert=slot, out=self.y_sorted, stream=stream)
         _run(lib.ft_moe_combine, dev, stream, self.y_sorted.data_ptr(), None, pi, pw, pv, pt, T, E, k, self.d,
              self.out.data_ptr(), self.mask.data_ptr(), FT_N_SLOTS(self.n_slots) | (FT_OUT_BF16 if self.out_bf16 else 0))
+        self._ran = True
         return self.out, self.mask[:T]
 
     def backward(self, dout, add: bool = False, stream=None):

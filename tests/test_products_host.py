@@ -205,15 +205,15 @@ def test_layer_orders_its_buffers_with_the_streams(monkeypatch):
 
 
 class StandInGpu:
-    """Stand-ins for the GPU under a Bf16MoELayer: what it allocates (filled with `fill`), which streams it records its buffers for, and
-    the names of its calls; a call named in `fails` raises."""
+    """Stand-ins for the GPU under a Bf16MoELayer: what it allocates (filled with `fill`), which streams it records its buffers for; a
+    call named in `fails` raises."""
 
     def __init__(self, monkeypatch, fill=0.0):
         import contextlib
         import types
 
         from routed_expert_ffn_wave_amd import products
-        self.made, self.used, self.calls, self.fails = [], [], [], ()
+        self.made, self.used, self.fails = [], [], ()
         gpu = self
 
         class Buffer(torch.Tensor):
@@ -226,7 +226,6 @@ class StandInGpu:
 
         def call(name):
             def stub(*a, **k):
-                gpu.calls.append(name)
                 if name in gpu.fails:
                     raise ft.FtError(ft.FT_E_UNSUPPORTED, name)
             return stub
@@ -266,3 +265,19 @@ def test_layer_gradients_start_from_zeros(monkeypatch):
     """A first backward(add=True) adds to zeros, and experts without a slot have zeros as long as nobody writes others."""
     layer = StandInGpu(monkeypatch, fill=7.0).layer(torch.tensor([0, -1, 1, 2]).int())
     assert not layer.dw13.any() and not layer.dw2.any()
+
+
+def test_layer_refuses_backward_after_a_forward_that_failed(monkeypatch):
+    """A forward() that raised on its way leaves buffers of two steps: backward() refuses until another has run."""
+    gpu = StandInGpu(monkeypatch)
+    layer, dout = gpu.layer(), STEP[1]
+    layer.forward(*STEP)
+    layer.backward(dout)
+    gpu.fails = ("ft_moe_swiglu",)
+    with pytest.raises(ft.FtError, match="ft_moe_swiglu"):
+        layer.forward(*STEP)
+    gpu.fails = ()
+    with pytest.raises(ft.FtError, match="needs a forward"):
+        layer.backward(dout)
+    layer.forward(*STEP)
+    layer.backward(dout)
