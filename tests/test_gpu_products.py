@@ -737,3 +737,34 @@ def test_layer_adds_from_the_first_step_on():
         outs.append(layer.backward(dout.cuda(), add=add)[2:])
     for a, b in zip(*outs):
         assert torch.equal(a, b) and not a[slot < 0].any() and a[slot >= 0].any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "add"])
+@pytest.mark.parametrize("P, N, K", [(1000, 264, 520), (5000, 1032, 2056), (40000, 264, 520)])
+def test_planned_matrix_gradient_of_every_kind(P, N, K, kind):
+    """Matrix gradients from queues in both types and added to what is there: experts of one stage to hundreds, whole and
+    short last ones, several tiles a block, some experts without rows or without a slot."""
+    g = gen(P + N)
+    E = 90 if N < 1000 else 20
+    cuts = (torch.rand(E - 1, generator=g) ** 4 * P).long().sort()[0]
+    cuts[1:4] = cuts[4]  # without rows
+    off = torch.cat([torch.zeros(1), cuts, torch.full((1,), P)]).int()
+    slot = torch.arange(E).int()
+    slot[7], slot[11] = -1, E
+    dout, a = normal(g, P, N), normal(g, P, K)
+    dtype = BF if kind == "bf16" else F32
+    old = torch.randn(E, N, K, generator=g).to(dtype)
+    assert ft.ft_moe_grouped_matmul_wgrad_workspace(N, K, E) > 0
+    dw = old.cuda()
+    ft.ft_moe_grouped_matmul_wgrad(dout.cuda(), a.cuda(), off.cuda(), slot_of_expert=slot.cuda(), dw=dw, n_slots=E, add=kind == "add")
+    for e in range(E):
+        got = dw[e].cpu().double()
+        before = old[e].double()
+        if not 0 <= slot[e] < E:
+            assert torch.equal(got, before)
+            continue
+        x, y = dout[off[e]:off[e + 1]].double(), a[off[e]:off[e + 1]].double()
+        want, mag = x.t() @ y, x.abs().t() @ y.abs()
+        if kind == "add":
+            want, mag = want + before, mag + before.abs()
+        assert ((got - want).abs() <= ref.sum_bound(want, mag, x.shape[0] + 1, dtype)).all(), e
