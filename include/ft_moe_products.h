@@ -95,7 +95,8 @@ int ft_moe_swiglu_grad(const uint16_t* gu, const uint16_t* dh, int rows, int I, 
  * r % 8 == 0, r <= 256 (adapters of smaller rank: zeros behind), N % 8 == 0, K % 8 == 0, both at most 2^20, T < 2^24;
  * sizes whose tiles an int cannot count, whatever offsets holds, are refused with FT_E_UNSUPPORTED.
  * The inner sums are held in fp32 and enter the outer ones as bf16 terms: two for bf16 results, within 2^-16 of themselves,
- * three for fp32 ones, within 2^-24 (above bf16's largest value, 3.39e38, as infinities).
+ * three for fp32 ones, all of them.  The terms have the sum's sign and none is 0 beside a sum that is not: infinities and NaN of x, a
+ * and b give what the formula gives.
  * ws: ft_moe_lora_workspace(T, E, r, N, K) bytes of device memory (0 for few rows: then ws may be NULL).
  */
 size_t ft_moe_lora_workspace(int T, int E, int r, int N, int K);

@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out[t] = base[t] + scale_s (x[t] A_s^T) B_s^T,  s the slot of row t's adapter; rows without one: out[t] = base[t].
-// The hidden rows h = x A^T (r values each) are held in fp32; the second product takes them as bf16 terms (the value, what its
-// rounding left, and for fp32 results what that one's left), which carry 16 bits or more of it, or all 24, and not 8.
+// The hidden rows h = x A^T (r values each) are held in fp32; the second product takes them as bf16 terms (the value cut to 8 bits, what that
+// left, and for fp32 results what that one's left), which carry 16 bits of it, or all 24, and not 8.
 //
 // lora_small_kernel: few rows.  A block has 16 rows of one adapter and 256 columns and forms their hidden rows by itself, its
 // waves sharing K; one launch, no workspace.  Bound by its chain of dependent loads (16 rows of 16 adapters 5.9 us, of which 3.6 are the
@@ -57,11 +57,18 @@ __device__ __forceinline__ bf16x8 load8(const uint16_t* p, bool in) {
 }
 // Bf16 terms that a hidden value is passed on as: with a bf16 result two hold more than it does, with an fp32 one three hold all of it.
 constexpr int terms(bool bf16) { return bf16 ? 2 : 3; }
-// The next term of v, of which v is left for the one after: nothing beside an infinity (whose own rest would be a NaN) or a NaN.
+// The next term of v, of which v is left for the ones after: cut from v short of its end, so that every term has v's sign and none is 0
+// beside a value that is not: an infinite value of b then gives infinities of one sign, not the NaN of a term of the other or of a 0.  The last one
+// is rounded.  What is left of a cut is under 2^-7 of v and has 16 bits at most: two terms hold v within 2^-16, three all of it.  0, an
+// infinity and a NaN are every term.
+template <bool LAST>
 __device__ __forceinline__ uint32_t next_term(float& v) {
-  const uint16_t h = f32_to_bf16_bits(v);
-  v = (h & 0x7f80) == 0x7f80 ? 0.0f : v - bf16_bits_to_f32(h);
-  return h;
+  if constexpr (LAST) return f32_to_bf16_bits(v);
+  const uint32_t bits = __float_as_uint(v);
+  const bool some = (bits & 0x7fffffffu) - 1 < 0x7f7fffffu;  // finite and not 0
+  const uint32_t cut = (bits - some) & 0xffff0000u;          // (a NaN that a sum gave keeps its upper bits)
+  v = some ? v - __uint_as_float(cut) : v;
+  return cut >> 16;
 }
 // four bf16 values plus four fp32, rounded
 __device__ __forceinline__ u32x2 pack_sum(u32x2 base, f32x4 v) {
@@ -146,8 +153,7 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
           for (int q = 0; q < C::SW; ++q) v += ((const float*)(smem + q * T::RING))[row * RF * 16 + j];
           v *= scale;
         }
-#pragma unroll
-        for (int q = 0; q < TERMS; ++q) s_hidden[q][row * C::PITCH + j] = (uint16_t)next_term(v);
+        unrolled<0, TERMS>([&](auto q) { s_hidden[decltype(q)::value][row * C::PITCH + j] = (uint16_t)next_term<decltype(q)::value == TERMS - 1>(v); });
       }
       __syncthreads();
 #pragma unroll
@@ -292,18 +298,18 @@ __global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int spl
           const int row = 16 * i + tid / 16;
           f32x4 h = v[i] * scale;
           uint8_t* to = smem + row * 128 + ((tid % 16 / 2 ^ Loader<DIRECT, ER, 4>::key(row)) << 4) + (tid & 1) * 8;
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
+          unrolled<0, TERMS>([&](auto k) {
+            constexpr bool LAST = decltype(k)::value == TERMS - 1;
             u32x2 pair;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               float lo = h[2 * q], hi = h[2 * q + 1];
-              pair[q] = next_term(lo);
-              pair[q] |= next_term(hi) << 16;
+              pair[q] = next_term<LAST>(lo);
+              pair[q] |= next_term<LAST>(hi) << 16;
               h[2 * q] = lo, h[2 * q + 1] = hi;
             }
-            *(u32x2*)(to + k * kHidden) = pair;
-          }
+            *(u32x2*)(to + decltype(k)::value * kHidden) = pair;
+          });
         }
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (red < 64) {

@@ -768,3 +768,68 @@ def test_planned_matrix_gradient_of_every_kind(P, N, K, kind):
         if kind == "add":
             want, mag = want + before, mag + before.abs()
         assert ((got - want).abs() <= ref.sum_bound(want, mag, x.shape[0] + 1, dtype)).all(), e
+
+
+# T, r, N, K: in one kernel and in two, ranks that end inside 32 and 64 columns
+SPECIAL = [(40, 8, 72, 136), (40, 56, 72, 136), (900, 40, 72, 520), (900, 64, 72, 520), (300, 136, 264, 264), (2000, 24, 2056, 1544)]
+
+
+def special_case(T, r, N, K, dtype):
+    """Hidden values of both signs, well away from 0, some of them bf16 values as they are, and a row of zeros."""
+    g, E = gen(T + r + K), 3
+    off, gather = adapter_rows(g, T, E, 0.1)
+    base = torch.randn(T, N, generator=g).to(dtype)
+    x, a, b = normal(g, T, K), normal(g, E, r, K, scale=0.1), normal(g, E, N, r)
+    x[::3, 1:], x[::3, 0] = 0, 2.0  # hidden values 2 a[j][0]
+    a[:, :, 0] = torch.where(a[:, :, 0] < 0, a[:, :, 0] - 0.5, a[:, :, 0] + 0.5)
+    x[6] = 0
+    return off, gather, base, x, a, b
+
+
+def adapter_of_rows(off, gather, T):
+    of = torch.full((T,), -1)
+    for e in range(off.numel() - 1):
+        of[gather[off[e]:off[e + 1]].long()] = e
+    return of
+
+
+@pytest.mark.parametrize("T, r, N, K", SPECIAL)
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adapters_with_infinite_values_in_b(T, r, N, K, dtype):
+    """An infinity in b gives infinities of the hidden value's sign (a NaN where that is 0), a NaN in b NaN, in its column of
+    its adapter's rows; every other value is what it is without them."""
+    off, gather, base, x, a, b = special_case(T, r, N, K, dtype)
+    args = [t.cuda() for t in (base, x, a)]
+    tables = (off.cuda(), gather.cuda())
+    plain = ft.ft_moe_lora(*args, b.cuda(), *tables).cpu()
+    spots = [(0, 3, 1, float("inf")), (0, 71, r - 1, -float("inf")), (1, 0, r // 2, -float("inf")), (2, 40, 2, NAN), (2, 41, r - 2, float("inf"))]
+    for e, n, j, v in spots:
+        b[e, n, j] = v
+    out = ft.ft_moe_lora(*args, b.cuda(), *tables).cpu()
+    of, same = adapter_of_rows(off, gather, T), torch.ones(out.shape, dtype=torch.bool)
+    for e, n, j, v in spots:
+        rows = (of == e).nonzero()[:, 0]
+        hid, mag = x[rows].double() @ a[e, j].double(), x[rows].double().abs() @ a[e, j].double().abs()
+        sure = (hid.abs() > 2 * K * ref.U32 * mag) | (mag == 0)  # its sign in fp32 is that of fp64
+        assert sure.sum() > rows.numel() // 2
+        want = (hid * v)[sure].to(dtype)  # the column's other terms and base are finite
+        got = out[rows[sure], n]
+        assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[~torch.isnan(got)], want[~torch.isnan(want)])
+        same[rows, n] = False
+    assert torch.equal(out[same], plain[same])
+
+
+@pytest.mark.parametrize("T, r, N, K", [(9, 8, 72, 8), (300, 72, 264, 520)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adapters_with_hidden_values_past_the_largest_bf16(T, r, N, K, dtype):
+    """A hidden value between bf16's largest one and fp32's is finite: so is its product with a small b."""
+    top = float(torch.finfo(BF).max)
+    x, a = torch.zeros(T, K, dtype=BF), torch.zeros(1, r, K, dtype=BF)
+    x[:, 0], x[:, 1] = top, 2.0 ** 119
+    a[:, :, 0] = a[:, :, 1] = torch.where(torch.arange(r) % 2 == 0, 1.0, -1.0).to(BF)
+    b = torch.zeros(1, N, r, dtype=BF)
+    b[:, :, 0], b[:, :, 1] = 2.0 ** -10, 2.0 ** -11
+    off, gather, base = torch.tensor([0, T]).int(), torch.arange(T).int(), torch.zeros(T, N).to(dtype)
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)]).cpu().double()
+    want, bound = ref.adapters(base, x, a, b, off, gather, None, None)
+    assert want.min() > 1e35 and ((out - want).abs() <= bound).all()
