@@ -151,7 +151,6 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
         if (row < c.rows && j < a.r) {
 #pragma unroll
           for (int q = 0; q < C::SW; ++q) v += ((const float*)(smem + q * T::RING))[row * RF * 16 + j];
-          v *= scale;
         }
         unrolled<0, TERMS>([&](auto q) { s_hidden[decltype(q)::value][row * C::PITCH + j] = (uint16_t)next_term<decltype(q)::value == TERMS - 1>(v); });
       }
@@ -166,6 +165,8 @@ __global__ __launch_bounds__(64 * SmallCfg<RF>::SW) void lora_small_kernel(LoraA
 #pragma unroll
           for (int k = 0; k < TERMS; ++k) acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[q][f], hf[k], acc[f], 0, 0, 0);
       }
+#pragma unroll
+      for (int f = 0; f < C::NF; ++f) acc[f] *= scale;
     }
 #pragma unroll
     for (int f = 0; f < C::NF; ++f)
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int spl
 #pragma unroll
         for (int i = 0; i < ER / 16; ++i) {
           const int row = 16 * i + tid / 16;
-          f32x4 h = v[i] * scale;
+          f32x4 h = v[i];
           uint8_t* to = smem + row * 128 + ((tid % 16 / 2 ^ Loader<DIRECT, ER, 4>::key(row)) << 4) + (tid & 1) * 8;
           unrolled<0, TERMS>([&](auto k) {
             constexpr bool LAST = decltype(k)::value == TERMS - 1;
@@ -338,6 +339,7 @@ __global__ __launch_bounds__(256, 3) void lora_expand_kernel(LoraArgs a, int spl
     each_piece<ER / 16, false>(acc, lane, [&](int i, int, int, f32x4 v) {
       Piece o = base[i];
       if (c.slot >= 0) {
+        v *= scale;
         if constexpr (BF16)
           o = pack_sum(o, v);
         else

@@ -833,3 +833,23 @@ def test_adapters_with_hidden_values_past_the_largest_bf16(T, r, N, K, dtype):
     out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)]).cpu().double()
     want, bound = ref.adapters(base, x, a, b, off, gather, None, None)
     assert want.min() > 1e35 and ((out - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("T, r, N, K", SPECIAL)
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adapters_of_infinite_scales(T, r, N, K, dtype):
+    """An infinite scale gives infinities of the outer sum's sign (a NaN where that is 0)."""
+    off, gather, base, x, a, b = special_case(T, r, N, K, dtype)
+    scale = torch.tensor([float("inf"), 0.75, -float("inf")])
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)], scale=scale.cuda()).cpu()
+    of = adapter_of_rows(off, gather, T)
+    total, slack = ref.adapters(torch.zeros(base.shape), x, a, b, off, gather, None, None)
+    sure = (total.abs() > slack) | (torch.arange(T) == 6)[:, None]  # its sign in fp32 is that of fp64
+    for e in (0, 2):
+        mine = sure & (of == e)[:, None]
+        assert mine.sum() > (of == e).sum() * N // 2
+        want, got = (total * scale[e].double())[mine].to(dtype), out[mine]
+        assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[~torch.isnan(got)], want[~torch.isnan(want)])
+    rows = of == 1
+    want, bound = ref.adapters(base, x, a, b, off, gather, None, scale)
+    assert ((out.double() - want).abs() <= bound)[rows].all()
