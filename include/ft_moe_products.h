@@ -88,15 +88,15 @@ int ft_moe_swiglu_grad(const uint16_t* gu, const uint16_t* dh, int rows, int I, 
  * [n_slots] (NULL: 1), base and out fp32 [T][N], or bf16 with FT_OUT_BF16; out may be base itself.
  * The rows of adapter i of E are gather[offsets[i]] .. gather[offsets[i+1]-1], as ft_moe_permute gives them for the
  * rows' adapters (k = 1); rows without an adapter are given number E there (and E + 1 experts), or an adapter
- * without a slot in [0, n_slots).  slot_of_adapter NULL: adapter i is in slot i (E <= n_slots).  Positions from
- * offsets[E] on count as rows without an adapter; entries of gather outside [0, T) are skipped; a row that gather
+ * without a slot in [0, n_slots).  slot_of_adapter NULL: adapter i is in slot i (E <= n_slots).  Positions before
+ * offsets[0] and from offsets[E] on count as rows without an adapter; entries of gather outside [0, T) are skipped; a row that gather
  * does not name is left as it was, one that it names twice is formed twice (with out == base: added twice or once),
  * and rows that a table which does not ascend gives to several adapters get values of no use.
  * r % 8 == 0, r <= 256 (adapters of smaller rank: zeros behind), N % 8 == 0, K % 8 == 0, both at most 2^20, T < 2^24;
  * sizes whose tiles an int cannot count, whatever offsets holds, are refused with FT_E_UNSUPPORTED.
  * The inner sums are held in fp32 and enter the outer ones as bf16 terms: two for bf16 results, within 2^-16 of themselves,
- * three for fp32 ones, all of them.  The terms have the sum's sign and none is 0 beside a sum that is not: infinities and NaN of x, a
- * and b give what the formula gives.
+ * three for fp32 ones, all of them.  The terms have the sum's sign and none is 0 beside a sum that is not: infinities and NaN of x, a, b
+ * and scale give what the formula gives.
  * ws: ft_moe_lora_workspace(T, E, r, N, K) bytes of device memory (0 for few rows: then ws may be NULL).
  */
 size_t ft_moe_lora_workspace(int T, int E, int r, int N, int K);

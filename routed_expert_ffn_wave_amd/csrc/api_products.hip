@@ -155,9 +155,9 @@ int ft_moe_lora(const void* base, const uint16_t* x, int T, const uint16_t* a, c
     if (rc) return rc;
     REQUIRE(r > 0 && r % 8 == 0 && r <= 256, FT_E_INVAL, "r must be a positive multiple of 8, at most 256 (got %d)", r);
     REQUIRE(n_slots >= 1, FT_E_INVAL, "n_slots must be >= 1 (got %d)", n_slots);
-    // items in an int whatever the table holds (one that does not ascend can give all rows to every second adapter): at most 16 rows
-    // by 256 columns each, or 64 hidden rows by 64 of at most 256 columns in up to 16 shares of K
-    REQUIRE(T < (1 << 24) && (T / 16 + 8LL) * (E / 2 + 1) * ((N + 255) / 256 > 16 ? (N + 255) / 256 : 16) < (1LL << 31) - (1 << 16),
+    // items in an int whatever the table holds (from 0 over E + 1 offsets to T, one that does not ascend can give all rows to every
+    // second of E + 2 groups): at most 16 rows by 256 columns each, or 64 hidden rows by 64 of at most 256 columns in up to 16 shares of K
+    REQUIRE(T < (1 << 24) && (T / 16 + 8LL) * ((E + 3) / 2) * ((N + 255) / 256 > 16 ? (N + 255) / 256 : 16) < (1LL << 31) - (1 << 16),
             FT_E_UNSUPPORTED, "T too large (%d rows, N=%d, E=%d)", T, N, E);
     if (T == 0) return ok();
     if ((rc = check_slots(n_slots, slot_of_adapter, "slot_of_adapter", E))) return rc;

@@ -20,26 +20,26 @@
 namespace ftk {
 namespace {
 
-// Chunks of up to ROWS rows of one adapter; with `copy` also those of rows without one (slot -1).
+// Chunks of up to ROWS rows of one adapter; with `copy` also those of rows without one (slot -1): positions of adapters without a slot, from
+// offsets[E] on (entry E) and before offsets[0] (entry E + 1).
 template <int ROWS>
 __device__ __forceinline__ int list_chunks(const RowGroups& s, bool copy, GroupList& g, int* lds) {
-  const int E2 = s.E + 3;
+  const int E2 = s.E + 4;
   g = GroupList{lds, lds + E2, lds + 2 * E2, lds + 3 * E2, 0};
   build_group_list(
-      s.E + 1, g, lds + 4 * E2,
+      s.E + 2, g, lds + 4 * E2,
       [&](int e, int& slot, int& row0, int& cnt) {
-        if (e <= s.E) {
-          row0 = min(max(s.offsets[e], 0), s.P);
-          cnt = (e < s.E ? min(max(s.offsets[e + 1], 0), s.P) : s.P) - row0;
-          slot = e == s.E ? -1 : s.slot_of ? s.slot_of[e] : e;
-          if ((uint32_t)slot >= s.n_slots) slot = -1;
-        }
-        return cnt > 0 && (copy || slot >= 0);
+        const int first = s.offsets[min(e, s.E)], next = s.offsets[e < s.E ? e + 1 : 0];  // loads that wait for no branch
+        slot = s.slot_of ? s.slot_of[min(e, s.E - 1)] : e;
+        if (e >= s.E || (uint32_t)slot >= s.n_slots) slot = -1;
+        row0 = e <= s.E ? min(max(first, 0), s.P) : 0;
+        cnt = (e == s.E ? s.P : min(max(next, 0), s.P)) - row0;
+        return e <= s.E + 1 && cnt > 0 && (copy || slot >= 0);
       },
       [](int cnt) { return (cnt + ROWS - 1) / ROWS; });
   return g.item0[g.n];
 }
-constexpr size_t list_lds(int E) { return group_lds_bytes(E + 1); }
+constexpr size_t list_lds(int E) { return group_lds_bytes(E + 2); }
 
 // An item's rows: positions p0 .. p0 + rows - 1 of gather.
 struct Chunk {
@@ -360,7 +360,7 @@ hipError_t launch_small(const LoraArgs& a, hipStream_t s) {
   const size_t lds = SmallCfg<RF>::Tile::LDS + list_lds(a.g.E);
   hipError_t e = cache.get((const void*)lora_small_kernel<RF, BF16>, SmallCfg<RF>::Tile::NT, lds, &f);
   if (e != hipSuccess) return e;
-  const long long items = (chunks(a.g.P, a.g.E + 1, 16) * ((a.N + 255) / 256) + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
+  const long long items = (chunks(a.g.P, a.g.E + 2, 16) * ((a.N + 255) / 256) + 7) / 8 * 8, most = (long long)f.per_cu * f.cus / 8 * 8;
   hipLaunchKernelGGL((lora_small_kernel<RF, BF16>), dim3((uint32_t)(items < most ? items : most)), dim3(SmallCfg<RF>::Tile::NT), lds, s, a, a.base != a.out);
   return hipGetLastError();
 }
@@ -384,7 +384,7 @@ hipError_t launch_expand(const LoraArgs& a, int splits, hipStream_t s) {
   const size_t lds = kExpandLds<BF16> + list_lds(a.g.E);
   hipError_t e = cache.get((const void*)lora_expand_kernel<BF16>, 256, lds, &f);
   if (e != hipSuccess) return e;
-  const long long items = chunks(a.g.P, a.g.E + 1, ER) * ((a.N + 255) / 256), most = (long long)f.per_cu * f.cus;
+  const long long items = chunks(a.g.P, a.g.E + 2, ER) * ((a.N + 255) / 256), most = (long long)f.per_cu * f.cus;
   hipLaunchKernelGGL(lora_expand_kernel<BF16>, dim3((uint32_t)(items < most ? items : most)), dim3(256), lds, s, a, splits, a.base != a.out);
   return hipGetLastError();
 }

@@ -143,8 +143,8 @@ def ft_moe_lora_workspace(T: int, E: int, r: int, N: int, K: int) -> int:
 def ft_moe_lora(base, x, a, b, offsets, gather, slot_of_adapter=None, scale=None, out=None, ws=None, stream=None):
     """base [T][N] (bf16 or fp32) plus every row's adapter: scale (x a^T) b^T with x bf16 [T][K], a bf16 [n_slots][r][K],
     b bf16 [n_slots][N][r] and scale fp32 [n_slots] (None: 1).  offsets [E + 1] and gather [T] list the rows of the E
-    adapters (ft_moe_permute of the rows' adapters, k = 1); rows without an adapter stand behind them or with one that
-    has no slot, and get base.  out may be base itself.  `ws`: ft_moe_lora_workspace(T, E, r, N, K) bytes."""
+    adapters (ft_moe_permute of the rows' adapters, k = 1); rows without an adapter stand before or behind them or with
+    one that has no slot, and get base.  out may be base itself.  `ws`: ft_moe_lora_workspace(T, E, r, N, K) bytes."""
     dev, (T, N) = _first(base, "base", 2, _FLOATS, stream)
     K = x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
     px = _take(x, "x", (_BF,), (T, K), dev)

@@ -853,3 +853,38 @@ def test_adapters_of_infinite_scales(T, r, N, K, dtype):
     rows = of == 1
     want, bound = ref.adapters(base, x, a, b, off, gather, None, scale)
     assert ((out.double() - want).abs() <= bound)[rows].all()
+
+
+@pytest.mark.parametrize("T, r, N, K", [(60, 16, 40, 72), (1, 8, 8, 8), (900, 40, 72, 520), (300, 72, 264, 520), (4000, 16, 2056, 1544)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adapters_of_a_table_that_begins_later(T, r, N, K, dtype):
+    """Positions before offsets[0], as a table cut to some of the adapters has them, are rows without an adapter."""
+    g = gen(T)
+    E = 4
+    off, gather = adapter_rows(g, T, E)
+    base = torch.randn(T, N, generator=g).to(dtype)
+    x, a, b = normal(g, T, K), normal(g, E, r, K, scale=K ** -0.5), normal(g, E, N, r)
+    for first, last in ((2, E), (1, 3), (E - 1, E)):
+        part = off[first:last + 1].contiguous()
+        slot = torch.arange(first, last).int()
+        want, bound = ref.adapters(base, x, a, b, part, gather, slot, None)
+        args = [t.cuda() for t in (base, x, a, b, part, gather)]
+        out = ft.ft_moe_lora(*args, slot_of_adapter=slot.cuda(), out=filled(T, N, dtype=dtype))
+        assert ((out.cpu().double() - want).abs() <= bound).all()
+        bare = (bound == 0).all(1)
+        assert bare[gather[:part[0]].long()].all() and same_bits(out[bare.cuda()], base[bare])
+        assert same_bits(ft.ft_moe_lora(*args, slot_of_adapter=slot.cuda(), out=args[0]), out)
+
+
+@pytest.mark.parametrize("E", [1, 2, 1023, 1024])
+def test_adapters_of_tables_of_every_size_with_rows_around(E):
+    """Rows before and behind the table's, beside as many groups as there can be."""
+    g = gen(E)
+    T, r, N, K = E + 40, 8, 24, 64
+    off = (torch.arange(E + 1) + 20).int()
+    gather = torch.randperm(T, generator=g).int()
+    base = torch.randn(T, N, generator=g)
+    x, a, b = normal(g, T, K), normal(g, E, r, K, scale=K ** -0.5), normal(g, E, N, r)
+    want, bound = ref.adapters(base, x, a, b, off, gather, None, None)
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)], out=filled(T, N, dtype=F32)).cpu()
+    assert ((out.double() - want).abs() <= bound).all()
