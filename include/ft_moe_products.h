@@ -10,8 +10,9 @@
  * Every convention of ft_moe.h holds here: device pointers, 16-byte aligned, dense row-major arrays,
  * caller-owned buffers, enqueue-only on `stream`, FT_OK or a status with ft_moe_last_error(), calls
  * reentrant and capturable into a graph.  No call keeps any state, and no result depends on the order in which
- * blocks run: the same inputs give the same bits.  Workspaces' contents do not matter; calls that may overlap, and graphs
- * that may, need their own.  Outputs must not
+ * blocks run: the same inputs give the same bits.  Only rows that tables name more than once are excepted (several
+ * experts' in offsets that do not ascend, twice in gather): which of their results remains may differ from call to call.
+ * Workspaces' contents do not matter; calls that may overlap, and graphs that may, need their own.  Outputs must not
  * overlap inputs or each other, except where said.  Sizes of 0 rows are no-ops, except where said.
  *
  * Rows of an expert.  offsets int32 [E+1] as from ft_moe_permute: expert e has rows offsets[e] .. offsets[e+1]-1
