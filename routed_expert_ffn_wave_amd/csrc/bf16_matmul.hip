@@ -198,9 +198,9 @@ __device__ __forceinline__ void join_waves(const f32x4 (&acc)[C::MF][C::NF], voi
 
 // Few rows an expert: BM rows by 64 columns a block, whose four waves have a share of the reduction each, with stages of
 // their own and no barriers; their sums meet in LDS in a fixed order.
-template <int BM, bool GRAD, bool BF16, int NS>
+template <int BM, bool GRAD, bool BF16>
 __device__ __forceinline__ void few_tile(const GroupedArgs& a, int slot, int row0, int rows, int n0, uint8_t* lds) {
-  using C = Bf16Cfg<BM, 64, 1, 1, NS, 4>;
+  using C = Bf16Cfg<BM, 64, 1, 1, 2, 4>;
   const int cols = GRAD ? a.K : a.N, red = GRAD ? a.N : a.K, stages = (red + 63) / 64;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int k0 = stages * wv / 4 * 64, k1 = min(stages * (wv + 1) / 4 * 64, red);
@@ -233,11 +233,11 @@ __global__ __launch_bounds__(256) void grouped_few_kernel(GroupedArgs a) {
     const int row0 = __builtin_amdgcn_readfirstlane(gl.row0[gi]), cnt = __builtin_amdgcn_readfirstlane(gl.cnt[gi]);
     const int m0 = local / ntn * ROWS, n0 = local % ntn * 64, rows = min(ROWS, cnt - m0);
     if (ROWS > 16 && rows > 32)
-      few_tile<64, GRAD, BF16, 2>(a, slot, row0 + m0, rows, n0, lds);
+      few_tile<64, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
     else if (ROWS > 16 && rows > 16)
-      few_tile<32, GRAD, BF16, 2>(a, slot, row0 + m0, rows, n0, lds);
+      few_tile<32, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
     else
-      few_tile<16, GRAD, BF16, 2>(a, slot, row0 + m0, rows, n0, lds);
+      few_tile<16, GRAD, BF16>(a, slot, row0 + m0, rows, n0, lds);
   }
 }
 
