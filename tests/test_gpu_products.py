@@ -888,3 +888,54 @@ def test_adapters_of_tables_of_every_size_with_rows_around(E):
     want, bound = ref.adapters(base, x, a, b, off, gather, None, None)
     out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)], out=filled(T, N, dtype=F32)).cpu()
     assert ((out.double() - want).abs() <= bound).all()
+
+
+WIDE = 1 << 20  # the most columns
+
+
+@pytest.mark.parametrize("N, K", [(WIDE, 8), (8, WIDE)])
+def test_products_of_the_most_columns(N, K):
+    g = gen(N)
+    off = torch.tensor([0, 2, 5]).int()
+    a, w, d = normal(g, 5, K), normal(g, 2, N, K), normal(g, 5, N)
+    for dtype in (BF, F32):
+        check_forward(a, w, off, None, dtype, False)
+        check_forward(d, w, off, None, dtype, True)
+        has, want, mag, most = ref.matrix_gradient(d, a, off, None, 2)
+        got = ft.ft_moe_grouped_matmul_wgrad(d.cuda(), a.cuda(), off.cuda(), out_dtype=dtype)
+        assert ((got.cpu().double() - want).abs() <= ref.sum_bound(want, mag, most, dtype)).all()
+
+
+@pytest.mark.parametrize("T, r", [(3, 16), (3, 256), (40, 8)])
+@pytest.mark.parametrize("N, K", [(WIDE, 8), (8, WIDE)])
+def test_adapters_of_the_most_columns(T, r, N, K):
+    g = gen(N + r)
+    off, gather = adapter_rows(g, T, 2)
+    base, x = torch.randn(T, N, generator=g), normal(g, T, K)
+    a, b = normal(g, 2, r, K, scale=K ** -0.5), normal(g, 2, N, r)
+    want, bound = ref.adapters(base, x, a, b, off, gather, None, None)
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)])
+    assert ((out.cpu().double() - want).abs() <= bound).all()
+
+
+def test_swiglu_of_the_most_columns():
+    g = gen(1)
+    gu, dh = normal(g, 2, 2 * WIDE), normal(g, 2, WIDE)
+    for got, (want, off) in ((ft.ft_moe_swiglu(gu.cuda()), ref.swiglu(gu)), (ft.ft_moe_swiglu_grad(gu.cuda(), dh.cuda()), ref.swiglu_gradient(gu, dh))):
+        assert ((got.cpu().double() - want).abs() <= off * (1 + ref.UBF) + ref.UBF * want.abs() + ref.TINY).all()
+
+
+def test_adapters_that_name_rows_twice():
+    """A row that gather names twice, in one group or in two, of one adapter, is formed twice with the same result."""
+    g = gen(21)
+    T, r, N, K = 80, 16, 72, 136
+    gather = torch.arange(T).int()
+    gather[10], gather[47], gather[79] = 3, 5, 5  # rows 3 and 5 again; 10, 47 and 79 are not named
+    off, slot = torch.tensor([0, 40, T]).int(), torch.zeros(2).int()
+    base, x = torch.randn(T, N, generator=g), normal(g, T, K)
+    a, b = normal(g, 1, r, K, scale=0.1), normal(g, 1, N, r)
+    out = ft.ft_moe_lora(*[t.cuda() for t in (base, x, a, b, off, gather)], slot_of_adapter=slot.cuda(), out=filled(T, N, dtype=F32)).cpu()
+    want, bound = ref.adapters(base, x, a, b, torch.tensor([0, T]), torch.arange(T).int(), None, None)
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[[10, 47, 79]] = False
+    assert (out[~rest] == FILL).all() and ((out.double() - want).abs() <= bound)[rest].all()
