@@ -367,16 +367,25 @@ hipError_t launch_wgrad_few(const WgradArgs& a, hipStream_t s) {
 // DIRECT their pieces would be 64 bytes: 8 % more (16384 rows, 7168 -> 4096: 707 -> 764 us).
 using T256 = Bf16Cfg<256, 256, 2, 4, 4, 1, 32>;
 
-// Which kernel, by times modelled for the rounds that the 256 compute units take, in us (a tile's start and end, and its
-// stages of 64): 256-column tiles, or blocks of 64 columns whose waves share the reduction.  How the rows lie is known on
-// the device only: as if experts were drawn evenly.  Measured, us, 256-column tiles / 64-column blocks, bf16 results:
+// Which kernel: 256-column tiles, or blocks of 64 columns whose waves share the reduction.  How the rows lie is known on the device
+// only: as if experts were drawn evenly.  Two rules.  By times modelled for the rounds that the 256 compute units take, in us (a
+// tile's start and end, and its stages of 64): what bounds products of many rows or few tiles.  The bytes are not in that model, and
+// with few rows an expert they are the time: there it takes tiles for faster than they are.  So forward products of up to 16 rows an
+// expert take the blocks whatever it says, by the times below.  Measured, us, 256-column tiles / 64-column blocks, bf16 results:
 //   forward, 128 experts of 1536 x 2048, top 8 of   1 token  18.9 / 11.8    4  34.4 / 29.9    8  70.7 / 60.6    64  143.6 / 137.7
 //                                                  256  148.8 / 147.3    512  154.1 / 160.8    4096 (Zipf)  274 / 533
 //   rows' gradient, the same                         1  17.3 / 11.9    4  32.5 / 33.2    16  99.3 / 110.5    256  147.4 / 178.8
 //   one matrix of 4096 x 4096, rows                 64  31.2 / 16.0    300  73.8 / 29.8
 // With few rows the forward product is bound by the matrices' bytes, which the smaller blocks read at 5.7 - 6.1 TB/s, the larger
 // ones at 5.3 - 5.6; in the rows' gradient, whose 64 columns are 128 bytes of a memory row, it is the other way round.
-// Tiles of 128 columns where 256 leave units without one, or a round nearly empty.  us, 256 (or 64) / 128: 256 tokens, top 2 of 8 experts of
+// Forward with up to 16 rows an expert elsewhere, 256-column tiles / 64-column blocks (/ 128-column tiles):
+//   64 experts of 2048 x 1024, top 4 of   1 token  11.7 / 6.8    8  24.9 / 26.5    32  46.7 / 47.9    128  50.8 / 56.2
+//   8 of 4096 x 8192, top 2               1        56.4 / 24.6   4  94.8 / 93.3 / 81.2    16  104.0 / 123.3 / 101.8
+//   16 of 2048 x 2048, top 4              1        23.6 / 10.5   4  28.3 / 23.8    16  30.4 / 28.0
+//   256 of 4096 x 7168, top 8             1        98.2 / 80.8  16  1002 / 975    128  2379 / 2375
+// so that from some 4 rows an expert on the tiles win by up to a fifth where rows are long or experts few.
+// Tiles of 128 columns where 256 leave units without one, or a round nearly empty (a tile's time as a share of a
+// 256-column one's, 0.58 forward and 0.68 back, is fitted to these times, not derived).  us, 256 (or 64) / 128: 256 tokens, top 2 of 8 experts of
 // 4096 x 4096 73 / 50, back 86 / 53; 300, top 4 of 16 of 2048 x 2048 32 / 25, back 33 / 27; 333, top 8 of 64, 40 here, of 2048 x 1032 56 / 49; but 128 experts
 // with 128 rows each 161 / 168, 512 tokens, top 2 of 8, 81 / 89; back 77 tokens, top 4 of 32 of 2048 x 768 19.8 / 21.0, 64, top 2 of 8, 54.6 / 51.1.
 // The list is put in order of heights where there are more than two rounds and heights to differ: it takes 1 - 2 us.
@@ -416,6 +425,10 @@ hipError_t launch_grouped_as(const GroupedArgs& a, hipStream_t s) {
 // compute units (rows as if drawn evenly).  Measured, us, tiles / blocks, fp32 results: 8 experts of 512 x 512 with 1024 rows 28.3 /
 // 20.5, with 128 rows 12.0 / 9.7; 4 experts of 256 x 256 with 4096 rows 77 / 17; 8 experts of 1024 x 1024 with 1024 rows 32.8 / 54.2;
 // 16 experts of 1024 x 512 with 512 rows 21.9 / 43.6.
+// A tile reduces all rows of its expert, so that few tiles take as long as the popular expert's: 32768 rows of 16 experts of 512 x 512 45 us
+// with even experts, 212 where one has 12000; of 64 of 512 x 1024 63 and 101 (one 4000); 8192 rows of 8 of 1536 x 2048 65 and 70.
+// Adding to fp32 gradients (ADD) waits for the old values of a piece before the next piece's are asked for: 4096 tokens, Zipf, 128 experts of
+// 1536 x 2048 820 us where writing takes 399, 8 experts of 4096 x 7168 with 2048 rows each 1051 and 828.
 bool wgrad_few(const WgradArgs& a) {
   const double stages = std::ceil((double)a.g.P / a.g.E / 64), blocks = (double)((a.N + 63) / 64) * ((a.K + 63) / 64) * a.g.E;
   return blocks < 1 << 24 && std::ceil(blocks / 256) * (5 + stages / 4 * 1.1) < std::ceil(wgrad_tiles(a.N, a.K, a.g.E) / 256.0) * (4 + stages * 1.4);

@@ -4,8 +4,8 @@
 // the block with the largest sum.  A first kernel of one block lists the experts by classes of falling rows in a
 // workspace; blocks of the second take tiles from one queue per XCD, each with a contiguous eighth of every class (tiles
 // that run together share rows through its L2), and from the other XCDs' queues when theirs is empty.  Who computes a tile
-// does not change it.  4096 tokens, Zipf, top 8 of 128 experts of 1536 x 2048, fp32: 454 us where the experts' order took 539 (the
-// same with even experts: 498 and 493); with what the tiles gained since, 395 - 400 (416 - 430).
+// does not change it.  4096 tokens, Zipf, top 8 of 128 experts of 1536 x 2048, fp32: 393 us where the experts' order takes 432 (the
+// same with even experts: 421 and 428).
 #pragma once
 #include "ft_device.h"
 #include "ft_products.h"

@@ -4,11 +4,11 @@
 // left, and for fp32 results what that one's left), which carry 16 bits of it, or all 24, and not 8.
 //
 // lora_small_kernel: few rows.  A block has 16 rows of one adapter and 256 columns and forms their hidden rows by itself, its
-// waves sharing K; one launch, no workspace.  Bound by its chain of dependent loads (16 rows of 16 adapters 5.9 us, of which 3.6 are the
+// waves sharing K; one launch, no workspace.  Bound by its chain of dependent loads (16 rows of 16 adapters 5.6 us in a graph, of which 3.6 are the
 // launch) and, with more blocks, by the reads of x and A that the blocks of an adapter repeat from L2.
 // lora_shrink_kernel, lora_expand_kernel: many rows.  The first forms hidden rows in tiles of 64 rows by splits of K, so that
 // every compute unit has loads in flight; the second adds the splits up in their order and multiplies with B.  4096 rows of 5
-// adapters, r = 64, 7168 -> 4096: 17.3 + 27.4 us.  The first streams x at 3.4 TB/s: latency, one or two blocks a unit (other splits, 128
+// adapters, r = 64, 7168 -> 4096: 17.0 + 27.4 us, 16.9 + 49.7 in fp32.  The first streams x at 3.4 TB/s: latency, one or two blocks a unit (other splits, 128
 // rows a block, another place in K to begin with: within 3 %); the second at 2.5 TB/s: its blocks' loads, sums and stores in turn.
 #include <algorithm>
 
@@ -391,9 +391,10 @@ hipError_t launch_expand(const LoraArgs& a, int splits, hipStream_t s) {
 
 // One kernel or two, by times modelled in us.  In the one every 256 columns' block reads its rows of x and A itself, which is what it
 // takes past 4.5 us: blocks of an adapter run on one XCD, and share the 256 compute units' loads where there are more blocks than
-// units, and in turn where one unit holds no more (two, with r > 16 one).  Measured, us, one kernel / two: 16 rows of 16 adapters, r = 16, 2048 -> 4096: 5.9 / 10.9; 32 rows of 32: 7.4 / 11.9; 256 rows of
-// 16: 8.4 / 11.5; 512 rows: 11.3 / 13.2; 1024 rows: 17.8 / 15.5; 131 rows of 40, r = 8, 7168 -> 2048: 12.7 / 14.3; 64 rows of 64, r = 16, 4096 -> 4096:
-// 12.5 / 14.7; 512 rows of 16: 15.5 / 13.8; 3000 rows of 7, 776 -> 520, r = 16: 8.8 / 13.5, r = 64: 18.8 / 18.3; 16 rows of 16, r = 64, 2048 -> 4096: 9.0 / 11.2, 7168 -> 4096: 14.7 / 14.4.
+// units, and in turn where one unit holds no more (two, with r > 16 one).  Measured, us in a graph with other calls' inputs in between,
+// one kernel / two: 16 rows of 16 adapters, r = 16, 2048 -> 4096: 5.6 / 10.7; 32 rows of 32: 7.7 / 12.0; 256 rows of 16: 8.9 / 12.3; 512 rows: 12.3 / 13.6;
+// 1024 rows: 17.6 / 15.7; 131 rows of 40, r = 8, 7168 -> 2048, fp32: 12.3 / 15.9; 64 rows of 64, r = 16, 4096 -> 4096: 14.1 / 15.3; 512 rows of 16: 15.9 / 14.3;
+// 3000 rows of 7, 776 -> 520, r = 16: 9.6 / 14.2, r = 64: 20.7 / 16.7; 16 rows of 16, r = 64, 2048 -> 4096: 10.0 / 12.9, 7168 -> 4096: 17.0 / 14.5.
 bool lora_small(int T, int E, int r, int N, int K) {
   const double ntn = (N + 255) / 256, blocks = chunks(T, E + 1, 16) * ntn, rows = std::min(16.0, std::max(1.0, (double)T / E));
   const double one = 4.5 + std::max(0.6, blocks / 256) * 38e-6 * (std::max(16, r) + rows) * K + std::max(0.0, r <= 16 ? blocks / 512 - 1 : 5 * (blocks / 256 - 1)) * 0.8;

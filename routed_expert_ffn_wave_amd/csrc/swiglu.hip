@@ -2,7 +2,8 @@
 //   dg = dh u s (1 + g (1 - s)),  du = dh g s.
 // fp32 in between, one rounding at the end.
 // A thread has 8 columns of a row: 16-byte loads and stores, no LDS, all of the GPU's waves in flight.  Bound by memory: 32768 rows of 768
-// columns 21.7 us forward (151 MB, 7.0 TB/s, part of it from the last-level cache), 36.2 us back (252 MB).
+// columns 24.0 us forward (151 MB, 6.3 TB/s), 43.4 us back (252 MB, 5.8 TB/s) with other calls' rows in between; 21.7 and 36.2 on the same
+// rows again, part of which the last-level cache still has.  Non-temporal stores as in store_rows (27.5 / 26.0, back 46.5 / 43.8).
 #include "ft_device.h"
 #include "ft_products.h"
 
